@@ -1,5 +1,5 @@
-"""ctypes binding of libsparse_ffn.so: the C-ABI entry points of include/sparse_ffn.h under
-the same names. Arguments are plain integers (device addresses, sizes, a stream handle);
+"""ctypes binding of libsparse_ffn.so: the C-ABI entry points of include/sparse_ffn.h
+and include/sparse_ffn_experts.h under the same names. Arguments are plain integers (device addresses, sizes, a stream handle);
 this module only marshals them and turns a non-zero status into SparseFFNError. There is no
 fallback: if the HIP library is not built, importing this module raises."""
 from __future__ import annotations
@@ -18,7 +18,9 @@ LIB_PATH = os.path.join(_HERE, "libsparse_ffn.so")
 
 SFFN_OK, SFFN_ERR_INVALID, SFFN_ERR_UNSUPPORTED, SFFN_ERR_HIP, SFFN_ERR_TOO_LARGE = 0, -1, -2, -3, -4
 SFFN_STATIC_SCRATCH_BYTES = 16 << 20
-SFFN_F32, SFFN_F16 = 0, 1
+SFFN_F32, SFFN_F16, SFFN_BF16, SFFN_I8 = 0, 1, 2, 3
+SFFN_SCORE_SOFTMAX, SFFN_SCORE_SIGMOID = 0, 1
+SFFN_MAX_EXPERTS, SFFN_MAX_TOPK, SFFN_I8_MAX_K = 1024, 64, 131071
 SFFN_LAYOUT_SPLIT, SFFN_LAYOUT_BUNDLE = 0, 1
 SFFN_UP_ROWS, SFFN_UP_COLUMNS = 0, 1
 SFFN_PREFILL_FP16_ACT = 1
@@ -39,6 +41,15 @@ class SffnDesc(C.Structure):
     ]
 
 
+class SffnExpertsDesc(C.Structure):
+    _fields_ = [
+        ("experts", C.c_int32), ("d", C.c_int32), ("d_ffn", C.c_int32), ("gated", C.c_int32),
+        ("w_act", C.c_void_p), ("ld_act", C.c_int64), ("act_scale", C.c_void_p),
+        ("b_act", C.c_void_p),
+        ("w_down", C.c_void_p), ("ld_down", C.c_int64), ("down_scale", C.c_void_p),
+    ]
+
+
 class SparseFFNError(RuntimeError):
     def __init__(self, status: int, what: str):
         self.status = status
@@ -51,7 +62,7 @@ def _load():
             f"{LIB_PATH} is not built: the HIP library is required (run "
             "`python -m activation_sparse_decode_rank_amd.build`); there is no fallback path")
     lib = C.CDLL(LIB_PATH)
-    P, I32, I64, SZ = C.c_void_p, C.c_int32, C.c_int64, C.c_size_t
+    P, I32, I64, SZ, F32 = C.c_void_p, C.c_int32, C.c_int64, C.c_size_t, C.c_float
     sig = {
         "sparse_ffn_workspace_bytes": (SZ, [C.POINTER(SffnDesc)]),
         "sparse_ffn_create": (C.c_int, [C.POINTER(SffnDesc), C.POINTER(P)]),
@@ -75,6 +86,16 @@ def _load():
         "sparse_ffn_prefill": (C.c_int, [P, P, I32, P, P, SZ, P]),
         "sparse_ffn_prefill_ex": (C.c_int, [P, P, I32, P, P, SZ, I32, P]),
         "sparse_ffn_up_probe": (C.c_int, [P, I32, I32, I32, P, P, P, P, P, P, SZ, P]),
+        # include/sparse_ffn_experts.h
+        "sparse_ffn_route": (C.c_int, [P, I32, I64, I32, I32, I32, I32, P, I32, I32, I32, I32, F32,
+                                       P, P, P]),
+        "sparse_ffn_quantize_rows": (C.c_int, [P, I32, I64, I32, I32, P, I64, P, P]),
+        "sparse_ffn_i8_matmul_work_bytes": (SZ, [I32, I32, I32, I32]),
+        "sparse_ffn_i8_matmul": (C.c_int, [P, I32, P, I64, I32, I32, P, I64, P, P, I32, P, I32, I64,
+                                           P, SZ, P]),
+        "sparse_ffn_experts_work_bytes": (SZ, [C.POINTER(SffnExpertsDesc), I32, I32]),
+        "sparse_ffn_experts": (C.c_int, [C.POINTER(SffnExpertsDesc), P, I32, I64, I32, P, P, I32, P,
+                                         I32, I64, P, SZ, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -92,6 +113,10 @@ EXPORTED = ("sparse_ffn_workspace_bytes", "sparse_ffn_create", "sparse_ffn_destr
             "sparse_ffn_profile_counts", "sparse_ffn_permutation", "sparse_ffn_pack_rows",
             "sparse_ffn_read_probe", "sparse_ffn_up_probe_work_bytes", "sparse_ffn_up_probe",
             "sparse_ffn_prefill_work_bytes", "sparse_ffn_prefill", "sparse_ffn_prefill_ex")
+# the entry points of include/sparse_ffn_experts.h
+EXPORTED_EXPERTS = ("sparse_ffn_route", "sparse_ffn_quantize_rows",
+                    "sparse_ffn_i8_matmul_work_bytes", "sparse_ffn_i8_matmul",
+                    "sparse_ffn_experts_work_bytes", "sparse_ffn_experts")
 
 
 def lib():
@@ -200,3 +225,34 @@ def sparse_ffn_up_probe(w_up, layout, d, d_ffn, x, idx, count, words, u, work, w
                         stream) -> None:
     _ck(_lib.sparse_ffn_up_probe(w_up, layout, d, d_ffn, x, idx, count, words, u, work,
                                  work_bytes, stream), "sparse_ffn_up_probe")
+
+
+def sparse_ffn_route(logits, dtype, ld, T, E, k, score, bias, groups, top_groups, group_top,
+                     renormalize, scale, idx, weights, stream) -> None:
+    _ck(_lib.sparse_ffn_route(logits, dtype, ld, T, E, k, score, bias, groups, top_groups, group_top,
+                              renormalize, scale, idx, weights, stream), "sparse_ffn_route")
+
+
+def sparse_ffn_quantize_rows(x, dtype, ldx, rows, cols, q, ldq, scale, stream) -> None:
+    _ck(_lib.sparse_ffn_quantize_rows(x, dtype, ldx, rows, cols, q, ldq, scale, stream),
+        "sparse_ffn_quantize_rows")
+
+
+def sparse_ffn_i8_matmul_work_bytes(x_dtype, M, N, K) -> int:
+    return int(_lib.sparse_ffn_i8_matmul_work_bytes(x_dtype, M, N, K))
+
+
+def sparse_ffn_i8_matmul(x, x_dtype, x_scale, ldx, M, K, w, ldw, w_scale, bias, N, y, y_dtype, ldy,
+                         work, work_bytes, stream) -> None:
+    _ck(_lib.sparse_ffn_i8_matmul(x, x_dtype, x_scale, ldx, M, K, w, ldw, w_scale, bias, N, y,
+                                  y_dtype, ldy, work, work_bytes, stream), "sparse_ffn_i8_matmul")
+
+
+def sparse_ffn_experts_work_bytes(desc: SffnExpertsDesc, tokens, k) -> int:
+    return int(_lib.sparse_ffn_experts_work_bytes(C.byref(desc), tokens, k))
+
+
+def sparse_ffn_experts(desc: SffnExpertsDesc, x, x_dtype, ldx, T, idx, weights, k, y, y_dtype, ldy,
+                       work, work_bytes, stream) -> None:
+    _ck(_lib.sparse_ffn_experts(C.byref(desc), x, x_dtype, ldx, T, idx, weights, k, y, y_dtype, ldy,
+                                work, work_bytes, stream), "sparse_ffn_experts")

@@ -1,0 +1,183 @@
+// The routed experts' FFNs on 8-bit weights (gfx950).
+//
+// The slots (token t, s-th choice) that name an expert are sorted by expert; each expert's
+// rows then meet its weights in tiles on the matrix cores (sffn_i8.hip): h = relu(...) as fp32,
+// h into 8 bits, the down product of each slot, and the weighted sum over a token's slots in
+// slot order. Every sum of the products is a whole number, so nothing depends on the order in
+// which the sort leaves an expert's rows.
+#include <algorithm>
+
+#include "sffn_device.h"
+#include "sffn_i8.h"
+
+namespace sffn {
+namespace {
+
+constexpr int DTPB = 1024;
+
+// sorted rows: offs[e] = first row of expert e (offs[E] = rows in all), src[row] = slot, and
+// the tile table (expert, first row), n_tiles
+__global__ __launch_bounds__(DTPB) void k_sort(const int32_t* __restrict__ idx, int R, int E,
+                                               int32_t* __restrict__ offs,
+                                               int32_t* __restrict__ src,
+                                               int32_t* __restrict__ tiles,
+                                               int32_t* __restrict__ n_tiles) {
+  __shared__ int s_cnt[1024], s_at[1024], s_tile[1024];
+  const int tid = threadIdx.x;
+  s_cnt[tid] = 0;
+  __syncthreads();
+  for (int i = tid; i < R; i += DTPB) {
+    const int e = idx[i];
+    if ((unsigned)e < (unsigned)E) atomicAdd(&s_cnt[e], 1);
+  }
+  __syncthreads();
+  if (tid == 0) {
+    int o = 0, t = 0;
+    for (int e = 0; e < E; ++e) {
+      s_at[e] = o;
+      s_tile[e] = t;
+      offs[e] = o;
+      o += s_cnt[e];
+      t += (s_cnt[e] + host::kI8Tile - 1) / host::kI8Tile;
+    }
+    offs[E] = o;
+    *n_tiles = t;
+  }
+  __syncthreads();
+  if (tid < E) {
+    const int n = (s_cnt[tid] + host::kI8Tile - 1) / host::kI8Tile;
+    for (int i = 0; i < n; ++i) {
+      tiles[2 * (s_tile[tid] + i)] = tid;
+      tiles[2 * (s_tile[tid] + i) + 1] = s_at[tid] + i * host::kI8Tile;
+    }
+  }
+  __syncthreads();
+  for (int i = tid; i < R; i += DTPB) {
+    const int e = idx[i];
+    if ((unsigned)e < (unsigned)E) src[atomicAdd(&s_at[e], 1)] = i;
+  }
+}
+
+// y_t = sum over slots s in order of weights[t][s] * part[t k + s], slots without an expert
+// left out
+template <typename T>
+__global__ __launch_bounds__(TPB) void k_combine(const float* __restrict__ part, int64_t ldp,
+                                                 const int32_t* __restrict__ idx,
+                                                 const float* __restrict__ weights, int k, int E,
+                                                 int d, T* __restrict__ y, int64_t ldy) {
+  const int t = blockIdx.x;
+  for (int c = threadIdx.x; c < d; c += TPB) {
+    float v = 0.f;
+    for (int s = 0; s < k; ++s) {
+      const int r = t * k + s;
+      if ((unsigned)idx[r] < (unsigned)E) v += weights[r] * part[(size_t)r * ldp + c];
+    }
+    y[(size_t)t * ldy + c] = (T)v;
+  }
+}
+
+size_t esize(int type) { return type == T_F32 ? 4 : 2; }
+
+}  // namespace
+
+hipError_t run_experts(const ExpertsArgs& a, const void* x, int x_type, int64_t ldx, int T,
+                       const int32_t* idx, const float* weights, int k, void* y, int y_type,
+                       int64_t ldy, void* work, int chunk, hipStream_t s) {
+  for (int t0 = 0; t0 < T; t0 += chunk) {
+    const int Tc = std::min(chunk, T - t0);
+    const int R = Tc * k;
+    const host::ExpertsCarve c = host::experts_carve(a.E, a.d, a.f, (size_t)Tc, (size_t)k);
+    char* p = static_cast<char*>(work);
+    int32_t* offs = reinterpret_cast<int32_t*>(p + c.offs);
+    int32_t* src = reinterpret_cast<int32_t*>(p + c.src);
+    int32_t* tiles = reinterpret_cast<int32_t*>(p + c.tiles);
+    int32_t* count = reinterpret_cast<int32_t*>(p + c.count);
+    const int32_t* ic = idx + (size_t)t0 * k;
+    const float* wc = weights + (size_t)t0 * k;
+
+    k_sort<<<dim3(1), dim3(DTPB), 0, s>>>(ic, R, a.E, offs, src, tiles, count);
+    QuantArgs qx{};
+    qx.x = static_cast<const char*>(x) + (size_t)t0 * ldx * esize(x_type);
+    qx.ldx = ldx;
+    qx.rows = Tc;
+    qx.cols = a.d;
+    qx.kpad = host::i8_kpad(a.d);
+    qx.q = reinterpret_cast<int8_t*>(p + c.xq);
+    qx.ldq = qx.kpad;
+    qx.scale = reinterpret_cast<float*>(p + c.xs);
+    hipError_t e = launch_quantize(qx, x_type, s);
+    if (e != hipSuccess) return e;
+
+    ProductArgs up{};
+    up.x = qx.q;
+    up.ldx = qx.ldq;
+    up.xs = qx.scale;
+    up.rows = R;
+    up.w = a.w_act;
+    up.ldw = a.ld_act;
+    up.ws = a.act_scale;
+    up.bias = a.b_act;
+    up.n = a.f;
+    up.kch = (a.d + 15) / 16;
+    up.out = p + c.h;
+    up.ldo = (int64_t)c.ldh;
+    up.out_type = T_F32;
+    up.offs = offs;
+    up.tiles = tiles;
+    up.n_tiles = count;
+    up.src = src;
+    up.max_tiles = (int)host::experts_max_tiles((size_t)R, (size_t)a.E);
+    up.k = k;
+    up.experts = a.E;
+    up.w_group = (int64_t)a.f * (a.gated ? 2 : 1) * a.ld_act;
+    e = launch_product(up, a.gated ? MODE_ACT_GATED : MODE_ACT, s);
+    if (e != hipSuccess) return e;
+
+    QuantArgs qh{};
+    qh.x = up.out;
+    qh.ldx = up.ldo;
+    qh.rows = R;
+    qh.cols = a.f;
+    qh.kpad = host::i8_kpad(a.f);
+    qh.q = reinterpret_cast<int8_t*>(p + c.hq);
+    qh.ldq = qh.kpad;
+    qh.scale = reinterpret_cast<float*>(p + c.hs);
+    qh.rows_dev = offs + a.E;
+    e = launch_quantize(qh, T_F32, s);
+    if (e != hipSuccess) return e;
+
+    ProductArgs dn = up;
+    dn.x = qh.q;
+    dn.ldx = qh.ldq;
+    dn.xs = qh.scale;
+    dn.w = a.w_down;
+    dn.ldw = a.ld_down;
+    dn.ws = a.down_scale;
+    dn.bias = nullptr;
+    dn.n = a.d;
+    dn.kch = (a.f + 15) / 16;
+    dn.out = p + c.part;
+    dn.ldo = (int64_t)c.ldp;
+    dn.w_group = (int64_t)a.d * a.ld_down;
+    e = launch_product(dn, MODE_DOWN, s);
+    if (e != hipSuccess) return e;
+
+    const float* part = reinterpret_cast<const float*>(p + c.part);
+    char* yc = static_cast<char*>(y) + (size_t)t0 * ldy * esize(y_type);
+    const dim3 grid((unsigned)Tc), block(TPB);
+    if (y_type == T_F32)
+      k_combine<float><<<grid, block, 0, s>>>(part, dn.ldo, ic, wc, k, a.E, a.d,
+                                              reinterpret_cast<float*>(yc), ldy);
+    else if (y_type == T_F16)
+      k_combine<_Float16><<<grid, block, 0, s>>>(part, dn.ldo, ic, wc, k, a.E, a.d,
+                                                 reinterpret_cast<_Float16*>(yc), ldy);
+    else
+      k_combine<__bf16><<<grid, block, 0, s>>>(part, dn.ldo, ic, wc, k, a.E, a.d,
+                                               reinterpret_cast<__bf16*>(yc), ldy);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+}  // namespace sffn

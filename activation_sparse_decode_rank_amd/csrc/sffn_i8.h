@@ -1,0 +1,91 @@
+// Internal interface of the 8-bit products and the expert layer (sffn_i8.hip,
+// sffn_experts.hip, sffn_route.hip) towards the C-ABI host code (sffn_experts_api.hip). The
+// public interface is include/sparse_ffn_experts.h.
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "sffn_i8_host.h"
+
+namespace sffn {
+
+// element types of activations and outputs: the values of the public dtype arguments
+enum : int { T_F32 = 0, T_F16 = 1, T_BF16 = 2, T_I8 = 3 };
+
+// rows [0, rows) (or [0, *rows_dev) when that is given) of x into 8 bits; the bytes from cols
+// to kpad (a multiple of 16, at most ldq) are written as zeros
+struct QuantArgs {
+  const void* x;
+  int64_t ldx;
+  int rows, cols, kpad;
+  int8_t* q;
+  int64_t ldq;
+  float* scale;
+  const int32_t* rows_dev;
+};
+hipError_t launch_quantize(const QuantArgs& a, int dtype, hipStream_t s);
+
+// What a product does with its sums. LINEAR: y = sum * (sx * sw) + bias in out_type.
+// ACT / ACT_GATED: h = relu(...) of an expert, fp32. DOWN: fp32 part rows of an expert.
+enum ProductMode : int { MODE_LINEAR = 0, MODE_ACT = 1, MODE_ACT_GATED = 2, MODE_DOWN = 3 };
+
+// One product of 8-bit rows x (tokens) with 8-bit rows w (channels), or of groups of them
+// (groups: the experts' tables below; group e multiplies its rows with w + e * w_group).
+struct ProductArgs {
+  const int8_t* x;     // rows of kch * 16 bytes that end in zeros up to a multiple of 128
+  int64_t ldx;         // bytes
+  const float* xs;     // scale of each row of x
+  int rows;            // rows of x (groups: sorted rows, an upper bound)
+  const int8_t* w;
+  int64_t ldw;         // bytes
+  const float* ws;
+  const float* bias;   // may be null
+  int n;               // channels (ACT_GATED: neurons, each of two rows of w)
+  int kch;             // 16-byte chunks of a row
+  void* out;
+  int64_t ldo;         // elements
+  int out_type;
+  // groups only
+  const int32_t* offs;    // [experts + 1] first sorted row of each expert
+  const int32_t* tiles;   // [tile] = expert * 2^? pairs, see ExpertTables
+  const int32_t* n_tiles;
+  const int32_t* src;     // [sorted row] slot t * k + s it stands for
+  int max_tiles;
+  int k;                  // slots of a token: row src's token is src / k
+  int experts;
+  int64_t w_group;        // bytes from an expert's w to the next one's
+};
+hipError_t launch_product(const ProductArgs& a, ProductMode mode, hipStream_t s);
+
+// x already in 8 bits, rows copied to zero-padded rows of kpad bytes
+hipError_t launch_pad_rows(const int8_t* x, int64_t ldx, int rows, int cols, int8_t* q, int kpad,
+                           hipStream_t s);
+
+struct RouteArgs {
+  const void* logits;
+  int64_t ld;
+  int T, E, k, score;
+  const float* bias;
+  int groups, top_groups, group_top, renorm;
+  float scale;
+  int32_t* idx;
+  float* weights;
+};
+hipError_t launch_route(const RouteArgs& a, int dtype, hipStream_t s);
+
+struct ExpertsArgs {
+  int E, d, f, gated;
+  const int8_t* w_act;
+  int64_t ld_act;
+  const float* act_scale;
+  const float* b_act;
+  const int8_t* w_down;
+  int64_t ld_down;
+  const float* down_scale;
+};
+hipError_t run_experts(const ExpertsArgs& a, const void* x, int x_type, int64_t ldx, int T,
+                       const int32_t* idx, const float* weights, int k, void* y, int y_type,
+                       int64_t ldy, void* work, int chunk, hipStream_t s);
+
+}  // namespace sffn

@@ -1,0 +1,90 @@
+// Host-side planning of the 8-bit products and the expert layer: pure C++ with no HIP
+// dependency, so that it can be built and checked on its own.
+#pragma once
+#include <algorithm>
+#include <cstddef>
+#include <cstdint>
+
+namespace sffn {
+namespace host {
+
+inline size_t up_to(size_t v, size_t m) { return (v + m - 1) / m * m; }
+
+// 8-bit rows of activations are padded with zeros to whole steps of the products
+constexpr int kI8Step = 128;
+inline int i8_kpad(int K) { return (int)up_to((size_t)K, kI8Step); }
+
+// rows of a product tile (the expert tables cut each expert's rows into tiles of this many)
+constexpr int kI8Tile = 64;
+
+// Scratch of an 8-bit product whose activations have to be held in 8 bits (or padded) first:
+// the rows, then their scales.
+struct I8MatmulCarve {
+  size_t q, scale, bytes;
+};
+inline I8MatmulCarve i8_matmul_carve(size_t M, int K) {
+  I8MatmulCarve c{};
+  c.q = 0;
+  c.scale = up_to(M * (size_t)i8_kpad(K), 256);
+  c.bytes = c.scale + up_to(M * 4, 256);
+  return c;
+}
+
+// most tiles that `rows` sorted rows of E experts can make
+inline size_t experts_max_tiles(size_t rows, size_t E) {
+  return rows / kI8Tile + std::min(rows, E);
+}
+
+// Scratch of the expert layer for a chunk of T tokens of k slots each (R = T k rows).
+struct ExpertsCarve {
+  size_t xq, xs;        // the tokens in 8 bits [T][i8_kpad(d)] and their scales
+  size_t offs, src;     // sorted rows: first of each expert [E + 1], slot of each row [R]
+  size_t tiles, count;  // tile table [max_tiles] of (expert, first row), number of tiles
+  size_t h, hq, hs;     // activations fp32 [R][ldh], 8 bits [R][i8_kpad(f)], scales [R]
+  size_t part;          // down product of each slot fp32 [R][ldp]
+  size_t ldh, ldp;
+  size_t bytes;
+};
+inline ExpertsCarve experts_carve(int E, int d, int f, size_t T, size_t k) {
+  ExpertsCarve c{};
+  const size_t R = T * k;
+  size_t o = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = o;
+    o += up_to(bytes, 256);
+    return at;
+  };
+  c.ldh = up_to((size_t)f, 64);
+  c.ldp = up_to((size_t)d, 64);
+  c.xq = take(T * (size_t)i8_kpad(d));
+  c.xs = take(T * 4);
+  c.offs = take(((size_t)E + 1) * 4);
+  c.src = take(R * 4);
+  c.tiles = take(experts_max_tiles(R, (size_t)E) * 8);
+  c.count = take(4);
+  c.h = take(R * c.ldh * 4);
+  c.hq = take(R * (size_t)i8_kpad(f));
+  c.hs = take(R * 4);
+  c.part = take(R * c.ldp * 4);
+  c.bytes = o;
+  return c;
+}
+
+// most rows one chunk may have: 32-bit row numbers, and grids below 2^31 workgroups
+constexpr size_t kExpertsMaxRows = (size_t)1 << 24;
+
+// tokens per chunk that work_bytes holds (0: not even one), at most T
+inline int experts_chunk(int E, int d, int f, int T, int k, size_t work_bytes) {
+  size_t lo = 0, hi = std::min((size_t)T, std::max<size_t>(1, kExpertsMaxRows / (size_t)k));
+  while (lo < hi) {
+    const size_t mid = (lo + hi + 1) / 2;
+    if (experts_carve(E, d, f, mid, (size_t)k).bytes <= work_bytes)
+      lo = mid;
+    else
+      hi = mid - 1;
+  }
+  return (int)lo;
+}
+
+}  // namespace host
+}  // namespace sffn
