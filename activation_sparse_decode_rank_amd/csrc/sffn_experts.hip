@@ -18,7 +18,7 @@ constexpr int DTPB = 1024;
 // sorted rows: offs[e] = first row of expert e (offs[E] = rows in all), src[row] = slot, and
 // the tile table (expert, first row), n_tiles
 __global__ __launch_bounds__(DTPB) void k_sort(const int32_t* __restrict__ idx, int R, int E,
-                                               int32_t* __restrict__ offs,
+                                               int tile, int32_t* __restrict__ offs,
                                                int32_t* __restrict__ src,
                                                int32_t* __restrict__ tiles,
                                                int32_t* __restrict__ n_tiles) {
@@ -38,17 +38,17 @@ __global__ __launch_bounds__(DTPB) void k_sort(const int32_t* __restrict__ idx, 
       s_tile[e] = t;
       offs[e] = o;
       o += s_cnt[e];
-      t += (s_cnt[e] + host::kI8Tile - 1) / host::kI8Tile;
+      t += (s_cnt[e] + tile - 1) / tile;
     }
     offs[E] = o;
     *n_tiles = t;
   }
   __syncthreads();
   if (tid < E) {
-    const int n = (s_cnt[tid] + host::kI8Tile - 1) / host::kI8Tile;
+    const int n = (s_cnt[tid] + tile - 1) / tile;
     for (int i = 0; i < n; ++i) {
       tiles[2 * (s_tile[tid] + i)] = tid;
-      tiles[2 * (s_tile[tid] + i) + 1] = s_at[tid] + i * host::kI8Tile;
+      tiles[2 * (s_tile[tid] + i) + 1] = s_at[tid] + i * tile;
     }
   }
   __syncthreads();
@@ -95,7 +95,7 @@ hipError_t run_experts(const ExpertsArgs& a, const void* x, int x_type, int64_t 
     const int32_t* ic = idx + (size_t)t0 * k;
     const float* wc = weights + (size_t)t0 * k;
 
-    k_sort<<<dim3(1), dim3(DTPB), 0, s>>>(ic, R, a.E, offs, src, tiles, count);
+    k_sort<<<dim3(1), dim3(DTPB), 0, s>>>(ic, R, a.E, c.tile, offs, src, tiles, count);
     QuantArgs qx{};
     qx.x = static_cast<const char*>(x) + (size_t)t0 * ldx * esize(x_type);
     qx.ldx = ldx;
@@ -126,7 +126,8 @@ hipError_t run_experts(const ExpertsArgs& a, const void* x, int x_type, int64_t 
     up.tiles = tiles;
     up.n_tiles = count;
     up.src = src;
-    up.max_tiles = (int)host::experts_max_tiles((size_t)R, (size_t)a.E);
+    up.max_tiles = c.max_tiles;
+    up.tile = c.tile;
     up.k = k;
     up.experts = a.E;
     up.w_group = (int64_t)a.f * (a.gated ? 2 : 1) * a.ld_act;

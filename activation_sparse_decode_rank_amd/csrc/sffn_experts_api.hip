@@ -101,7 +101,7 @@ int sparse_ffn_i8_matmul(const void* x, int32_t x_dtype, const float* x_scale, i
   if ((!float_type(x_dtype) && !i8) || !float_type(y_dtype)) return SFFN_ERR_INVALID;
   if (M < 0 || N < 1 || K < 1 || ldx < K || ldy < N) return SFFN_ERR_INVALID;
   if (K > SFFN_I8_MAX_K) return SFFN_ERR_UNSUPPORTED;
-  if ((((int64_t)M + 63) / 64) * (((int64_t)N + 63) / 64) >= (int64_t)1 << 31)
+  if ((((int64_t)M + 63) / 64) * (((int64_t)N + 15) / 16) >= (int64_t)1 << 31)
     return SFFN_ERR_UNSUPPORTED;
   if (M == 0) return SFFN_OK;
   if (!x || (i8 != (x_scale != nullptr)) || !w_scale || !y || !i8_matrix_ok(w, ldw, K))
@@ -145,6 +145,7 @@ int sparse_ffn_i8_matmul(const void* x, int32_t x_dtype, const float* x_scale, i
     a.xs = q.scale;
   }
   a.rows = M;
+  a.tile = sffn::host::i8_tile((size_t)M, 1);
   a.w = w;
   a.ldw = ldw;
   a.ws = w_scale;

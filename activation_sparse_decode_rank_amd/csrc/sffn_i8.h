@@ -31,7 +31,8 @@ hipError_t launch_quantize(const QuantArgs& a, int dtype, hipStream_t s);
 enum ProductMode : int { MODE_LINEAR = 0, MODE_ACT = 1, MODE_ACT_GATED = 2, MODE_DOWN = 3 };
 
 // One product of 8-bit rows x (tokens) with 8-bit rows w (channels), or of groups of them
-// (groups: the experts' tables below; group e multiplies its rows with w + e * w_group).
+// (group e multiplies its rows with
+// w + e * w_group).
 struct ProductArgs {
   const int8_t* x;     // rows of kch * 16 bytes that end in zeros up to a multiple of 128
   int64_t ldx;         // bytes
@@ -46,9 +47,11 @@ struct ProductArgs {
   void* out;
   int64_t ldo;         // elements
   int out_type;
+  int vec_out;         // set by launch_product: out's rows start at multiples of four elements
+  int tile;            // rows of a tile (host::i8_tile)
   // groups only
   const int32_t* offs;    // [experts + 1] first sorted row of each expert
-  const int32_t* tiles;   // [tile] = expert * 2^? pairs, see ExpertTables
+  const int32_t* tiles;   // [tile] (expert, first sorted row)
   const int32_t* n_tiles;
   const int32_t* src;     // [sorted row] slot t * k + s it stands for
   int max_tiles;

@@ -14,8 +14,12 @@ inline size_t up_to(size_t v, size_t m) { return (v + m - 1) / m * m; }
 constexpr int kI8Step = 128;
 inline int i8_kpad(int K) { return (int)up_to((size_t)K, kI8Step); }
 
-// rows of a product tile (the expert tables cut each expert's rows into tiles of this many)
-constexpr int kI8Tile = 64;
+// Rows of a product tile, from the mean rows of a group (of the whole product where there are
+// no groups).
+inline int i8_tile(size_t rows, size_t groups) {
+  const size_t mean = (rows + groups - 1) / groups;
+  return mean <= 16 ? 16 : mean <= 32 ? 32 : 64;
+}
 
 // Scratch of an 8-bit product whose activations have to be held in 8 bits (or padded) first:
 // the rows, then their scales.
@@ -31,8 +35,8 @@ inline I8MatmulCarve i8_matmul_carve(size_t M, int K) {
 }
 
 // most tiles that `rows` sorted rows of E experts can make
-inline size_t experts_max_tiles(size_t rows, size_t E) {
-  return rows / kI8Tile + std::min(rows, E);
+inline size_t experts_max_tiles(size_t rows, size_t E, int tile) {
+  return rows / (size_t)tile + std::min(rows, E);
 }
 
 // Scratch of the expert layer for a chunk of T tokens of k slots each (R = T k rows).
@@ -43,6 +47,7 @@ struct ExpertsCarve {
   size_t h, hq, hs;     // activations fp32 [R][ldh], 8 bits [R][i8_kpad(f)], scales [R]
   size_t part;          // down product of each slot fp32 [R][ldp]
   size_t ldh, ldp;
+  int tile, max_tiles;
   size_t bytes;
 };
 inline ExpertsCarve experts_carve(int E, int d, int f, size_t T, size_t k) {
@@ -54,13 +59,15 @@ inline ExpertsCarve experts_carve(int E, int d, int f, size_t T, size_t k) {
     o += up_to(bytes, 256);
     return at;
   };
+  c.tile = i8_tile(R, std::min(R, (size_t)E));
+  c.max_tiles = (int)experts_max_tiles(R, (size_t)E, c.tile);
   c.ldh = up_to((size_t)f, 64);
   c.ldp = up_to((size_t)d, 64);
   c.xq = take(T * (size_t)i8_kpad(d));
   c.xs = take(T * 4);
   c.offs = take(((size_t)E + 1) * 4);
   c.src = take(R * 4);
-  c.tiles = take(experts_max_tiles(R, (size_t)E) * 8);
+  c.tiles = take(experts_max_tiles(R, (size_t)E, 16) * 8);  // the most any tile makes
   c.count = take(4);
   c.h = take(R * c.ldh * 4);
   c.hq = take(R * (size_t)i8_kpad(f));

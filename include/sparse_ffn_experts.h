@@ -15,9 +15,9 @@
  * Calls can be captured in a HIP graph. Calls that share a `work` buffer must be ordered, and
  * so must the replays of graphs that hold such calls.
  *
- * 8-bit rows. A row r of numbers is held as q and s: s is the 32-bit float max|r| / 127
- * (rounded to nearest) and q_j the whole number nearest to r_j / s, ties to even, decided
- * exactly (|q| <= 127). A row whose largest magnitude is below 2^-100 is held as zeros with
+ * 8-bit rows. A row r of numbers is held as q and s: s is max|r| times the 32-bit float
+ * nearest to 1 / 127, rounded to 32 bits, and q_j the whole number nearest to r_j / s, ties to
+ * even, decided exactly (|q| <= 127). A row whose largest magnitude is below 2^-100 is held as zeros with
  * s = 0; a row with an infinity or a NaN as zeros with s = NaN, so that everything computed
  * from it is NaN.
  *

@@ -43,11 +43,12 @@ def route(l, k, score="softmax", bias=None, groups=1, top_groups=1, group_top=1,
 
 
 def quantize(x):
-    """Rows of numbers -> (q, s): s the 32-bit float max|x| / 127, q the nearest whole numbers."""
+    """Rows of numbers -> (q, s): s = max|x| times the 32-bit float 1 / 127, rounded to
+    32 bits, q the whole numbers nearest to x / s."""
     x = np.asarray(x, np.float64)
     a = np.abs(x).max(axis=1)
     with np.errstate(all="ignore"):
-        s = (a.astype(np.float32) / np.float32(127)).astype(np.float64)
+        s = (a.astype(np.float32) * (np.float32(1) / np.float32(127))).astype(np.float64)
         s[a < 2.0 ** -100] = 0.0
         bad = ~np.isfinite(a)
         s[bad] = np.nan

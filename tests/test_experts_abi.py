@@ -191,7 +191,7 @@ int main() {
     const size_t R = (size_t)T * k;
     const size_t at[] = {c.xq, c.xs, c.offs, c.src, c.tiles, c.count, c.h, c.hq, c.hs, c.part, c.bytes};
     const size_t need[] = {(size_t)T * i8_kpad(d), (size_t)T * 4, ((size_t)E + 1) * 4, R * 4,
-                           experts_max_tiles(R, E) * 8, 4, R * c.ldh * 4, R * (size_t)i8_kpad(f), R * 4,
+                           (size_t)c.max_tiles * 8, 4, R * c.ldh * 4, R * (size_t)i8_kpad(f), R * 4,
                            R * c.ldp * 4};
     for (int i = 0; i < 10; ++i) { CHECK(at[i] % 256 == 0); CHECK(at[i] + need[i] <= at[i + 1]); }
     CHECK(c.ldh >= (size_t)f && c.ldp >= (size_t)d && i8_kpad(d) >= d && i8_kpad(d) % 128 == 0);
@@ -200,8 +200,8 @@ int main() {
     const int used = pick(1, E);
     for (size_t r = 0; r < std::min<size_t>(R, 4000); ++r) n[g() % used]++;
     size_t tiles = 0, rows = 0;
-    for (size_t v : n) { tiles += (v + kI8Tile - 1) / kI8Tile; rows += v; }
-    CHECK(tiles <= experts_max_tiles(rows, E));
+    for (size_t v : n) { tiles += (v + c.tile - 1) / c.tile; rows += v; }
+    if (rows == R) CHECK(tiles <= (size_t)c.max_tiles);
     const size_t some = c.bytes / (size_t)pick(1, 9) + 1;
     const int ch = experts_chunk(E, d, f, T, k, some);
     CHECK(ch <= T && (size_t)ch * k <= kExpertsMaxRows);

@@ -182,7 +182,7 @@ def test_quantize_borders(P):
     n = np.arange(-126, 127) + 0.5
     rows = []
     for amax in (127.0, 127.0 * 2 ** -20, 1.0, 3.3, 1e30, 7e-25):
-        s = float(np.float32(np.float32(amax) / np.float32(127)))
+        s = float(np.float32(amax) * (np.float32(1) / np.float32(127)))
         b = (n * s).astype(np.float32)
         rows.append(np.concatenate([[np.float32(amax)], b, np.nextafter(b, np.float32(np.inf)),
                                     np.nextafter(b, np.float32(-np.inf))]))
