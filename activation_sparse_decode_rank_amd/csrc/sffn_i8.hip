@@ -331,80 +331,155 @@ __global__ __launch_bounds__(SK_W * 64) void k_product_few(ProductArgs a) {
   }
 }
 
-// Tile of 64 rows x 64 channels over the whole length, steps of 128 bytes. Wave w takes the
-// 16 tokens 16 w .. +16 and all 64 channels (four 16 x 16 tiles); the gated form's channels
-// are 32 neurons, gate and up rows of 16 neurons in neighbouring tiles.
-constexpr int LDT = 128 + 16;  // LDS row: 128 bytes and a 16-byte pad against bank conflicts
+// Many rows: a workgroup of 8 waves takes 256 rows of w (channels; gated: 128 neurons, 16 gate
+// rows and their 16 up rows in turn) and TK rows of x over the whole length, in stages of 64
+// bytes. Both operands go from memory straight into LDS (global_load_lds_dwordx4: each lane's
+// 16 bytes land at the next 16 bytes of a 1 KB block), NS stages deep. Within a block, 16 rows
+// of 64 bytes, row r's 16-byte chunk c sits at position (c + r / 4) mod 4 of the row, so that a
+// fragment read (16 rows, one chunk each) touches every LDS bank once. A step waits for the
+// next stage, refills the buffer that was read with the stage NS ahead, and reads the next
+// stage's fragments into registers while the matrix cores take the current ones.
+constexpr int T_CH = 256;   // rows of w per tile
+constexpr int T_K = 64;     // bytes per stage
+constexpr int T_W = 8;      // waves
+// s_waitcnt operand (gfx9 encoding): LDS reads only (lgkmcnt 0, vmcnt and expcnt at most)
+constexpr int I8_WAIT_LGKM0 = 0xC07F;
 
-template <int MODE>
-__global__ __launch_bounds__(TPB) void k_product(ProductArgs a) {
-  constexpr int NT = MODE == MODE_ACT_GATED ? 32 : 64;  // channels (neurons) per tile
-  __shared__ __attribute__((aligned(16))) int8_t s_w[64 * LDT];
-  __shared__ __attribute__((aligned(16))) int8_t s_x[64 * LDT];
+// this lane's 16 bytes at src to place 16 * lane of the 1 KB block at dst (LDS)
+__device__ __forceinline__ void load_block(const int8_t* src, int8_t* dst) {
+  __builtin_amdgcn_global_load_lds(reinterpret_cast<const u32x4*>(src),
+                                   (__attribute__((address_space(3))) void*)dst, 16, 0, 0);
+}
+
+// until at most MOST (FEWER: for waves that load one block less a stage) of this wave's loads
+// are in flight
+template <int MOST, int FEWER>
+__device__ __forceinline__ void wait_loads(bool most) {
+  if (most)
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(MOST) : "memory");
+  else
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(FEWER) : "memory");
+}
+
+template <int MODE, int TK>
+__global__ __launch_bounds__(T_W * 64) void k_product(ProductArgs a) {
+  constexpr bool G = MODE == MODE_ACT_GATED;
+  constexpr int NT = G ? T_CH / 2 : T_CH;          // channels (neurons) per tile
+  constexpr int WT = TK >= 256 ? 4 : TK >= 128 ? 2 : 1;  // waves along the rows of x
+  constexpr int WC = T_W / WT;                     // waves along the channels
+  constexpr int NI = T_CH / 16 / WC, NJ = TK / 16 / WT;  // 16 x 16 tiles of a wave
+  constexpr int BW = T_CH * T_K, BX = TK * T_K, STAGE = BW + BX;
+  constexpr int NS = 4;
+  constexpr int NG = STAGE / 1024;                 // 1 KB loads a stage
+  constexpr int DPS = (NG + T_W - 1) / T_W;        // most of one wave
+  static_assert((NS - 1) * DPS <= 63, "vmcnt range");
+  __shared__ __attribute__((aligned(16))) int8_t sbuf[NS * STAGE];
   const int nnt = (a.n + NT - 1) / NT;
-  const int nt = blockIdx.x % nnt, mt = blockIdx.x / nnt;
+  const int nmt = MODE == MODE_LINEAR ? (a.rows + TK - 1) / TK : *a.n_tiles;
+  // Tiles in runs of 8 row tiles, channels outer: 32 neighbours share 8 row tiles and 4 channel
+  // tiles. Workgroups 8 apart run on one XCD; each XCD takes a run of neighbours.
+  const int total = nmt * nnt, per = (total + 7) / 8;
+  const int id = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
+  if ((int)(blockIdx.x >> 3) >= per || id >= total) return;
+  const int run = id / (8 * nnt), in = id % (8 * nnt);
+  const int rm = min(8, nmt - run * 8);
+  const int mt = run * 8 + in % rm, nt = in / rm;
   int e, r0, r1;
   if (!tile_rows<MODE>(a, mt, e, r0, r1)) return;
-  const int8_t* w = a.w + (size_t)e * a.w_group;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  r1 = min(r1, r0 + TK);
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wc = wave % WC, wt = wave / WC;
   const int r16 = lane & 15, g = lane >> 4;
   const int n0 = nt * NT;
-  const int nw = MODE == MODE_ACT_GATED ? 2 * a.n : a.n;  // rows of w
-  // row of w that row i of the tile stands for
-  auto wrow = [&](int i) {
-    if (MODE == MODE_ACT_GATED) return 2 * (n0 + (i >> 5) * 16 + (i & 15)) + ((i >> 4) & 1);
-    return n0 + i;
+  const int nw = G ? 2 * a.n : a.n;
+  const int8_t* w = a.w + (size_t)e * a.w_group;
+
+  // the lane's row in a 16-row block and the chunk its place holds
+  const int lr = lane >> 2;
+  const int lc = ((lane & 3) - (lr >> 2)) & 3;
+  const int8_t* src[DPS];
+#pragma unroll
+  for (int v = 0; v < DPS; ++v) {
+    const int u = wave + T_W * v;  // block of the stage, wave-uniform
+    if (u < T_CH / 16) {
+      const int row = G ? 2 * (n0 + (u >> 1) * 16 + lr) + (u & 1) : n0 + u * 16 + lr;
+      src[v] = w + (size_t)min(row, nw - 1) * a.ldw;
+    } else {
+      src[v] = a.x + (size_t)row_of_x<MODE>(a, min(r0 + (u - T_CH / 16) * 16 + lr, r1 - 1)) * a.ldx;
+    }
+  }
+  const int nk = (a.kch + 7) / 8 * 2;  // stages: x's rows end in zeros up to 128 bytes
+  auto issue = [&](int st, int buf) {
+    const int kc = st * (T_K / 16) + lc;
+    const int kw = min(kc, a.kch - 1);  // past w's row x is zero: any chunk will do
+#pragma unroll
+    for (int v = 0; v < DPS; ++v) {
+      const int u = wave + T_W * v;
+      if (NG % T_W && u >= NG) break;
+      load_block(src[v] + (size_t)(u < T_CH / 16 ? kw : kc) * 16, sbuf + buf * STAGE + u * 1024);
+    }
   };
-  auto xrow = [&](int i) { return row_of_x<MODE>(a, min(r0 + i, r1 - 1)); };
-  int4_t acc[4];
+  auto frag = [&](const int8_t* base, int block) {
+    return *reinterpret_cast<const int4_t*>(base + block * 1024 +
+                                            (r16 * 4 + ((g + (r16 >> 2)) & 3)) * 16);
+  };
+  int4_t acc[NI][NJ];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) acc[i] = int4_t{0, 0, 0, 0};
-  // each thread stages two 16-byte chunks of each operand
-  const int c8 = tid & 7;
-  const int8_t *pw[2], *px[2];
+  for (int i = 0; i < NI; ++i)
 #pragma unroll
-  for (int u = 0; u < 2; ++u) {
-    const int i = (tid >> 3) + 32 * u;
-    pw[u] = w + (size_t)min(wrow(i), nw - 1) * a.ldw;
-    px[u] = a.x + (size_t)xrow(i) * a.ldx;
+    for (int j = 0; j < NJ; ++j) acc[i][j] = int4_t{0, 0, 0, 0};
+  struct Frags {
+    int4_t w[NI], x[NJ];
+  };
+  auto read_frags = [&](Frags& F, int st) {
+    const int8_t* base = sbuf + (st % NS) * STAGE;
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) F.x[j] = frag(base, T_CH / 16 + wt * NJ + j);
+#pragma unroll
+    for (int i = 0; i < NI; ++i) F.w[i] = frag(base, wc * NI + i);
+  };
+  auto products = [&](const Frags& F) {
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+#pragma unroll
+      for (int j = 0; j < NJ; ++j)
+        acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(F.w[i], F.x[j], acc[i][j], 0, 0, 0);
+  };
+  // Past the last stage the refill loads the last stage again (in bounds, never read), so
+  // every step has the same loads in flight and no branch.
+  const bool most = NG % T_W == 0 || wave < NG % T_W;  // else it loads one block less a stage
+  auto step = [&](int st, Frags& Fc, Frags& Fn) {
+    wait_loads<(NS - 2) * DPS, (NS - 2) * (DPS - 1)>(most);
+    __builtin_amdgcn_s_waitcnt(I8_WAIT_LGKM0);  // this wave's reads of stage st are done
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    issue(min(st + NS, nk - 1), st % NS);
+    read_frags(Fn, st + 1);
+    products(Fc);
+  };
+#pragma unroll
+  for (int st = 0; st < NS; ++st) issue(min(st, nk - 1), st);
+  wait_loads<(NS - 1) * DPS, (NS - 1) * (DPS - 1)>(most);
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+  Frags F0, F1;
+  read_frags(F0, 0);
+  for (int st = 0; st < nk; st += 2) {  // nk is even
+    step(st, F0, F1);
+    step(st + 1, F1, F0);
   }
-  for (int k0 = 0; k0 < a.kch; k0 += 8) {
-    // past the row's end x holds zeros (its rows are padded), so any chunk of w will do
-    const int cw = min(k0 + c8, a.kch - 1);
-    int4_t vw[2], vx[2];
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no load may land in LDS after the loop
+  // lane holds rows 16 j + r16 and channels 16 i + 4 g .. +3 of the wave's part
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      vw[u] = *reinterpret_cast<const int4_t*>(pw[u] + (size_t)cw * 16);
-      vx[u] = *reinterpret_cast<const int4_t*>(px[u] + (size_t)(k0 + c8) * 16);
-    }
-    __syncthreads();
+  for (int j = 0; j < NJ; ++j) {
+    const int r = r0 + (wt * NJ + j) * 16 + r16;
+    if (r >= r1) continue;
+    const float xs = a.xs[row_of_x<MODE>(a, r)];
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const int i = (tid >> 3) + 32 * u;
-      *reinterpret_cast<int4_t*>(s_w + i * LDT + c8 * 16) = vw[u];
-      *reinterpret_cast<int4_t*>(s_x + i * LDT + c8 * 16) = vx[u];
-    }
-    __syncthreads();
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int4_t b =
-          *reinterpret_cast<const int4_t*>(s_x + (wave * 16 + r16) * LDT + h * 64 + g * 16);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int4_t m =
-            *reinterpret_cast<const int4_t*>(s_w + (i * 16 + r16) * LDT + h * 64 + g * 16);
-        acc[i] = __builtin_amdgcn_mfma_i32_16x16x64_i8(m, b, acc[i], 0, 0, 0);
-      }
-    }
+    for (int i = 0; i < NI; i += G ? 2 : 1)
+      emit<MODE>(a, e, r, xs, n0 + (G ? (wc * NI + i) / 2 : wc * NI + i) * 16 + 4 * g, acc[i][j],
+                 acc[G ? i + 1 : i][j]);
   }
-  // lane holds row r16 of its wave and channels 16 i + 4 g .. +3
-  const int r = r0 + wave * 16 + r16;
-  if (r >= r1) return;
-  const float xs = a.xs[xrow(wave * 16 + r16)];
-#pragma unroll
-  for (int i = 0; i < 4; i += MODE == MODE_ACT_GATED ? 2 : 1)
-    emit<MODE>(a, e, r, xs, n0 + (MODE == MODE_ACT_GATED ? (i >> 1) : i) * 16 + 4 * g, acc[i],
-               acc[(i + 1) & 3]);
 }
 
 template <int MODE, int NC, int NR>
@@ -424,8 +499,11 @@ void product_launch(ProductArgs a, hipStream_t s) {
   } else if (a.tile == 32) {
     few_launch<MODE, MODE == MODE_ACT_GATED ? 2 : 1, 2>(a, tiles, s);
   } else {
-    constexpr int NT = MODE == MODE_ACT_GATED ? 32 : 64;
-    k_product<MODE><<<dim3((unsigned)(tiles * ((a.n + NT - 1) / NT))), dim3(TPB), 0, s>>>(a);
+    constexpr int NT = MODE == MODE_ACT_GATED ? T_CH / 2 : T_CH;
+    const dim3 grid((unsigned)((tiles * ((a.n + NT - 1) / NT) + 7) / 8 * 8)), block(T_W * 64);
+    if (a.tile == 64) k_product<MODE, 64><<<grid, block, 0, s>>>(a);
+    else if (a.tile == 128) k_product<MODE, 128><<<grid, block, 0, s>>>(a);
+    else k_product<MODE, 256><<<grid, block, 0, s>>>(a);
   }
 }
 

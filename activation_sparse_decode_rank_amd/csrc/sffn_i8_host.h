@@ -18,7 +18,7 @@ inline int i8_kpad(int K) { return (int)up_to((size_t)K, kI8Step); }
 // no groups).
 inline int i8_tile(size_t rows, size_t groups) {
   const size_t mean = (rows + groups - 1) / groups;
-  return mean <= 16 ? 16 : mean <= 32 ? 32 : 64;
+  return mean <= 16 ? 16 : mean <= 32 ? 32 : mean <= 64 ? 64 : mean <= 512 ? 128 : 256;
 }
 
 // Scratch of an 8-bit product whose activations have to be held in 8 bits (or padded) first:
