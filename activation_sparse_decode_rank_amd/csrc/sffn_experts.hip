@@ -59,24 +59,80 @@ __global__ __launch_bounds__(DTPB) void k_sort(const int32_t* __restrict__ idx, 
 }
 
 // y_t = sum over slots s in order of weights[t][s] * part[t k + s], slots without an expert
-// left out
+// left out; a thread takes four channels
 template <typename T>
 __global__ __launch_bounds__(TPB) void k_combine(const float* __restrict__ part, int64_t ldp,
                                                  const int32_t* __restrict__ idx,
                                                  const float* __restrict__ weights, int k, int E,
-                                                 int d, T* __restrict__ y, int64_t ldy) {
-  const int t = blockIdx.x;
-  for (int c = threadIdx.x; c < d; c += TPB) {
-    float v = 0.f;
-    for (int s = 0; s < k; ++s) {
-      const int r = t * k + s;
-      if ((unsigned)idx[r] < (unsigned)E) v += weights[r] * part[(size_t)r * ldp + c];
-    }
-    y[(size_t)t * ldy + c] = (T)v;
+                                                 int d, int blocks, T* __restrict__ y, int64_t ldy) {
+  const int t = blockIdx.x / blocks;
+  const int c = 4 * ((blockIdx.x % blocks) * TPB + threadIdx.x);
+  if (c >= d) return;
+  float4_t v = {0.f, 0.f, 0.f, 0.f};
+  for (int s = 0; s < k; ++s) {
+    const size_t r = (size_t)t * k + s;
+    if ((unsigned)idx[r] < (unsigned)E)  // part's rows have room up to a multiple of 64 channels
+      v += weights[r] * *reinterpret_cast<const float4_t*>(part + r * ldp + c);
   }
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (c + j < d) y[(size_t)t * ldy + c + j] = (T)v[j];
 }
 
 size_t esize(int type) { return type == T_F32 ? 4 : 2; }
+
+// the weights' side of the two products
+ProductArgs act_product(const ExpertsArgs& a) {
+  ProductArgs p{};
+  p.w = a.w_act;
+  p.ldw = a.ld_act;
+  p.ws = a.act_scale;
+  p.bias = a.b_act;
+  p.n = a.f;
+  p.kch = (a.d + 15) / 16;
+  p.cols = a.d;
+  p.out_type = T_F32;
+  p.experts = a.E;
+  p.w_group = (int64_t)a.f * (a.gated ? 2 : 1) * a.ld_act;
+  return p;
+}
+ProductArgs down_product(const ExpertsArgs& a) {
+  ProductArgs p{};
+  p.w = a.w_down;
+  p.ldw = a.ld_down;
+  p.ws = a.down_scale;
+  p.n = a.d;
+  p.kch = (a.f + 15) / 16;
+  p.cols = a.f;
+  p.out_type = T_F32;
+  p.experts = a.E;
+  p.w_group = (int64_t)a.d * a.ld_down;
+  return p;
+}
+
+// One token: h of its slots, then their down products and weighted sum, in two launches.
+hipError_t run_token(const ExpertsArgs& a, const void* x, int x_type, const int32_t* idx,
+                     const float* weights, int k, void* y, int y_type, char* work,
+                     const host::ExpertsCarve& c, hipStream_t s) {
+  ProductArgs up = act_product(a);
+  up.x = static_cast<const int8_t*>(x);
+  up.rows = k;
+  up.out = work + c.h;
+  up.ldo = (int64_t)c.ldh;
+  up.src = idx;
+  up.k = k;
+  const hipError_t e =
+      launch_product_fused(up, x_type, a.gated ? MODE_ACT_GATED : MODE_ACT, s);
+  if (e != hipSuccess) return e;
+  ProductArgs dn = down_product(a);
+  dn.x = reinterpret_cast<const int8_t*>(up.out);
+  dn.ldx = up.ldo;
+  dn.out = y;
+  dn.out_type = y_type;
+  dn.src = idx;
+  dn.k = k;
+  return launch_token_down(dn, weights, s);
+}
 
 }  // namespace
 
@@ -94,10 +150,18 @@ hipError_t run_experts(const ExpertsArgs& a, const void* x, int x_type, int64_t 
     int32_t* count = reinterpret_cast<int32_t*>(p + c.count);
     const int32_t* ic = idx + (size_t)t0 * k;
     const float* wc = weights + (size_t)t0 * k;
+    const char* xc = static_cast<const char*>(x) + (size_t)t0 * ldx * esize(x_type);
+    char* yc = static_cast<char*>(y) + (size_t)t0 * ldy * esize(y_type);
 
+    if (Tc == 1 && host::token_fused(a.d, a.f, k) &&
+        reinterpret_cast<uintptr_t>(xc) % (4 * esize(x_type)) == 0) {
+      const hipError_t e = run_token(a, xc, x_type, ic, wc, k, yc, y_type, p, c, s);
+      if (e != hipSuccess) return e;
+      continue;
+    }
     k_sort<<<dim3(1), dim3(DTPB), 0, s>>>(ic, R, a.E, c.tile, offs, src, tiles, count);
     QuantArgs qx{};
-    qx.x = static_cast<const char*>(x) + (size_t)t0 * ldx * esize(x_type);
+    qx.x = xc;
     qx.ldx = ldx;
     qx.rows = Tc;
     qx.cols = a.d;
@@ -108,20 +172,13 @@ hipError_t run_experts(const ExpertsArgs& a, const void* x, int x_type, int64_t 
     hipError_t e = launch_quantize(qx, x_type, s);
     if (e != hipSuccess) return e;
 
-    ProductArgs up{};
+    ProductArgs up = act_product(a);
     up.x = qx.q;
     up.ldx = qx.ldq;
     up.xs = qx.scale;
     up.rows = R;
-    up.w = a.w_act;
-    up.ldw = a.ld_act;
-    up.ws = a.act_scale;
-    up.bias = a.b_act;
-    up.n = a.f;
-    up.kch = (a.d + 15) / 16;
     up.out = p + c.h;
     up.ldo = (int64_t)c.ldh;
-    up.out_type = T_F32;
     up.offs = offs;
     up.tiles = tiles;
     up.n_tiles = count;
@@ -129,8 +186,6 @@ hipError_t run_experts(const ExpertsArgs& a, const void* x, int x_type, int64_t 
     up.max_tiles = c.max_tiles;
     up.tile = c.tile;
     up.k = k;
-    up.experts = a.E;
-    up.w_group = (int64_t)a.f * (a.gated ? 2 : 1) * a.ld_act;
     e = launch_product(up, a.gated ? MODE_ACT_GATED : MODE_ACT, s);
     if (e != hipSuccess) return e;
 
@@ -147,33 +202,34 @@ hipError_t run_experts(const ExpertsArgs& a, const void* x, int x_type, int64_t 
     e = launch_quantize(qh, T_F32, s);
     if (e != hipSuccess) return e;
 
-    ProductArgs dn = up;
+    ProductArgs dn = down_product(a);
     dn.x = qh.q;
     dn.ldx = qh.ldq;
     dn.xs = qh.scale;
-    dn.w = a.w_down;
-    dn.ldw = a.ld_down;
-    dn.ws = a.down_scale;
-    dn.bias = nullptr;
-    dn.n = a.d;
-    dn.kch = (a.f + 15) / 16;
+    dn.rows = R;
     dn.out = p + c.part;
     dn.ldo = (int64_t)c.ldp;
-    dn.w_group = (int64_t)a.d * a.ld_down;
+    dn.offs = offs;
+    dn.tiles = tiles;
+    dn.n_tiles = count;
+    dn.src = src;
+    dn.max_tiles = c.max_tiles;
+    dn.tile = c.tile;
+    dn.k = k;
     e = launch_product(dn, MODE_DOWN, s);
     if (e != hipSuccess) return e;
 
     const float* part = reinterpret_cast<const float*>(p + c.part);
-    char* yc = static_cast<char*>(y) + (size_t)t0 * ldy * esize(y_type);
-    const dim3 grid((unsigned)Tc), block(TPB);
+    const int blocks = (a.d + 4 * TPB - 1) / (4 * TPB);
+    const dim3 grid((unsigned)(Tc * blocks)), block(TPB);
     if (y_type == T_F32)
-      k_combine<float><<<grid, block, 0, s>>>(part, dn.ldo, ic, wc, k, a.E, a.d,
+      k_combine<float><<<grid, block, 0, s>>>(part, dn.ldo, ic, wc, k, a.E, a.d, blocks,
                                               reinterpret_cast<float*>(yc), ldy);
     else if (y_type == T_F16)
-      k_combine<_Float16><<<grid, block, 0, s>>>(part, dn.ldo, ic, wc, k, a.E, a.d,
+      k_combine<_Float16><<<grid, block, 0, s>>>(part, dn.ldo, ic, wc, k, a.E, a.d, blocks,
                                                  reinterpret_cast<_Float16*>(yc), ldy);
     else
-      k_combine<__bf16><<<grid, block, 0, s>>>(part, dn.ldo, ic, wc, k, a.E, a.d,
+      k_combine<__bf16><<<grid, block, 0, s>>>(part, dn.ldo, ic, wc, k, a.E, a.d, blocks,
                                                reinterpret_cast<__bf16*>(yc), ldy);
     e = hipGetLastError();
     if (e != hipSuccess) return e;

@@ -115,9 +115,28 @@ int sparse_ffn_i8_matmul(const void* x, int32_t x_dtype, const float* x_scale, i
   char* p = static_cast<char*>(work);
   const int kpad = sffn::host::i8_kpad(K);
   sffn::ProductArgs a{};
+  a.cols = K;
+  a.rows = M;
+  a.tile = sffn::host::i8_tile((size_t)M, 1);
+  a.w = w;
+  a.ldw = ldw;
+  a.ws = w_scale;
+  a.bias = bias;
+  a.n = N;
+  a.kch = (K + 15) / 16;
+  a.out = y;
+  a.ldo = ldy;
+  a.out_type = y_dtype;
+  // few rows: held in 8 bits by the product's own workgroups
+  if (!i8 && sffn::host::i8_fused((size_t)M, K) && ldx % 4 == 0 &&
+      aligned(x, 4 * type_size(x_dtype))) {
+    a.x = static_cast<const int8_t*>(x);
+    a.ldx = ldx;
+    return status(sffn::launch_product_fused(a, x_dtype, sffn::MODE_LINEAR, s));
+  }
   if (i8) {
-    // whole steps, rows on 16 bytes: read in place; otherwise copied to padded rows
-    if (K % sffn::host::kI8Step == 0 && ldx % 16 == 0 && aligned(x, 16)) {
+    // rows on 16 bytes that need no zeros behind them: read in place, otherwise copied
+    if (K % sffn::host::kI8Read == 0 && ldx % 16 == 0 && aligned(x, 16)) {
       a.x = static_cast<const int8_t*>(x);
       a.ldx = ldx;
     } else {
@@ -144,17 +163,6 @@ int sparse_ffn_i8_matmul(const void* x, int32_t x_dtype, const float* x_scale, i
     a.ldx = kpad;
     a.xs = q.scale;
   }
-  a.rows = M;
-  a.tile = sffn::host::i8_tile((size_t)M, 1);
-  a.w = w;
-  a.ldw = ldw;
-  a.ws = w_scale;
-  a.bias = bias;
-  a.n = N;
-  a.kch = (K + 15) / 16;
-  a.out = y;
-  a.ldo = ldy;
-  a.out_type = y_dtype;
   return status(sffn::launch_product(a, sffn::MODE_LINEAR, s));
 }
 

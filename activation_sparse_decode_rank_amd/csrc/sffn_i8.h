@@ -44,6 +44,7 @@ struct ProductArgs {
   const float* bias;   // may be null
   int n;               // channels (ACT_GATED: neurons, each of two rows of w)
   int kch;             // 16-byte chunks of a row
+  int cols;            // values of a row of x (fused forms only)
   void* out;
   int64_t ldo;         // elements
   int out_type;
@@ -60,6 +61,13 @@ struct ProductArgs {
   int64_t w_group;        // bytes from an expert's w to the next one's
 };
 hipError_t launch_product(const ProductArgs& a, ProductMode mode, hipStream_t s);
+// The same where a.x holds rows of x_type values (a.cols of them, a.ldx elements apart, at
+// places of 4 elements), which the kernel holds in 8 bits itself (host::i8_fused). LINEAR: a.rows
+// rows. ACT, ACT_GATED: one token, a.src is its idx [k] and slot s gives row s of out.
+hipError_t launch_product_fused(const ProductArgs& a, int x_type, ProductMode mode, hipStream_t s);
+// One token's down products and their weighted sum: a.x holds fp32 rows h (a.cols values, a.ldx
+// apart), a.src the token's idx [k], a.out the token's output row (host::token_fused).
+hipError_t launch_token_down(const ProductArgs& a, const float* weights, hipStream_t s);
 
 // x already in 8 bits, rows copied to zero-padded rows of kpad bytes
 hipError_t launch_pad_rows(const int8_t* x, int64_t ldx, int rows, int cols, int8_t* q, int kpad,

@@ -13,6 +13,9 @@ namespace {
 
 typedef int int4_t __attribute__((ext_vector_type(4)));
 
+// s_waitcnt operand (gfx9 encoding): LDS accesses only (lgkmcnt 0, vmcnt and expcnt at most)
+constexpr int I8_WAIT_LGKM0 = 0xC07F;
+
 constexpr float SMALLEST_ROW = 0x1p-100f;  // rows below this are held as zeros
 
 // The whole number nearest to x / s, ties to even, decided exactly: x * r (r about 1 / s)
@@ -74,18 +77,34 @@ __device__ __forceinline__ float4_t load4(const T* x, int i, int cols) {
   return v;
 }
 
+// Four values of a row, packed. Almost always every remainder is clearly inside half a step and
+// q stands; the neighbours are looked at only where one is not.
 __device__ __forceinline__ int quantize4(const float4_t& v, float s, float r) {
-  int p = 0;
+#pragma clang fp contract(off)
+  const float lim = 0.4999f * s;
+  int q[4];
+  bool near = false;
 #pragma unroll
-  for (int e = 0; e < 4; ++e) p |= (quantize(v[e], s, r) & 0xff) << (8 * e);
-  return p;
+  for (int e = 0; e < 4; ++e) {
+    const float f = rintf(v[e] * r);
+    near |= fabsf(__builtin_fmaf(-f, s, v[e])) > lim;
+    q[e] = (int)f;
+  }
+  if (near) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) q[e] = quantize(v[e], s, r);
+  }
+  const unsigned lo = (q[0] & 0xff) | ((q[1] & 0xff) << 8);
+  const unsigned hi = (q[2] & 0xff) | ((q[3] & 0xff) << 8);
+  return (int)(lo | (hi << 16));
 }
 
-// A workgroup takes a row. NV groups of four values per thread stay in registers between the
-// maximum and the rounding, so the row is read once (NV = 0: longer rows, read twice).
-template <typename T, bool VEC, int NV>
-__global__ __launch_bounds__(TPB) void k_quantize(QuantArgs a) {
-  __shared__ unsigned s_max[TPB / 64];
+// A workgroup of W waves takes a row. NV groups of four values per thread stay in registers
+// between the maximum and the rounding, so the row is read once (NV = 0: longer rows, twice).
+template <typename T, bool VEC, int W, int NV>
+__global__ __launch_bounds__(W * 64) void k_quantize(QuantArgs a) {
+  constexpr int TH = W * 64;
+  __shared__ unsigned s_max[W];
   const int rows = a.rows_dev ? min(*a.rows_dev, a.rows) : a.rows;
   const int nq = a.kpad / 4;
   for (int row = blockIdx.x; row < rows; row += gridDim.x) {
@@ -93,32 +112,32 @@ __global__ __launch_bounds__(TPB) void k_quantize(QuantArgs a) {
     int* q = reinterpret_cast<int*>(a.q + (size_t)row * a.ldq);
     unsigned m = 0;
     float r;
+    float4_t v[NV > 0 ? NV : 1];
     if constexpr (NV > 0) {
-      float4_t v[NV];
 #pragma unroll
-      for (int u = 0; u < NV; ++u) v[u] = load4<T, VEC>(x, threadIdx.x + u * TPB, a.cols);
+      for (int u = 0; u < NV; ++u) v[u] = load4<T, VEC>(x, threadIdx.x + u * TH, a.cols);
 #pragma unroll
       for (int u = 0; u < NV; ++u)
 #pragma unroll
         for (int e = 0; e < 4; ++e) m = max(m, mag(v[u][e]));
-      m = wg_max<TPB / 64>(m, s_max);
-      const float s = row_scale(m, r);
-      if (threadIdx.x == 0) a.scale[row] = s;
+    } else {
+      for (int i = threadIdx.x; i < nq; i += TH) {
+        const float4_t t = load4<T, VEC>(x, i, a.cols);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) m = max(m, mag(t[e]));
+      }
+    }
+    m = wg_max<W>(m, s_max);
+    const float s = row_scale(m, r);
+    if (threadIdx.x == 0) a.scale[row] = s;
+    if constexpr (NV > 0) {
 #pragma unroll
       for (int u = 0; u < NV; ++u) {
-        const int i = threadIdx.x + u * TPB;
+        const int i = threadIdx.x + u * TH;
         if (i < nq) q[i] = s > 0.f ? quantize4(v[u], s, r) : 0;
       }
     } else {
-      for (int i = threadIdx.x; i < nq; i += TPB) {
-        const float4_t v = load4<T, VEC>(x, i, a.cols);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) m = max(m, mag(v[e]));
-      }
-      m = wg_max<TPB / 64>(m, s_max);
-      const float s = row_scale(m, r);
-      if (threadIdx.x == 0) a.scale[row] = s;
-      for (int i = threadIdx.x; i < nq; i += TPB)
+      for (int i = threadIdx.x; i < nq; i += TH)
         q[i] = s > 0.f ? quantize4(load4<T, VEC>(x, i, a.cols), s, r) : 0;
     }
   }
@@ -213,121 +232,330 @@ __device__ __forceinline__ int row_of_x(const ProductArgs& a, int r) {
   return MODE == MODE_ACT || MODE == MODE_ACT_GATED ? a.src[r] / a.k : r;
 }
 
+// LDS accesses before it are done, in every wave of the workgroup, before any after it; loads
+// from memory stay in flight.
+__device__ __forceinline__ void lds_barrier() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(I8_WAIT_LGKM0);
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
 // Few rows: the weights are streamed from memory once, straight into the matrix cores'
-// registers. A workgroup of 8 waves takes 16 NC channels (gated: 8 NC neurons, gate and up rows
-// in tiles 2 i and 2 i + 1) and up to 16 NR rows; its waves take blocks of 256 bytes of the
-// length in turn (each lane 16 bytes of 4 steps; the next block's loads are issued before the
-// current block's products) and add their sums through LDS at the end, whole numbers, so the
-// split changes nothing. x comes from the caches.
+// registers. A workgroup of 8 waves takes tiles of 16 NC channels (gated: 8 NC neurons, gate and
+// up rows in 16-row tiles 2 i and 2 i + 1) and up to 16 NR rows; its waves take blocks of 256
+// bytes (128 where x comes from the caches: registers) of the length in turn and add their sums through LDS at
+// the end of a tile, whole numbers, so the split changes nothing. The next block's loads, also
+// those of the next tile, are issued before the current block's products, so that the stream
+// does not stop at a tile's end.
+// X = void: x is in 8 bits and comes from the caches. Otherwise x is X's rows, which each
+// workgroup first holds in 8 bits in its own LDS: that costs less than a launch before this one
+// while the rows are few.
 constexpr int SK_W = 8;          // waves
-constexpr int SK_BLK = 16;       // 16-byte chunks of a block
 
-template <int MODE, int NC, int NR>
-__global__ __launch_bounds__(SK_W * 64) void k_product_few(ProductArgs a) {
-  constexpr bool G = MODE == MODE_ACT_GATED;
-  constexpr int NT = G ? 8 * NC : 16 * NC;
-  __shared__ __attribute__((aligned(16))) int4_t s_acc[SK_W][NC * NR][64];
-  const int nnt = (a.n + NT - 1) / NT;
-  const int nt = blockIdx.x % nnt;
-  int e, r0, r1;
-  if (!tile_rows<MODE>(a, blockIdx.x / nnt, e, r0, r1)) return;
-  r1 = min(r1, r0 + 16 * NR);
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int r16 = lane & 15, g = lane >> 4;
-  const int n0 = nt * NT;
-  const int nw = G ? 2 * a.n : a.n;
-  const int8_t* pw[NC];
-  const int8_t* px[NR];
+// row `row` of x (X's, cols values) into 8 bits at s_q [kpad], by all W waves; its scale
+template <typename X, int W>
+__device__ __forceinline__ float quantize_to_lds(const X* x, int cols, int kpad, int8_t* s_q,
+                                                 unsigned* s_max) {
+  unsigned m = 0;
+  for (int i = threadIdx.x; i < kpad / 4; i += W * 64) {
+    const float4_t v = load4<X, true>(x, i, cols);
 #pragma unroll
-  for (int i = 0; i < NC; ++i) {
-    const int row = G ? 2 * (n0 + (i >> 1) * 16 + r16) + (i & 1) : n0 + i * 16 + r16;
-    pw[i] = a.w + (size_t)e * a.w_group + (size_t)min(row, nw - 1) * a.ldw + g * 16;
+    for (int e = 0; e < 4; ++e) m = max(m, mag(v[e]));
   }
-#pragma unroll
-  for (int t = 0; t < NR; ++t)
-    px[t] = a.x + (size_t)row_of_x<MODE>(a, min(r0 + t * 16 + r16, r1 - 1)) * a.ldx + g * 16;
+  m = wg_max<W>(m, s_max);
+  float r;
+  const float s = row_scale(m, r);
+  for (int i = threadIdx.x; i < kpad / 4; i += W * 64)
+    reinterpret_cast<int*>(s_q)[i] = s > 0.f ? quantize4(load4<X, true>(x, i, cols), s, r) : 0;
+  return s;
+}
 
-  int4_t acc[NC][NR];
+template <int MODE, int NC, int NR, typename X>
+__global__ __launch_bounds__(SK_W * 64, 4) void k_product_few(ProductArgs a) {
+  // steps of 64 bytes in a block: as many as keep two workgroups' registers on a compute unit
+  constexpr int S = std::is_void<X>::value ? 2 : 4;
+  constexpr int BLK = S * 4;  // 16-byte chunks of a block
+  constexpr bool G = MODE == MODE_ACT_GATED;
+  constexpr bool FUSED = !std::is_void<X>::value;
+  constexpr int NT = G ? 8 * NC : 16 * NC;
+  __shared__ int s_sum[2][NC * NR][4][64];  // [tile parity][16 x 16 tile][channel][lane]
+  __shared__ unsigned s_max[SK_W];
+  extern __shared__ __attribute__((aligned(16))) int8_t s_x[];  // FUSED: rows of kpad bytes
+  const int nnt = (a.n + NT - 1) / NT;
+  const int nmt = FUSED ? (MODE == MODE_LINEAR ? 1 : a.k)
+                        : MODE == MODE_LINEAR ? (a.rows + 16 * NR - 1) / (16 * NR) : *a.n_tiles;
+  const int total = nmt * nnt;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int r16 = lane & 15, g = lane >> 4;
+  const int nw = G ? 2 * a.n : a.n;
+  const int nb = (a.kch + BLK - 1) / BLK;
+  const int kpad = nb * BLK * 16;  // FUSED: bytes of a row in LDS
+
+  struct Tile {
+    int id, e, r0, r1, n0;
+  };
+  // the first tile from id on (in steps of the grid) that has rows; its id is >= total if none
+  auto tile_from = [&](int id) {
+    Tile t{id, 0, 0, 0, 0};
+    for (; t.id < total; t.id += gridDim.x) {
+      const int mt = t.id / nnt;
+      t.n0 = (t.id % nnt) * NT;
+      if (FUSED && MODE != MODE_LINEAR) {  // one token: tile row mt is its slot
+        t.e = a.src[mt];
+        t.r0 = mt;
+        t.r1 = mt + 1;
+        if ((unsigned)t.e < (unsigned)a.experts) break;
+      } else {
+        tile_rows<MODE>(a, mt, t.e, t.r0, t.r1);
+        t.r1 = min(t.r1, t.r0 + 16 * NR);
+        break;
+      }
+    }
+    return t;
+  };
+  const int8_t* wbase = nullptr;  // first row of the tile, one for all lanes
+  unsigned wrow[NC];              // this lane's rows from there, in bytes
+  const int8_t* px[NR];
+  auto aim = [&](const Tile& t) {
+    const int first = G ? 2 * t.n0 : t.n0;
+    wbase = a.w + (size_t)t.e * a.w_group + (size_t)first * a.ldw;
 #pragma unroll
-  for (int i = 0; i < NC; ++i)
+    for (int i = 0; i < NC; ++i) {
+      const int row = G ? (i >> 1) * 32 + 2 * r16 + (i & 1) : i * 16 + r16;
+      wrow[i] = (unsigned)min(row, nw - 1 - first) * (unsigned)a.ldw + g * 16;
+    }
+    if constexpr (!FUSED) {
 #pragma unroll
-    for (int t = 0; t < NR; ++t) acc[i][t] = int4_t{0, 0, 0, 0};
+      for (int j = 0; j < NR; ++j)
+        px[j] = a.x + (size_t)row_of_x<MODE>(a, min(t.r0 + j * 16 + r16, t.r1 - 1)) * a.ldx + g * 16;
+    }
+  };
   struct Block {
-    int4_t w[4][NC], x[4][NR];
+    int4_t w[S][NC], x[FUSED ? 1 : S][NR];
   };
   auto load = [&](Block& B, int b) {
+    const unsigned o = (unsigned)b * (BLK * 16);
+    if ((b + 1) * BLK <= a.kch) {
 #pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      const size_t o = (size_t)b * (SK_BLK * 16) + s * 64;
+      for (int s = 0; s < S; ++s)
 #pragma unroll
-      for (int i = 0; i < NC; ++i)
-        B.w[s][i] = __builtin_nontemporal_load(reinterpret_cast<const int4_t*>(pw[i] + o));
+        for (int i = 0; i < NC; ++i)
+          B.w[s][i] = __builtin_nontemporal_load(
+              reinterpret_cast<const int4_t*>(wbase + (size_t)(wrow[i] + o) + s * 64));
+    } else {
+      // past w's row x is zero (its rows are padded to whole blocks), so any chunk will do
 #pragma unroll
-      for (int t = 0; t < NR; ++t) B.x[s][t] = *reinterpret_cast<const int4_t*>(px[t] + o);
+      for (int s = 0; s < S; ++s)
+#pragma unroll
+        for (int i = 0; i < NC; ++i)
+          B.w[s][i] = *reinterpret_cast<const int4_t*>(
+              wbase + (size_t)(wrow[i] + (unsigned)(min(b * BLK + s * 4 + g, a.kch - 1) - g) * 16));
+    }
+    if constexpr (!FUSED) {
+#pragma unroll
+      for (int s = 0; s < S; ++s)
+#pragma unroll
+        for (int j = 0; j < NR; ++j)
+          B.x[s][j] = *reinterpret_cast<const int4_t*>(px[j] + (size_t)o + s * 64);
     }
   };
-  auto products = [&](const Block& B) {
+  Tile t = tile_from(blockIdx.x);
+  if (t.id >= total) return;
+  Block B0, B1;
+  if (wave < nb) {
+    aim(t);
+    load(B0, wave);
+  }
+  for (int i = tid; i < 2 * NC * NR * 256; i += SK_W * 64) (&s_sum[0][0][0][0])[i] = 0;
+  const int rows_x = MODE == MODE_LINEAR ? a.rows : 1;
+  float xs_own = 0.f;
+  if constexpr (FUSED) {
+    for (int m = 0; m < rows_x; ++m) {
+      const float s = quantize_to_lds<X, SK_W>(reinterpret_cast<const X*>(a.x) + (size_t)m * a.ldx,
+                                               a.cols, kpad, s_x + m * kpad,
+                                               s_max);
+      if (m == r16 || MODE != MODE_LINEAR) xs_own = s;
+    }
+  }
+  lds_barrier();
+  const int8_t* fx = s_x + (MODE == MODE_LINEAR ? min(r16, rows_x - 1) : 0) * kpad + g * 16;
+  for (int par = 0; t.id < total; par ^= 1) {
+    const Tile next = tile_from(t.id + gridDim.x);
+    int4_t acc[NC][NR];
+#pragma unroll
+    for (int i = 0; i < NC; ++i)
+#pragma unroll
+      for (int j = 0; j < NR; ++j) acc[i][j] = int4_t{0, 0, 0, 0};
+    for (int b = wave; b < nb; b += SK_W) {
+      if (b + SK_W < nb) {
+        load(B1, b + SK_W);
+      } else if (next.id < total) {
+        aim(next);
+        load(B1, wave);
+      }
+#pragma unroll
+      for (int s = 0; s < S; ++s) {
+        int4_t x[NR];
+#pragma unroll
+        for (int j = 0; j < NR; ++j) {
+          if constexpr (FUSED)
+            x[j] = *reinterpret_cast<const int4_t*>(fx + b * (BLK * 16) + s * 64);
+          else
+            x[j] = B0.x[s][j];
+        }
+#pragma unroll
+        for (int i = 0; i < NC; ++i)
+#pragma unroll
+          for (int j = 0; j < NR; ++j)
+            acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(B0.w[s][i], x[j], acc[i][j], 0, 0, 0);
+      }
+      B0 = B1;
+    }
+    if (wave < nb) {
+#pragma unroll
+      for (int i = 0; i < NC; ++i)
+#pragma unroll
+        for (int j = 0; j < NR; ++j)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) atomicAdd(&s_sum[par][i * NR + j][c][lane], acc[i][j][c]);
+    }
+    // The sums of the tile two before this one were read and cleared before this wave's
+    // arrival here, and the other parity's are free to be added to after it.
+    lds_barrier();
+    auto take = [&](int q) {
+      int4_t v;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        v[c] = s_sum[par][q][c][lane];
+        s_sum[par][q][c][lane] = 0;
+      }
+      return v;
+    };
+    // wave w: tiles w, w + 8, ... (gated: pairs of tiles); lane: row r16, channels 4 g .. +3
+    for (int q = wave; q < (G ? NC / 2 : NC) * NR; q += SK_W) {
+      const int i = q / NR, j = q % NR;
+      const int r = t.r0 + j * 16 + r16;
+      int4_t v, u = {0, 0, 0, 0};
+      if (G) {
+        v = take(2 * i * NR + j);
+        u = take((2 * i + 1) * NR + j);
+      } else {
+        v = take(q);
+      }
+      if (r >= t.r1) continue;
+      const float xs = FUSED ? xs_own : a.xs[row_of_x<MODE>(a, r)];
+      emit<MODE>(a, t.e, r, xs, t.n0 + i * 16 + 4 * g, v, u);
+    }
+    t = next;
+  }
+}
+
+// The down product of one token, with everything around it: each workgroup holds the rows h of
+// the token's slots in 8 bits in its LDS, 16 waves take blocks of 256 bytes of all slots'
+// lengths in turn for 16 channels of every slot's expert, and the weighted sum over the slots,
+// in slot order, is the token's output. Sums of one slot meet in LDS by whole-number adds.
+constexpr int TD_W = 16;
+constexpr int SK_BLK = 16;       // 16-byte chunks of a block
+
+__global__ __launch_bounds__(TD_W * 64) void k_token_down(ProductArgs a, const float* __restrict__ weights) {
+  __shared__ int s_sum[2][64][16];  // [tile parity][slot][channel]
+  __shared__ float s_hs[64];
+  __shared__ int s_e[64];           // expert of the v-th slot that has one, and its slot
+  __shared__ int s_slot[64];
+  __shared__ unsigned s_max[64];
+  extern __shared__ __attribute__((aligned(16))) int8_t s_h[];  // [slots][kpad]
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int r16 = lane & 15, g = lane >> 4;
+  const int nb = (a.kch + SK_BLK - 1) / SK_BLK, kpad = nb * SK_BLK * 16;
+  // every wave lists the slots that have an expert
+  const int my = lane < a.k ? a.src[lane] : -1;
+  const uint64_t on = __ballot((unsigned)my < (unsigned)a.experts);
+  const int nv = __popcll(on);
+  if (wave == 0 && ((on >> lane) & 1)) {
+    const int v = __popcll(on & ((1ull << lane) - 1));
+    s_e[v] = my;
+    s_slot[v] = lane;
+  }
+  if (tid < 64) s_max[tid] = 0;
+  for (int i = tid; i < 2 * 64 * 16; i += TD_W * 64) (&s_sum[0][0][0])[i] = 0;
+  lds_barrier();
+  const int units = nv * nb;
+  const int nnt = (a.n + 15) / 16;
+  int4_t w0[4], w1[4];
+  auto load = [&](int4_t* w, int nt, int u) {
+    const int row = min(nt * 16 + r16, a.n - 1);
+    const int8_t* p = a.w + (size_t)s_e[u / nb] * a.w_group + (size_t)row * a.ldw;
 #pragma unroll
     for (int s = 0; s < 4; ++s)
-#pragma unroll
-      for (int i = 0; i < NC; ++i)
-#pragma unroll
-        for (int t = 0; t < NR; ++t)
-          acc[i][t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(B.w[s][i], B.x[s][t], acc[i][t], 0, 0, 0);
+      w[s] = __builtin_nontemporal_load(reinterpret_cast<const int4_t*>(
+          p + (size_t)min((u % nb) * SK_BLK + s * 4 + g, a.kch - 1) * 16));
   };
-  const int nb = a.kch / SK_BLK;  // whole blocks
-  Block B0, B1;
-  int b = wave;
-  if (b < nb) load(B0, b);
-  while (b < nb) {
-    if (b + SK_W < nb) load(B1, b + SK_W);
-    products(B0);
-    b += SK_W;
-    if (b >= nb) break;
-    if (b + SK_W < nb) load(B0, b + SK_W);
-    products(B1);
-    b += SK_W;
-  }
-  // the last, part block: one wave, chunk by chunk
-  if (nb * SK_BLK < a.kch && wave == nb % SK_W) {
-    for (int c = nb * SK_BLK; c < a.kch; c += 4) {
-      const int4_t z = {0, 0, 0, 0};
-      const bool in = c + g < a.kch;
-      int4_t w[NC], x[NR];
+  int nt = blockIdx.x;
+  if (wave < units && nt < nnt) load(w0, nt, wave);
+  // h into 8 bits: the slots' maxima, then the whole numbers
+  const float* h = reinterpret_cast<const float*>(a.x);
+  for (int v = 0; v < nv; ++v) {
+    unsigned m = 0;
+    for (int i = tid; i < kpad / 4; i += TD_W * 64) {
+      const float4_t t = load4<float, true>(h + (size_t)s_slot[v] * a.ldx, i, a.cols);
 #pragma unroll
-      for (int i = 0; i < NC; ++i)
-        w[i] = in ? *reinterpret_cast<const int4_t*>(pw[i] + (size_t)c * 16) : z;
-#pragma unroll
-      for (int t = 0; t < NR; ++t)
-        x[t] = in ? *reinterpret_cast<const int4_t*>(px[t] + (size_t)c * 16) : z;
-#pragma unroll
-      for (int i = 0; i < NC; ++i)
-#pragma unroll
-        for (int t = 0; t < NR; ++t)
-          acc[i][t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[i], x[t], acc[i][t], 0, 0, 0);
+      for (int e = 0; e < 4; ++e) m = max(m, mag(t[e]));
     }
+    for (int o = 32; o; o >>= 1) m = max(m, (unsigned)__shfl_xor((int)m, o));
+    if (lane == 0) atomicMax(&s_max[v], m);
   }
+  lds_barrier();
+  for (int v = 0; v < nv; ++v) {
+    float r;
+    const float s = row_scale(s_max[v], r);
+    if (tid == 0) s_hs[v] = s;
+    for (int i = tid; i < kpad / 4; i += TD_W * 64)
+      reinterpret_cast<int*>(s_h + v * kpad)[i] =
+          s > 0.f ? quantize4(load4<float, true>(h + (size_t)s_slot[v] * a.ldx, i, a.cols), s, r) : 0;
+  }
+  lds_barrier();
+  for (int par = 0; nt < nnt; nt += gridDim.x, par ^= 1) {
+    const int nn = nt + gridDim.x;
+    int4_t acc = {0, 0, 0, 0};
+    for (int u = wave; u < units; u += TD_W) {
+      if (u + TD_W < units) load(w1, nt, u + TD_W);
+      else if (nn < nnt) load(w1, nn, wave);
+      const int8_t* f = s_h + u * (SK_BLK * 16) + g * 16;  // slot u / nb, block u % nb
 #pragma unroll
-  for (int i = 0; i < NC; ++i)
+      for (int s = 0; s < 4; ++s)
+        acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(w0[s], *reinterpret_cast<const int4_t*>(f + s * 64),
+                                                    acc, 0, 0, 0);
+      if (u + TD_W >= units || (u + TD_W) / nb != u / nb) {
+        if (r16 == 0) {
 #pragma unroll
-    for (int t = 0; t < NR; ++t) s_acc[wave][i * NR + t][lane] = acc[i][t];
-  __syncthreads();
-  auto total = [&](int q) {
-    int4_t v = s_acc[0][q][lane];
+          for (int j = 0; j < 4; ++j) atomicAdd(&s_sum[par][u / nb][4 * g + j], acc[j]);
+        }
+        acc = int4_t{0, 0, 0, 0};
+      }
 #pragma unroll
-    for (int w = 1; w < SK_W; ++w) v += s_acc[w][q][lane];
-    return v;
-  };
-  // wave w: tiles w, w + 8, ... (gated: pairs of tiles); lane: row r16, channels 4 g .. +3
-  for (int q = wave; q < (G ? NC / 2 : NC) * NR; q += SK_W) {
-    const int i = q / NR, t = q % NR;
-    const int r = r0 + t * 16 + r16;
-    if (r >= r1) continue;
-    const float xs = a.xs[row_of_x<MODE>(a, r)];
-    if (G)
-      emit<MODE>(a, e, r, xs, n0 + i * 16 + 4 * g, total(2 * i * NR + t), total((2 * i + 1) * NR + t));
-    else
-      emit<MODE>(a, e, r, xs, n0 + i * 16 + 4 * g, total(q), int4_t{0, 0, 0, 0});
+      for (int s = 0; s < 4; ++s) w0[s] = w1[s];
+    }
+    lds_barrier();
+    if (tid < 16) {
+      const int c = nt * 16 + tid;
+      float y = 0.f;
+      for (int v = 0; v < nv; ++v) {
+        const int sum = s_sum[par][v][tid];
+        s_sum[par][v][tid] = 0;
+        if (c < a.n) {
+          const float p = (float)sum * (s_hs[v] * a.ws[(size_t)s_e[v] * a.n + c]);
+          y += weights[s_slot[v]] * p;
+        }
+      }
+      if (c < a.n) {
+        if (a.out_type == T_F32) static_cast<float*>(a.out)[c] = y;
+        else if (a.out_type == T_F16) static_cast<_Float16*>(a.out)[c] = (_Float16)y;
+        else static_cast<__bf16*>(a.out)[c] = (__bf16)y;
+      }
+    }
   }
 }
 
@@ -342,8 +570,6 @@ __global__ __launch_bounds__(SK_W * 64) void k_product_few(ProductArgs a) {
 constexpr int T_CH = 256;   // rows of w per tile
 constexpr int T_K = 64;     // bytes per stage
 constexpr int T_W = 8;      // waves
-// s_waitcnt operand (gfx9 encoding): LDS reads only (lgkmcnt 0, vmcnt and expcnt at most)
-constexpr int I8_WAIT_LGKM0 = 0xC07F;
 
 // this lane's 16 bytes at src to place 16 * lane of the 1 KB block at dst (LDS)
 __device__ __forceinline__ void load_block(const int8_t* src, int8_t* dst) {
@@ -482,11 +708,24 @@ __global__ __launch_bounds__(T_W * 64) void k_product(ProductArgs a) {
   }
 }
 
-template <int MODE, int NC, int NR>
-void few_launch(const ProductArgs& a, int64_t tiles, hipStream_t s) {
+// workgroups of a kernel that the current device holds at once (asked once per kernel)
+template <typename K>
+int resident(K kernel, int threads, size_t lds) {
+  int dev = 0, cus = 0, per = 0;
+  if (hipGetDevice(&dev) != hipSuccess ||
+      hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess ||
+      hipOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, threads, lds) != hipSuccess)
+    return 512;
+  return std::max(1, cus * per);
+}
+
+template <int MODE, int NC, int NR, typename X>
+void few_launch(const ProductArgs& a, int64_t row_tiles, size_t lds, hipStream_t s) {
   constexpr int NT = MODE == MODE_ACT_GATED ? 8 * NC : 16 * NC;
-  const dim3 grid((unsigned)(tiles * ((a.n + NT - 1) / NT)));
-  k_product_few<MODE, NC, NR><<<grid, dim3(SK_W * 64), 0, s>>>(a);
+  const int64_t tiles = row_tiles * ((a.n + NT - 1) / NT);
+  const int at_once = resident(k_product_few<MODE, NC, NR, X>, SK_W * 64, lds);
+  k_product_few<MODE, NC, NR, X>
+      <<<dim3((unsigned)std::min<int64_t>(tiles, at_once)), dim3(SK_W * 64), lds, s>>>(a);
 }
 
 template <int MODE>
@@ -495,9 +734,9 @@ void product_launch(ProductArgs a, hipStream_t s) {
               reinterpret_cast<uintptr_t>(a.out) % (a.out_type == T_F32 ? 16 : 8) == 0;
   const int64_t tiles = MODE == MODE_LINEAR ? ((int64_t)a.rows + a.tile - 1) / a.tile : a.max_tiles;
   if (a.tile == 16) {
-    few_launch<MODE, MODE == MODE_ACT_GATED ? 2 : 1, 1>(a, tiles, s);
+    few_launch<MODE, MODE == MODE_ACT_GATED ? 2 : 1, 1, void>(a, tiles, 0, s);
   } else if (a.tile == 32) {
-    few_launch<MODE, MODE == MODE_ACT_GATED ? 2 : 1, 2>(a, tiles, s);
+    few_launch<MODE, MODE == MODE_ACT_GATED ? 2 : 1, 2, void>(a, tiles, 0, s);
   } else {
     constexpr int NT = MODE == MODE_ACT_GATED ? T_CH / 2 : T_CH;
     const dim3 grid((unsigned)((tiles * ((a.n + NT - 1) / NT) + 7) / 8 * 8)), block(T_W * 64);
@@ -509,12 +748,12 @@ void product_launch(ProductArgs a, hipStream_t s) {
 
 template <typename T, bool VEC>
 void quantize_rows(const QuantArgs& a, hipStream_t s) {
-  const dim3 grid((unsigned)std::min(a.rows, 1 << 20)), block(TPB);
-  const int nv = (a.kpad / 4 + TPB - 1) / TPB;
-  if (nv <= 2) k_quantize<T, VEC, 2><<<grid, block, 0, s>>>(a);
-  else if (nv <= 4) k_quantize<T, VEC, 4><<<grid, block, 0, s>>>(a);
-  else if (nv <= 12) k_quantize<T, VEC, 12><<<grid, block, 0, s>>>(a);
-  else k_quantize<T, VEC, 0><<<grid, block, 0, s>>>(a);
+  const dim3 grid((unsigned)std::min(a.rows, 1 << 20));
+  const int nq = a.kpad / 4;
+  if (nq <= 4 * 64) k_quantize<T, VEC, 1, 4><<<grid, dim3(64), 0, s>>>(a);
+  else if (nq <= 4 * 256) k_quantize<T, VEC, 4, 4><<<grid, dim3(256), 0, s>>>(a);
+  else if (nq <= 4 * 1024) k_quantize<T, VEC, 16, 4><<<grid, dim3(1024), 0, s>>>(a);
+  else k_quantize<T, VEC, 16, 0><<<grid, dim3(1024), 0, s>>>(a);
 }
 
 template <typename T>
@@ -524,7 +763,37 @@ void quantize_launch(const QuantArgs& a, hipStream_t s) {
   else quantize_rows<T, false>(a, s);
 }
 
+template <int MODE, typename X>
+void fused_launch(ProductArgs a, hipStream_t s) {
+  a.vec_out = a.ldo % 4 == 0 &&
+              reinterpret_cast<uintptr_t>(a.out) % (a.out_type == T_F32 ? 16 : 8) == 0;
+  const size_t rows = MODE == MODE_LINEAR ? a.rows : 1;
+  few_launch<MODE, MODE == MODE_ACT_GATED ? 2 : 1, 1, X>(a, MODE == MODE_LINEAR ? 1 : a.k,
+                                                         rows * host::i8_kpad(a.cols), s);
+}
+
+template <typename X>
+void fused_launch(const ProductArgs& a, ProductMode mode, hipStream_t s) {
+  if (mode == MODE_LINEAR) fused_launch<MODE_LINEAR, X>(a, s);
+  else if (mode == MODE_ACT) fused_launch<MODE_ACT, X>(a, s);
+  else fused_launch<MODE_ACT_GATED, X>(a, s);
+}
+
 }  // namespace
+
+hipError_t launch_product_fused(const ProductArgs& a, int x_type, ProductMode mode, hipStream_t s) {
+  if (x_type == T_F32) fused_launch<float>(a, mode, s);
+  else if (x_type == T_F16) fused_launch<_Float16>(a, mode, s);
+  else fused_launch<__bf16>(a, mode, s);
+  return hipGetLastError();
+}
+
+hipError_t launch_token_down(const ProductArgs& a, const float* weights, hipStream_t s) {
+  const size_t lds = (size_t)a.k * host::i8_kpad(a.cols);
+  const int at_once = resident(k_token_down, TD_W * 64, lds);
+  k_token_down<<<dim3((unsigned)std::min((a.n + 15) / 16, at_once)), dim3(TD_W * 64), lds, s>>>(a, weights);
+  return hipGetLastError();
+}
 
 hipError_t launch_quantize(const QuantArgs& a, int dtype, hipStream_t s) {
   if (dtype == T_F32) quantize_launch<float>(a, s);

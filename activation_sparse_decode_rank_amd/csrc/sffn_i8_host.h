@@ -10,8 +10,10 @@ namespace host {
 
 inline size_t up_to(size_t v, size_t m) { return (v + m - 1) / m * m; }
 
-// 8-bit rows of activations are padded with zeros to whole steps of the products
-constexpr int kI8Step = 128;
+// 8-bit rows of activations are padded with zeros to whole blocks of the products (256 bytes);
+// the products read them up to a multiple of 128 bytes.
+constexpr int kI8Step = 256;
+constexpr int kI8Read = 128;
 inline int i8_kpad(int K) { return (int)up_to((size_t)K, kI8Step); }
 
 // Rows of a product tile, from the mean rows of a group (of the whole product where there are
@@ -19,6 +21,19 @@ inline int i8_kpad(int K) { return (int)up_to((size_t)K, kI8Step); }
 inline int i8_tile(size_t rows, size_t groups) {
   const size_t mean = (rows + groups - 1) / groups;
   return mean <= 16 ? 16 : mean <= 32 ? 32 : mean <= 64 ? 64 : mean <= 512 ? 128 : 256;
+}
+
+// Whether M rows of K values are held in 8 bits by the product itself: every workgroup does it
+// for all rows, so few of them, and within the LDS that leaves two workgroups a compute unit.
+constexpr int kFusedRows = 4;
+constexpr int kFusedLds = 64 * 1024;
+inline bool i8_fused(size_t M, int K) {
+  return M <= (size_t)kFusedRows && M * (size_t)i8_kpad(K) <= (size_t)kFusedLds;
+}
+// Whether one token of k slots goes through its experts in two launches, the slots' rows of f
+// values held in LDS.
+inline bool token_fused(int d, int f, int k) {
+  return i8_fused(1, d) && (size_t)k * (size_t)i8_kpad(f) <= (size_t)kFusedLds;
 }
 
 // Scratch of an 8-bit product whose activations have to be held in 8 bits (or padded) first:

@@ -194,7 +194,7 @@ int main() {
                            (size_t)c.max_tiles * 8, 4, R * c.ldh * 4, R * (size_t)i8_kpad(f), R * 4,
                            R * c.ldp * 4};
     for (int i = 0; i < 10; ++i) { CHECK(at[i] % 256 == 0); CHECK(at[i] + need[i] <= at[i + 1]); }
-    CHECK(c.ldh >= (size_t)f && c.ldp >= (size_t)d && i8_kpad(d) >= d && i8_kpad(d) % 128 == 0);
+    CHECK(c.ldh >= (size_t)f && c.ldp >= (size_t)d && i8_kpad(d) >= d && i8_kpad(d) % 256 == 0);
     // any split of the rows over the experts
     std::vector<size_t> n(E, 0);
     const int used = pick(1, E);
