@@ -241,6 +241,20 @@ __device__ __forceinline__ void lds_barrier() {
   asm volatile("" ::: "memory");
 }
 
+// The stream of weights reads whole 128-byte lines: one load takes 8 rows x 128 bytes, lane
+// (r16 = lane % 16, g = lane / 16) the 16-byte chunk g + 4 (r16 / 8) of row r16 % 8, and a second
+// one the 8 rows after them. The matrix cores want chunk g (then 4 + g) of row r16 in that
+// lane: the two loads' values change places between the halves of each 16 lanes. Loads of 16
+// rows x 64 bytes need no change but halve the lines: 6.1 against 6.9 TB/s for a plain stream.
+constexpr int DPP_ROW_ROR8 = 0x128;
+__device__ __forceinline__ void to_steps(const int4_t& a, const int4_t& b, int4_t& s0, int4_t& s1) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    s0[i] = __builtin_amdgcn_update_dpp(a[i], b[i], DPP_ROW_ROR8, 0xF, 0xC, false);
+    s1[i] = __builtin_amdgcn_update_dpp(b[i], a[i], DPP_ROW_ROR8, 0xF, 0x3, false);
+  }
+}
+
 // Few rows: the weights are streamed from memory once, straight into the matrix cores'
 // registers. A workgroup of 8 waves takes tiles of 16 NC channels (gated: 8 NC neurons, gate and
 // up rows in 16-row tiles 2 i and 2 i + 1) and up to 16 NR rows; its waves take blocks of 256
@@ -315,16 +329,21 @@ __global__ __launch_bounds__(SK_W * 64, 4) void k_product_few(ProductArgs a) {
     }
     return t;
   };
+  const int lc = g + 4 * (r16 >> 3);  // chunk of 128 bytes that this lane loads
   const int8_t* wbase = nullptr;  // first row of the tile, one for all lanes
-  unsigned wrow[NC];              // this lane's rows from there, in bytes
+  unsigned wrow[NC][2];           // this lane's two rows of each 16 from there, in bytes
   const int8_t* px[NR];
   auto aim = [&](const Tile& t) {
     const int first = G ? 2 * t.n0 : t.n0;
     wbase = a.w + (size_t)t.e * a.w_group + (size_t)first * a.ldw;
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
-      const int row = G ? (i >> 1) * 32 + 2 * r16 + (i & 1) : i * 16 + r16;
-      wrow[i] = (unsigned)min(row, nw - 1 - first) * (unsigned)a.ldw + g * 16;
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const int r = (r16 & 7) + 8 * q;
+        const int row = G ? (i >> 1) * 32 + 2 * r + (i & 1) : i * 16 + r;
+        wrow[i][q] = (unsigned)min(row, nw - 1 - first) * (unsigned)a.ldw;
+      }
     }
     if constexpr (!FUSED) {
 #pragma unroll
@@ -337,21 +356,16 @@ __global__ __launch_bounds__(SK_W * 64, 4) void k_product_few(ProductArgs a) {
   };
   auto load = [&](Block& B, int b) {
     const unsigned o = (unsigned)b * (BLK * 16);
-    if ((b + 1) * BLK <= a.kch) {
 #pragma unroll
-      for (int s = 0; s < S; ++s)
-#pragma unroll
-        for (int i = 0; i < NC; ++i)
-          B.w[s][i] = __builtin_nontemporal_load(
-              reinterpret_cast<const int4_t*>(wbase + (size_t)(wrow[i] + o) + s * 64));
-    } else {
+    for (int s = 0; s < S; s += 2) {
       // past w's row x is zero (its rows are padded to whole blocks), so any chunk will do
+      const unsigned c = (unsigned)min(b * BLK + s * 4 + lc, a.kch - 1) * 16;
 #pragma unroll
-      for (int s = 0; s < S; ++s)
+      for (int i = 0; i < NC; ++i)
 #pragma unroll
-        for (int i = 0; i < NC; ++i)
-          B.w[s][i] = *reinterpret_cast<const int4_t*>(
-              wbase + (size_t)(wrow[i] + (unsigned)(min(b * BLK + s * 4 + g, a.kch - 1) - g) * 16));
+        for (int q = 0; q < 2; ++q)
+          B.w[s + q][i] = __builtin_nontemporal_load(
+              reinterpret_cast<const int4_t*>(wbase + (size_t)(wrow[i][q] + c)));
     }
     if constexpr (!FUSED) {
 #pragma unroll
@@ -396,20 +410,26 @@ __global__ __launch_bounds__(SK_W * 64, 4) void k_product_few(ProductArgs a) {
         load(B1, wave);
       }
 #pragma unroll
-      for (int s = 0; s < S; ++s) {
-        int4_t x[NR];
+      for (int s = 0; s < S; s += 2) {
+        int4_t w[2][NC];
 #pragma unroll
-        for (int j = 0; j < NR; ++j) {
-          if constexpr (FUSED)
-            x[j] = *reinterpret_cast<const int4_t*>(fx + b * (BLK * 16) + s * 64);
-          else
-            x[j] = B0.x[s][j];
+        for (int i = 0; i < NC; ++i) to_steps(B0.w[s][i], B0.w[s + 1][i], w[0][i], w[1][i]);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          int4_t x[NR];
+#pragma unroll
+          for (int j = 0; j < NR; ++j) {
+            if constexpr (FUSED)
+              x[j] = *reinterpret_cast<const int4_t*>(fx + b * (BLK * 16) + (s + h) * 64);
+            else
+              x[j] = B0.x[s + h][j];
+          }
+#pragma unroll
+          for (int i = 0; i < NC; ++i)
+#pragma unroll
+            for (int j = 0; j < NR; ++j)
+              acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[h][i], x[j], acc[i][j], 0, 0, 0);
         }
-#pragma unroll
-        for (int i = 0; i < NC; ++i)
-#pragma unroll
-          for (int j = 0; j < NR; ++j)
-            acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(B0.w[s][i], x[j], acc[i][j], 0, 0, 0);
       }
       B0 = B1;
     }
@@ -486,12 +506,16 @@ __global__ __launch_bounds__(TD_W * 64) void k_token_down(ProductArgs a, const f
   const int nnt = (a.n + 15) / 16;
   int4_t w0[4], w1[4];
   auto load = [&](int4_t* w, int nt, int u) {
-    const int row = min(nt * 16 + r16, a.n - 1);
-    const int8_t* p = a.w + (size_t)s_e[u / nb] * a.w_group + (size_t)row * a.ldw;
+    const int8_t* p = a.w + (size_t)__builtin_amdgcn_readfirstlane(s_e[u / nb]) * a.w_group +
+                      (size_t)(nt * 16) * a.ldw;
+    const int rows = a.n - 1 - nt * 16;
 #pragma unroll
-    for (int s = 0; s < 4; ++s)
+    for (int s = 0; s < 4; ++s) {  // 8 rows x 128 bytes each (see to_steps)
+      const int row = min((r16 & 7) + 8 * (s & 1), rows);
+      const int c = min((u % nb) * SK_BLK + (s >> 1) * 8 + g + 4 * (r16 >> 3), a.kch - 1);
       w[s] = __builtin_nontemporal_load(reinterpret_cast<const int4_t*>(
-          p + (size_t)min((u % nb) * SK_BLK + s * 4 + g, a.kch - 1) * 16));
+          p + (size_t)((unsigned)row * (unsigned)a.ldw + (unsigned)c * 16)));
+    }
   };
   int nt = blockIdx.x;
   if (wave < units && nt < nnt) load(w0, nt, wave);
@@ -525,9 +549,14 @@ __global__ __launch_bounds__(TD_W * 64) void k_token_down(ProductArgs a, const f
       else if (nn < nnt) load(w1, nn, wave);
       const int8_t* f = s_h + u * (SK_BLK * 16) + g * 16;  // slot u / nb, block u % nb
 #pragma unroll
-      for (int s = 0; s < 4; ++s)
-        acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(w0[s], *reinterpret_cast<const int4_t*>(f + s * 64),
-                                                    acc, 0, 0, 0);
+      for (int s = 0; s < 4; s += 2) {
+        int4_t m[2];
+        to_steps(w0[s], w0[s + 1], m[0], m[1]);
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(
+              m[h], *reinterpret_cast<const int4_t*>(f + (s + h) * 64), acc, 0, 0, 0);
+      }
       if (u + TD_W >= units || (u + TD_W) / nb != u / nb) {
         if (r16 == 0) {
 #pragma unroll
