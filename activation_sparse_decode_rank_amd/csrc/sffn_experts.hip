@@ -121,6 +121,8 @@ hipError_t run_token(const ExpertsArgs& a, const void* x, int x_type, const int3
   up.ldo = (int64_t)c.ldh;
   up.src = idx;
   up.k = k;
+  // act_tiles(f) words a slot: less than the slot's row in 8 bits, which this path does not use
+  up.tile_max = reinterpret_cast<unsigned*>(work + c.hq);
   const hipError_t e =
       launch_product_fused(up, x_type, a.gated ? MODE_ACT_GATED : MODE_ACT, s);
   if (e != hipSuccess) return e;
@@ -131,6 +133,8 @@ hipError_t run_token(const ExpertsArgs& a, const void* x, int x_type, const int3
   dn.out_type = y_type;
   dn.src = idx;
   dn.k = k;
+  dn.tile_max = up.tile_max;
+  dn.max_tiles = act_tiles(a.f, a.gated);
   return launch_token_down(dn, weights, s);
 }
 

@@ -56,6 +56,7 @@ struct ProductArgs {
   const int32_t* n_tiles;
   const int32_t* src;     // [sorted row] slot t * k + s it stands for
   int max_tiles;
+  unsigned* tile_max;     // fused ACT forms: bits of the largest |h| of each (slot, tile)
   int k;                  // slots of a token: row src's token is src / k
   int experts;
   int64_t w_group;        // bytes from an expert's w to the next one's
@@ -66,7 +67,8 @@ hipError_t launch_product(const ProductArgs& a, ProductMode mode, hipStream_t s)
 // rows. ACT, ACT_GATED: one token, a.src is its idx [k] and slot s gives row s of out.
 hipError_t launch_product_fused(const ProductArgs& a, int x_type, ProductMode mode, hipStream_t s);
 // One token's down products and their weighted sum: a.x holds fp32 rows h (a.cols values, a.ldx
-// apart), a.src the token's idx [k], a.out the token's output row (host::token_fused).
+// apart), a.tile_max the a.max_tiles maxima of each that the launch before left, a.src the token's idx [k], a.out the token's output row (host::token_fused).
+int act_tiles(int f, bool gated);  // tiles of one slot in the fused ACT forms
 hipError_t launch_token_down(const ProductArgs& a, const float* weights, hipStream_t s);
 
 // x already in 8 bits, rows copied to zero-padded rows of kpad bytes

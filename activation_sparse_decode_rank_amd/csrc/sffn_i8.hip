@@ -171,10 +171,12 @@ __device__ __forceinline__ void store4(void* p, size_t i, const float4_t& v, int
 
 // What becomes of the sums of sorted row (or row) r at channels (neurons) c .. c + 3 of expert
 // e: v, and in the gated form u of the up rows. xs: the scale of the row of x behind r.
+// Returns the largest |h|'s bits (ACT forms).
 template <int MODE>
-__device__ __forceinline__ void emit(const ProductArgs& a, int e, int r, float xs, int c,
+__device__ __forceinline__ unsigned emit(const ProductArgs& a, int e, int r, float xs, int c,
                                      const int4_t& v, const int4_t& u) {
-  if (c >= a.n) return;
+  if (c >= a.n) return 0;
+  unsigned big = 0;
   const int left = a.n - c;
   const bool whole = left >= 4 && a.vec_out;
   float4_t y;
@@ -190,6 +192,7 @@ __device__ __forceinline__ void emit(const ProductArgs& a, int e, int r, float x
       h = h < 0.0 ? 0.0 : h;  // NaN stays
       if (M == 2) h *= (double)u[j] * ((double)xs * (double)ws[M * j + 1]);
       y[j] = (float)h;
+      big = max(big, mag(y[j]));
     }
     store4<float>(a.out, (size_t)r * a.ldo + c, y, left, whole);
   } else {
@@ -209,6 +212,7 @@ __device__ __forceinline__ void emit(const ProductArgs& a, int e, int r, float x
       else store4<__bf16>(a.out, o, y, left, whole);
     }
   }
+  return big;
 }
 
 // The rows that tile mt stands for: [r0, r1) of expert e; false: no such tile.
@@ -256,45 +260,88 @@ __device__ __forceinline__ void to_steps(const int4_t& a, const int4_t& b, int4_
 }
 
 // Few rows: the weights are streamed from memory once, straight into the matrix cores'
-// registers. A workgroup of 8 waves takes tiles of 16 NC channels (gated: 8 NC neurons, gate and
-// up rows in 16-row tiles 2 i and 2 i + 1) and up to 16 NR rows; its waves take blocks of 256
-// bytes (128 where x comes from the caches: registers) of the length in turn and add their sums through LDS at
-// the end of a tile, whole numbers, so the split changes nothing. The next block's loads, also
-// those of the next tile, are issued before the current block's products, so that the stream
-// does not stop at a tile's end.
-// X = void: x is in 8 bits and comes from the caches. Otherwise x is X's rows, which each
-// workgroup first holds in 8 bits in its own LDS: that costs less than a launch before this one
-// while the rows are few.
-constexpr int SK_W = 8;          // waves
+// registers. SK waves take a tile of 16 rows of w (16 channels; gated: the gate rows, then the up
+// rows of 8 neurons) and up to 16 NR rows of x, one block of 256 bytes of the length after the
+// other in turn. Two blocks ahead of the products, also across the end of a tile, are always in
+// flight. With enough tiles one wave does a tile alone (SK = 1) and meets nobody; otherwise the
+// sums of the workgroup's W = SK waves are added through LDS, whole numbers, so the split
+// changes nothing.
+// X = void: x is in 8 bits and comes from the caches. Otherwise x is X's rows (at most
+// host::kFusedRows), which each workgroup first holds in 8 bits in its own LDS while its first
+// weights are on their way: that costs less than a launch before this one.
+constexpr int F_BLK = 16;  // 16-byte chunks of a block
 
-// row `row` of x (X's, cols values) into 8 bits at s_q [kpad], by all W waves; its scale
+// M rows of x (X's, cols values) into 8 bits in LDS, by all W waves: W / M waves take a row.
+// load() only issues the reads (before the weights', whose wait would include theirs).
 template <typename X, int W>
-__device__ __forceinline__ float quantize_to_lds(const X* x, int cols, int kpad, int8_t* s_q,
-                                                 unsigned* s_max) {
-  unsigned m = 0;
-  for (int i = threadIdx.x; i < kpad / 4; i += W * 64) {
-    const float4_t v = load4<X, true>(x, i, cols);
+struct RowsToLds {
+  static constexpr int KEEP = 6;  // groups of four values per thread that stay in registers
+  const X* xr;
+  int row, i0, step, nq, cols, M;
+  bool kept;
+  float4_t v[KEEP];
+  __device__ __forceinline__ void load(const X* x, int64_t ldx, int rows, int n, int kpad) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int per = W / rows;
+    M = rows;
+    cols = n;
+    row = wave / per;
+    i0 = (wave % per) * 64 + lane;
+    step = per * 64;
+    nq = kpad / 4;
+    xr = x + (size_t)min(row, M - 1) * ldx;
+    kept = nq <= KEEP * step;
+    if (kept && row < M) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) m = max(m, mag(v[e]));
+      for (int u = 0; u < KEEP; ++u) v[u] = load4<X, true>(xr, i0 + u * step, cols);
+    }
   }
-  m = wg_max<W>(m, s_max);
-  float r;
-  const float s = row_scale(m, r);
-  for (int i = threadIdx.x; i < kpad / 4; i += W * 64)
-    reinterpret_cast<int*>(s_q)[i] = s > 0.f ? quantize4(load4<X, true>(x, i, cols), s, r) : 0;
-  return s;
-}
+  // s_q [M][kpad]; s_max: M cleared words; returns the scale of row lane % 16 (row 0 past the last)
+  __device__ __forceinline__ float finish(int kpad, int8_t* s_q, unsigned* s_max) {
+    const int lane = threadIdx.x & 63;
+    float r;
+    if (row < M) {
+      unsigned m = 0;
+      if (kept) {
+#pragma unroll
+        for (int u = 0; u < KEEP; ++u)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) m = max(m, mag(v[u][e]));
+      } else {
+        for (int i = i0; i < nq; i += step) {
+          const float4_t t = load4<X, true>(xr, i, cols);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) m = max(m, mag(t[e]));
+        }
+      }
+      for (int o = 32; o; o >>= 1) m = max(m, (unsigned)__shfl_xor((int)m, o));
+      if (lane == 0) atomicMax(&s_max[row], m);
+    }
+    lds_barrier();
+    if (row < M) {
+      const float s = row_scale(s_max[row], r);
+      int* q = reinterpret_cast<int*>(s_q + (size_t)row * kpad);
+      if (kept) {
+#pragma unroll
+        for (int u = 0; u < KEEP; ++u)
+          if (i0 + u * step < nq) q[i0 + u * step] = s > 0.f ? quantize4(v[u], s, r) : 0;
+      } else {
+        for (int i = i0; i < nq; i += step)
+          q[i] = s > 0.f ? quantize4(load4<X, true>(xr, i, cols), s, r) : 0;
+      }
+    }
+    return row_scale(s_max[(lane & 15) < M ? lane & 15 : 0], r);
+  }
+};
 
-template <int MODE, int NC, int NR, typename X>
-__global__ __launch_bounds__(SK_W * 64, 4) void k_product_few(ProductArgs a) {
-  // steps of 64 bytes in a block: as many as keep two workgroups' registers on a compute unit
-  constexpr int S = std::is_void<X>::value ? 2 : 4;
-  constexpr int BLK = S * 4;  // 16-byte chunks of a block
+template <int MODE, int NR, typename X, int W, int SK>
+__global__ __launch_bounds__(W * 64, NR == 1 || W > 8 ? 4 : 2) void k_product_few(ProductArgs a) {
+  static_assert(SK == 1 || SK == W, "a wave alone or the whole workgroup");
   constexpr bool G = MODE == MODE_ACT_GATED;
   constexpr bool FUSED = !std::is_void<X>::value;
-  constexpr int NT = G ? 8 * NC : 16 * NC;
-  __shared__ int s_sum[2][NC * NR][4][64];  // [tile parity][16 x 16 tile][channel][lane]
-  __shared__ unsigned s_max[SK_W];
+  constexpr int NT = G ? 8 : 16;  // channels (neurons) of a tile
+  __shared__ int s_sum[SK > 1 ? 2 : 1][SK > 1 ? NR : 1][4][64];  // [tile parity][16 rows of x][channel][lane]
+  __shared__ unsigned s_max[host::kFusedRows];
   extern __shared__ __attribute__((aligned(16))) int8_t s_x[];  // FUSED: rows of kpad bytes
   const int nnt = (a.n + NT - 1) / NT;
   const int nmt = FUSED ? (MODE == MODE_LINEAR ? 1 : a.k)
@@ -304,8 +351,11 @@ __global__ __launch_bounds__(SK_W * 64, 4) void k_product_few(ProductArgs a) {
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r16 = lane & 15, g = lane >> 4;
   const int nw = G ? 2 * a.n : a.n;
-  const int nb = (a.kch + BLK - 1) / BLK;
-  const int kpad = nb * BLK * 16;  // FUSED: bytes of a row in LDS
+  const int nb = (a.kch + F_BLK - 1) / F_BLK;
+  const int kpad = nb * F_BLK * 16;  // FUSED: bytes of a row in LDS
+  const int wk = SK > 1 ? wave : 0;
+  const int first = SK > 1 ? blockIdx.x : blockIdx.x * W + wave;
+  const int step = SK > 1 ? gridDim.x : gridDim.x * W;
 
   struct Tile {
     int id, e, r0, r1, n0;
@@ -313,10 +363,10 @@ __global__ __launch_bounds__(SK_W * 64, 4) void k_product_few(ProductArgs a) {
   // the first tile from id on (in steps of the grid) that has rows; its id is >= total if none
   auto tile_from = [&](int id) {
     Tile t{id, 0, 0, 0, 0};
-    for (; t.id < total; t.id += gridDim.x) {
+    for (; t.id < total; t.id += step) {
       const int mt = t.id / nnt;
       t.n0 = (t.id % nnt) * NT;
-      if (FUSED && MODE != MODE_LINEAR) {  // one token: tile row mt is its slot
+      if (FUSED && MODE != MODE_LINEAR) {  // one token: row mt is its slot
         t.e = a.src[mt];
         t.r0 = mt;
         t.r1 = mt + 1;
@@ -329,254 +379,317 @@ __global__ __launch_bounds__(SK_W * 64, 4) void k_product_few(ProductArgs a) {
     }
     return t;
   };
+  // the stream: next block (tile, block of it) to load
   const int lc = g + 4 * (r16 >> 3);  // chunk of 128 bytes that this lane loads
-  const int8_t* wbase = nullptr;  // first row of the tile, one for all lanes
-  unsigned wrow[NC][2];           // this lane's two rows of each 16 from there, in bytes
-  const int8_t* px[NR];
-  auto aim = [&](const Tile& t) {
-    const int first = G ? 2 * t.n0 : t.n0;
-    wbase = a.w + (size_t)t.e * a.w_group + (size_t)first * a.ldw;
+  Tile ft = tile_from(first);
+  int fb = wk;
+  const int8_t* wbase = nullptr;  // first row of that tile, one for all lanes
+  unsigned wrow[2];               // this lane's two rows from there, in bytes
+  auto aim = [&]() {
+    const int row0 = G ? 2 * ft.n0 : ft.n0;
+    wbase = a.w + (size_t)ft.e * a.w_group + (size_t)row0 * a.ldw;
 #pragma unroll
-    for (int i = 0; i < NC; ++i) {
-#pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        const int r = (r16 & 7) + 8 * q;
-        const int row = G ? (i >> 1) * 32 + 2 * r + (i & 1) : i * 16 + r;
-        wrow[i][q] = (unsigned)min(row, nw - 1 - first) * (unsigned)a.ldw;
-      }
-    }
-    if constexpr (!FUSED) {
-#pragma unroll
-      for (int j = 0; j < NR; ++j)
-        px[j] = a.x + (size_t)row_of_x<MODE>(a, min(t.r0 + j * 16 + r16, t.r1 - 1)) * a.ldx + g * 16;
+    for (int q = 0; q < 2; ++q) {
+      const int row = G ? 2 * (r16 & 7) + q : (r16 & 7) + 8 * q;
+      wrow[q] = (unsigned)min(row, nw - 1 - row0) * (unsigned)a.ldw;
     }
   };
   struct Block {
-    int4_t w[S][NC], x[FUSED ? 1 : S][NR];
+    int4_t w[4];
   };
-  auto load = [&](Block& B, int b) {
-    const unsigned o = (unsigned)b * (BLK * 16);
+  auto fetch = [&](Block& B) {
+    if (ft.id >= total) return;
 #pragma unroll
-    for (int s = 0; s < S; s += 2) {
+    for (int s = 0; s < 4; s += 2) {
       // past w's row x is zero (its rows are padded to whole blocks), so any chunk will do
-      const unsigned c = (unsigned)min(b * BLK + s * 4 + lc, a.kch - 1) * 16;
+      const unsigned c = (unsigned)min(fb * F_BLK + s * 4 + lc, a.kch - 1) * 16;
 #pragma unroll
-      for (int i = 0; i < NC; ++i)
-#pragma unroll
-        for (int q = 0; q < 2; ++q)
-          B.w[s + q][i] = __builtin_nontemporal_load(
-              reinterpret_cast<const int4_t*>(wbase + (size_t)(wrow[i][q] + c)));
+      for (int q = 0; q < 2; ++q)
+        B.w[s + q] = __builtin_nontemporal_load(
+            reinterpret_cast<const int4_t*>(wbase + (size_t)(wrow[q] + c)));
     }
-    if constexpr (!FUSED) {
-#pragma unroll
-      for (int s = 0; s < S; ++s)
-#pragma unroll
-        for (int j = 0; j < NR; ++j)
-          B.x[s][j] = *reinterpret_cast<const int4_t*>(px[j] + (size_t)o + s * 64);
+    fb += SK;
+    if (fb >= nb) {
+      fb = wk;
+      ft = tile_from(ft.id + step);
+      if (ft.id < total) aim();
     }
   };
-  Tile t = tile_from(blockIdx.x);
-  if (t.id >= total) return;
-  Block B0, B1;
-  if (wave < nb) {
-    aim(t);
-    load(B0, wave);
-  }
-  for (int i = tid; i < 2 * NC * NR * 256; i += SK_W * 64) (&s_sum[0][0][0][0])[i] = 0;
+  Tile t = ft;
+  if (SK > 1 && t.id >= total) return;
   const int rows_x = MODE == MODE_LINEAR ? a.rows : 1;
-  float xs_own = 0.f;
-  if constexpr (FUSED) {
-    for (int m = 0; m < rows_x; ++m) {
-      const float s = quantize_to_lds<X, SK_W>(reinterpret_cast<const X*>(a.x) + (size_t)m * a.ldx,
-                                               a.cols, kpad, s_x + m * kpad,
-                                               s_max);
-      if (m == r16 || MODE != MODE_LINEAR) xs_own = s;
-    }
+  typedef typename std::conditional<FUSED, X, float>::type XT;
+  RowsToLds<XT, W> own;
+  if constexpr (FUSED) own.load(reinterpret_cast<const XT*>(a.x), a.ldx, rows_x, a.cols, kpad);
+  Block B0, B1, B2;
+  if (wk < nb && t.id < total) {
+    aim();
+    fetch(B0);
+    fetch(B1);
   }
-  lds_barrier();
+  float xs_own = 0.f;
+  if constexpr (SK > 1)
+    for (int i = tid; i < 2 * NR * 256; i += W * 64) (&s_sum[0][0][0][0])[i] = 0;
+  if constexpr (FUSED) {
+    if (tid < host::kFusedRows) s_max[tid] = 0;
+    lds_barrier();
+    xs_own = own.finish(kpad, s_x, s_max);
+  }
+  if (SK > 1 || FUSED) lds_barrier();
   const int8_t* fx = s_x + (MODE == MODE_LINEAR ? min(r16, rows_x - 1) : 0) * kpad + g * 16;
   for (int par = 0; t.id < total; par ^= 1) {
-    const Tile next = tile_from(t.id + gridDim.x);
-    int4_t acc[NC][NR];
+    const int8_t* px[NR];
+    float xs[NR];
 #pragma unroll
-    for (int i = 0; i < NC; ++i)
-#pragma unroll
-      for (int j = 0; j < NR; ++j) acc[i][j] = int4_t{0, 0, 0, 0};
-    for (int b = wave; b < nb; b += SK_W) {
-      if (b + SK_W < nb) {
-        load(B1, b + SK_W);
-      } else if (next.id < total) {
-        aim(next);
-        load(B1, wave);
+    for (int j = 0; j < NR; ++j) {
+      if constexpr (FUSED) {
+        xs[j] = xs_own;
+      } else {
+        const int xr = row_of_x<MODE>(a, min(t.r0 + j * 16 + r16, t.r1 - 1));
+        px[j] = a.x + (size_t)xr * a.ldx + g * 16;
+        xs[j] = a.xs[xr];
       }
+    }
+    int4_t acc[NR];
 #pragma unroll
-      for (int s = 0; s < S; s += 2) {
-        int4_t w[2][NC];
+    for (int j = 0; j < NR; ++j) acc[j] = int4_t{0, 0, 0, 0};
+    // x one block ahead: its loads are then older than those of the weights two blocks ahead,
+    // which a wait for it leaves in flight
+    struct Rows {
+      int4_t x[4][NR];
+    };
+    auto rows_of = [&](Rows& R, int b) {
 #pragma unroll
-        for (int i = 0; i < NC; ++i) to_steps(B0.w[s][i], B0.w[s + 1][i], w[0][i], w[1][i]);
+      for (int s = 0; s < 4; ++s)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          int4_t x[NR];
-#pragma unroll
-          for (int j = 0; j < NR; ++j) {
-            if constexpr (FUSED)
-              x[j] = *reinterpret_cast<const int4_t*>(fx + b * (BLK * 16) + (s + h) * 64);
-            else
-              x[j] = B0.x[s + h][j];
+        for (int j = 0; j < NR; ++j) {
+          if constexpr (FUSED) {
+            R.x[s][j] = *reinterpret_cast<const int4_t*>(fx + b * (F_BLK * 16) + s * 64);
+          } else {
+            // rows of x are read up to 128 bytes past a.kch only where they have them
+            const int c = b * F_BLK + s * 4;
+            R.x[s][j] = c < a.kch ? *reinterpret_cast<const int4_t*>(px[j] + (size_t)c * 16)
+                                  : int4_t{0, 0, 0, 0};
           }
-#pragma unroll
-          for (int i = 0; i < NC; ++i)
-#pragma unroll
-            for (int j = 0; j < NR; ++j)
-              acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[h][i], x[j], acc[i][j], 0, 0, 0);
         }
+    };
+    Rows X0, X1;
+    if (wk < nb && !FUSED) rows_of(X0, wk);
+    for (int b = wk; b < nb; b += SK) {
+      if (FUSED) rows_of(X0, b);
+      else if (b + SK < nb) rows_of(X1, b + SK);
+      fetch(B2);
+#pragma unroll
+      for (int s = 0; s < 4; s += 2) {
+        int4_t w[2];
+        to_steps(B0.w[s], B0.w[s + 1], w[0], w[1]);
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int j = 0; j < NR; ++j)
+            acc[j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[h], X0.x[s + h][j], acc[j], 0, 0, 0);
       }
       B0 = B1;
+      B1 = B2;
+      if (!FUSED) X0 = X1;
     }
-    if (wave < nb) {
+    // rows 16 j .. +15 of the tile; lane: row r16, channels 4 g .. +3 (gated: lanes of g 2 and 3
+    // hold the up sums of those of g 0 and 1)
+    auto finish = [&](int j, float xs_j, const int4_t& v, const int4_t& u) {
+      const int r = t.r0 + j * 16 + r16;
+      unsigned big = 0;
+      if (r < t.r1 && (!G || lane < 32)) big = emit<MODE>(a, t.e, r, xs_j, t.n0 + 4 * g, v, u);
+      if (FUSED && MODE != MODE_LINEAR) {  // the largest |h| of the tile, for the down product
+        for (int o = 16; o <= 32; o <<= 1) big = max(big, (unsigned)__shfl_xor((int)big, o));
+        if (lane == 0) a.tile_max[t.r0 * nnt + t.n0 / NT] = big;
+      }
+    };
+    if constexpr (SK == 1) {
 #pragma unroll
-      for (int i = 0; i < NC; ++i)
+      for (int j = 0; j < NR; ++j) {
+        int4_t u = {0, 0, 0, 0};
+        if (G) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) u[c] = __shfl_xor(acc[j][c], 32);
+        }
+        finish(j, xs[j], acc[j], u);
+      }
+    } else {
+      if (wk < nb) {
 #pragma unroll
         for (int j = 0; j < NR; ++j)
 #pragma unroll
-          for (int c = 0; c < 4; ++c) atomicAdd(&s_sum[par][i * NR + j][c][lane], acc[i][j][c]);
-    }
-    // The sums of the tile two before this one were read and cleared before this wave's
-    // arrival here, and the other parity's are free to be added to after it.
-    lds_barrier();
-    auto take = [&](int q) {
-      int4_t v;
+          for (int c = 0; c < 4; ++c) atomicAdd(&s_sum[par][j][c][lane], acc[j][c]);
+      }
+      // The sums of the tile two before this one were read and cleared before their reader's
+      // arrival here, and the other parity's are free to be added to after it.
+      lds_barrier();
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        v[c] = s_sum[par][q][c][lane];
-        s_sum[par][q][c][lane] = 0;
+      for (int j = 0; j < NR; ++j) {
+        if (wave != j) continue;
+        int4_t v, u = {0, 0, 0, 0};
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          v[c] = s_sum[par][j][c][lane];
+          if (G) u[c] = s_sum[par][j][c][lane ^ 32];
+        }
+        wave_lds_sync();  // another lane reads what this one clears
+#pragma unroll
+        for (int c = 0; c < 4; ++c) s_sum[par][j][c][lane] = 0;
+        finish(j, xs[j], v, u);
       }
-      return v;
-    };
-    // wave w: tiles w, w + 8, ... (gated: pairs of tiles); lane: row r16, channels 4 g .. +3
-    for (int q = wave; q < (G ? NC / 2 : NC) * NR; q += SK_W) {
-      const int i = q / NR, j = q % NR;
-      const int r = t.r0 + j * 16 + r16;
-      int4_t v, u = {0, 0, 0, 0};
-      if (G) {
-        v = take(2 * i * NR + j);
-        u = take((2 * i + 1) * NR + j);
-      } else {
-        v = take(q);
-      }
-      if (r >= t.r1) continue;
-      const float xs = FUSED ? xs_own : a.xs[row_of_x<MODE>(a, r)];
-      emit<MODE>(a, t.e, r, xs, t.n0 + i * 16 + 4 * g, v, u);
     }
-    t = next;
+    t = tile_from(t.id + step);
   }
 }
 
 // The down product of one token, with everything around it: each workgroup holds the rows h of
-// the token's slots in 8 bits in its LDS, 16 waves take blocks of 256 bytes of all slots'
-// lengths in turn for 16 channels of every slot's expert, and the weighted sum over the slots,
-// in slot order, is the token's output. Sums of one slot meet in LDS by whole-number adds.
+// the token's slots in 8 bits in its LDS (the scales from the tiles' maxima that the launch
+// before left), 16 waves take blocks of 256 bytes of all slots' lengths in turn for 16 channels
+// of every slot's expert, and the weighted sum over the slots, in slot order, is the token's
+// output. Sums of one slot meet in LDS by whole-number adds. The reads of h go before the
+// weights', whose wait would include theirs.
 constexpr int TD_W = 16;
-constexpr int SK_BLK = 16;       // 16-byte chunks of a block
 
 __global__ __launch_bounds__(TD_W * 64) void k_token_down(ProductArgs a, const float* __restrict__ weights) {
+  constexpr int TH = TD_W * 64;
+  constexpr int KEEP = 8;           // groups of four values of h per thread that stay in registers
   __shared__ int s_sum[2][64][16];  // [tile parity][slot][channel]
-  __shared__ float s_hs[64];
   __shared__ int s_e[64];           // expert of the v-th slot that has one, and its slot
   __shared__ int s_slot[64];
-  __shared__ unsigned s_max[64];
+  __shared__ float s_w[64];         // its weight
+  __shared__ unsigned s_max[64];    // by slot
   extern __shared__ __attribute__((aligned(16))) int8_t s_h[];  // [slots][kpad]
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r16 = lane & 15, g = lane >> 4;
-  const int nb = (a.kch + SK_BLK - 1) / SK_BLK, kpad = nb * SK_BLK * 16;
-  // every wave lists the slots that have an expert
+  const int nb = (a.kch + F_BLK - 1) / F_BLK, kpad = nb * F_BLK * 16, nq = kpad / 4;
+  const float* h = reinterpret_cast<const float*>(a.x);
   const int my = lane < a.k ? a.src[lane] : -1;
+  const float my_w = lane < a.k ? weights[lane] : 0.f;
+  const int groups = a.k * nq;
+  const bool kept = groups <= KEEP * TH;
+  float4_t v[KEEP];
+  if (kept) {
+#pragma unroll
+    for (int u = 0; u < KEEP; ++u) {
+      const int i = tid + u * TH;
+      if (i < groups) v[u] = load4<float, true>(h + (size_t)(i / nq) * a.ldx, i % nq, a.cols);
+    }
+  }
+  unsigned most = 0;  // this wave's share of slot wave % k's maxima
+  const int ms = wave % a.k, mw = wave / a.k, mstep = ((TD_W - 1 - ms) / a.k + 1) * 64;
+  const bool shared = a.k <= TD_W;
+  if (shared) {
+#pragma unroll 4
+    for (int i = mw * 64 + lane; i < a.max_tiles; i += mstep)
+      most = max(most, a.tile_max[ms * a.max_tiles + i]);
+  }
+  // every wave lists the slots that have an expert
   const uint64_t on = __ballot((unsigned)my < (unsigned)a.experts);
   const int nv = __popcll(on);
-  if (wave == 0 && ((on >> lane) & 1)) {
-    const int v = __popcll(on & ((1ull << lane) - 1));
-    s_e[v] = my;
-    s_slot[v] = lane;
+  if (wave == 0) {
+    if ((on >> lane) & 1) {
+      const int n = __popcll(on & ((1ull << lane) - 1));
+      s_e[n] = my;
+      s_slot[n] = lane;
+      s_w[n] = my_w;
+    }
+    s_max[lane] = 0;
   }
-  if (tid < 64) s_max[tid] = 0;
-  for (int i = tid; i < 2 * 64 * 16; i += TD_W * 64) (&s_sum[0][0][0])[i] = 0;
+  for (int i = tid; i < 2 * 64 * 16; i += TH) (&s_sum[0][0][0])[i] = 0;
   lds_barrier();
   const int units = nv * nb;
   const int nnt = (a.n + 15) / 16;
-  int4_t w0[4], w1[4];
-  auto load = [&](int4_t* w, int nt, int u) {
-    const int8_t* p = a.w + (size_t)__builtin_amdgcn_readfirstlane(s_e[u / nb]) * a.w_group +
-                      (size_t)(nt * 16) * a.ldw;
-    const int rows = a.n - 1 - nt * 16;
+  int4_t w0[4], w1[4], w2[4];
+  // the stream: two units (blocks of all slots' lengths) ahead of the products
+  int nt = blockIdx.x, fnt = nt, fu = wave;
+  auto fetch = [&](int4_t* w) {
+    if (fnt >= nnt || fu >= units) return;
+    const int8_t* p = a.w + (size_t)__builtin_amdgcn_readfirstlane(s_e[fu / nb]) * a.w_group +
+                      (size_t)(fnt * 16) * a.ldw;
+    const int rows = a.n - 1 - fnt * 16;
 #pragma unroll
     for (int s = 0; s < 4; ++s) {  // 8 rows x 128 bytes each (see to_steps)
       const int row = min((r16 & 7) + 8 * (s & 1), rows);
-      const int c = min((u % nb) * SK_BLK + (s >> 1) * 8 + g + 4 * (r16 >> 3), a.kch - 1);
+      const int c = min((fu % nb) * F_BLK + (s >> 1) * 8 + g + 4 * (r16 >> 3), a.kch - 1);
       w[s] = __builtin_nontemporal_load(reinterpret_cast<const int4_t*>(
           p + (size_t)((unsigned)row * (unsigned)a.ldw + (unsigned)c * 16)));
     }
-  };
-  int nt = blockIdx.x;
-  if (wave < units && nt < nnt) load(w0, nt, wave);
-  // h into 8 bits: the slots' maxima, then the whole numbers
-  const float* h = reinterpret_cast<const float*>(a.x);
-  for (int v = 0; v < nv; ++v) {
-    unsigned m = 0;
-    for (int i = tid; i < kpad / 4; i += TD_W * 64) {
-      const float4_t t = load4<float, true>(h + (size_t)s_slot[v] * a.ldx, i, a.cols);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) m = max(m, mag(t[e]));
+    fu += TD_W;
+    if (fu >= units) {
+      fu = wave;
+      fnt += gridDim.x;
     }
-    for (int o = 32; o; o >>= 1) m = max(m, (unsigned)__shfl_xor((int)m, o));
-    if (lane == 0) atomicMax(&s_max[v], m);
+  };
+  fetch(w0);
+  fetch(w1);
+  if (shared) {
+    for (int o = 32; o; o >>= 1) most = max(most, (unsigned)__shfl_xor((int)most, o));
+    if (lane == 0) atomicMax(&s_max[ms], most);
+  } else {
+    for (int s = wave; s < a.k; s += TD_W) {
+      for (int i = lane; i < a.max_tiles; i += 64) most = max(most, a.tile_max[s * a.max_tiles + i]);
+      for (int o = 32; o; o >>= 1) most = max(most, (unsigned)__shfl_xor((int)most, o));
+      if (lane == 0) s_max[s] = most;
+      most = 0;
+    }
   }
   lds_barrier();
-  for (int v = 0; v < nv; ++v) {
+  // slots without an expert have no maximum, and no unit reads their rows
+  auto put = [&](int i, const float4_t& x) {
     float r;
-    const float s = row_scale(s_max[v], r);
-    if (tid == 0) s_hs[v] = s;
-    for (int i = tid; i < kpad / 4; i += TD_W * 64)
-      reinterpret_cast<int*>(s_h + v * kpad)[i] =
-          s > 0.f ? quantize4(load4<float, true>(h + (size_t)s_slot[v] * a.ldx, i, a.cols), s, r) : 0;
+    const float s = row_scale(s_max[i / nq], r);
+    reinterpret_cast<int*>(s_h)[i] = s > 0.f ? quantize4(x, s, r) : 0;
+  };
+  if (kept) {
+#pragma unroll
+    for (int u = 0; u < KEEP; ++u)
+      if (tid + u * TH < groups) put(tid + u * TH, v[u]);
+  } else {
+    for (int i = tid; i < groups; i += TH)
+      put(i, load4<float, true>(h + (size_t)(i / nq) * a.ldx, i % nq, a.cols));
   }
   lds_barrier();
   for (int par = 0; nt < nnt; nt += gridDim.x, par ^= 1) {
-    const int nn = nt + gridDim.x;
     int4_t acc = {0, 0, 0, 0};
     for (int u = wave; u < units; u += TD_W) {
-      if (u + TD_W < units) load(w1, nt, u + TD_W);
-      else if (nn < nnt) load(w1, nn, wave);
-      const int8_t* f = s_h + u * (SK_BLK * 16) + g * 16;  // slot u / nb, block u % nb
+      fetch(w2);
+      const int n = u / nb;
+      const int8_t* f = s_h + (size_t)s_slot[n] * kpad + (u - n * nb) * (F_BLK * 16) + g * 16;
 #pragma unroll
       for (int s = 0; s < 4; s += 2) {
         int4_t m[2];
         to_steps(w0[s], w0[s + 1], m[0], m[1]);
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+        for (int q = 0; q < 2; ++q)
           acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(
-              m[h], *reinterpret_cast<const int4_t*>(f + (s + h) * 64), acc, 0, 0, 0);
+              m[q], *reinterpret_cast<const int4_t*>(f + (s + q) * 64), acc, 0, 0, 0);
       }
-      if (u + TD_W >= units || (u + TD_W) / nb != u / nb) {
+      if (u + TD_W >= units || (u + TD_W) / nb != n) {
         if (r16 == 0) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) atomicAdd(&s_sum[par][u / nb][4 * g + j], acc[j]);
+          for (int j = 0; j < 4; ++j) atomicAdd(&s_sum[par][n][4 * g + j], acc[j]);
         }
         acc = int4_t{0, 0, 0, 0};
       }
 #pragma unroll
-      for (int s = 0; s < 4; ++s) w0[s] = w1[s];
+      for (int s = 0; s < 4; ++s) {
+        w0[s] = w1[s];
+        w1[s] = w2[s];
+      }
     }
     lds_barrier();
     if (tid < 16) {
       const int c = nt * 16 + tid;
       float y = 0.f;
-      for (int v = 0; v < nv; ++v) {
-        const int sum = s_sum[par][v][tid];
-        s_sum[par][v][tid] = 0;
+      for (int n = 0; n < nv; ++n) {
+        const int sum = s_sum[par][n][tid];
+        s_sum[par][n][tid] = 0;
         if (c < a.n) {
-          const float p = (float)sum * (s_hs[v] * a.ws[(size_t)s_e[v] * a.n + c]);
-          y += weights[s_slot[v]] * p;
+          float r;
+          const float hs = row_scale(s_max[s_slot[n]], r);
+          y += s_w[n] * ((float)sum * (hs * a.ws[(size_t)s_e[n] * a.n + c]));
         }
       }
       if (c < a.n) {
@@ -748,13 +861,21 @@ int resident(K kernel, int threads, size_t lds) {
   return std::max(1, cus * per);
 }
 
-template <int MODE, int NC, int NR, typename X>
+template <int MODE, int NR, typename X, int W, int SK>
+void few_launch(const ProductArgs& a, int64_t tiles, size_t lds, hipStream_t s) {
+  const int64_t groups = SK == 1 ? (tiles + W - 1) / W : tiles;
+  const int at_once = resident(k_product_few<MODE, NR, X, W, SK>, W * 64, lds);
+  k_product_few<MODE, NR, X, W, SK>
+      <<<dim3((unsigned)std::min<int64_t>(groups, at_once)), dim3(W * 64), lds, s>>>(a);
+}
+// waves of a tile: one where the tiles give every compute unit ten, else four, else sixteen
+template <int MODE, int NR, typename X>
 void few_launch(const ProductArgs& a, int64_t row_tiles, size_t lds, hipStream_t s) {
-  constexpr int NT = MODE == MODE_ACT_GATED ? 8 * NC : 16 * NC;
+  constexpr int NT = MODE == MODE_ACT_GATED ? 8 : 16;
   const int64_t tiles = row_tiles * ((a.n + NT - 1) / NT);
-  const int at_once = resident(k_product_few<MODE, NC, NR, X>, SK_W * 64, lds);
-  k_product_few<MODE, NC, NR, X>
-      <<<dim3((unsigned)std::min<int64_t>(tiles, at_once)), dim3(SK_W * 64), lds, s>>>(a);
+  if (tiles >= 2560) few_launch<MODE, NR, X, 4, 1>(a, tiles, lds, s);
+  else if (tiles >= 512) few_launch<MODE, NR, X, 4, 4>(a, tiles, lds, s);
+  else few_launch<MODE, NR, X, NR == 1 ? 16 : 8, NR == 1 ? 16 : 8>(a, tiles, lds, s);
 }
 
 template <int MODE>
@@ -763,9 +884,9 @@ void product_launch(ProductArgs a, hipStream_t s) {
               reinterpret_cast<uintptr_t>(a.out) % (a.out_type == T_F32 ? 16 : 8) == 0;
   const int64_t tiles = MODE == MODE_LINEAR ? ((int64_t)a.rows + a.tile - 1) / a.tile : a.max_tiles;
   if (a.tile == 16) {
-    few_launch<MODE, MODE == MODE_ACT_GATED ? 2 : 1, 1, void>(a, tiles, 0, s);
+    few_launch<MODE, 1, void>(a, tiles, 0, s);
   } else if (a.tile == 32) {
-    few_launch<MODE, MODE == MODE_ACT_GATED ? 2 : 1, 2, void>(a, tiles, 0, s);
+    few_launch<MODE, 2, void>(a, tiles, 0, s);
   } else {
     constexpr int NT = MODE == MODE_ACT_GATED ? T_CH / 2 : T_CH;
     const dim3 grid((unsigned)((tiles * ((a.n + NT - 1) / NT) + 7) / 8 * 8)), block(T_W * 64);
@@ -797,7 +918,7 @@ void fused_launch(ProductArgs a, hipStream_t s) {
   a.vec_out = a.ldo % 4 == 0 &&
               reinterpret_cast<uintptr_t>(a.out) % (a.out_type == T_F32 ? 16 : 8) == 0;
   const size_t rows = MODE == MODE_LINEAR ? a.rows : 1;
-  few_launch<MODE, MODE == MODE_ACT_GATED ? 2 : 1, 1, X>(a, MODE == MODE_LINEAR ? 1 : a.k,
+  few_launch<MODE, 1, X>(a, MODE == MODE_LINEAR ? 1 : a.k,
                                                          rows * host::i8_kpad(a.cols), s);
 }
 
@@ -816,6 +937,8 @@ hipError_t launch_product_fused(const ProductArgs& a, int x_type, ProductMode mo
   else fused_launch<__bf16>(a, mode, s);
   return hipGetLastError();
 }
+
+int act_tiles(int f, bool gated) { return gated ? (f + 7) / 8 : (f + 15) / 16; }
 
 hipError_t launch_token_down(const ProductArgs& a, const float* weights, hipStream_t s) {
   const size_t lds = (size_t)a.k * host::i8_kpad(a.cols);
