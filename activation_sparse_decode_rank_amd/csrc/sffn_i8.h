@@ -45,6 +45,7 @@ struct ProductArgs {
   int n;               // channels (ACT_GATED: neurons, each of two rows of w)
   int kch;             // 16-byte chunks of a row
   int cols;            // values of a row of x (fused forms only)
+  unsigned div_nq, div_nb;  // set by launch_token_down
   void* out;
   int64_t ldo;         // elements
   int out_type;
@@ -69,7 +70,7 @@ hipError_t launch_product_fused(const ProductArgs& a, int x_type, ProductMode mo
 // One token's down products and their weighted sum: a.x holds fp32 rows h (a.cols values, a.ldx
 // apart), a.tile_max the a.max_tiles maxima of each that the launch before left, a.src the token's idx [k], a.out the token's output row (host::token_fused).
 int act_tiles(int f, bool gated);  // tiles of one slot in the fused ACT forms
-hipError_t launch_token_down(const ProductArgs& a, const float* weights, hipStream_t s);
+hipError_t launch_token_down(ProductArgs a, const float* weights, hipStream_t s);
 
 // x already in 8 bits, rows copied to zero-padded rows of kpad bytes
 hipError_t launch_pad_rows(const int8_t* x, int64_t ldx, int rows, int cols, int8_t* q, int kpad,

@@ -262,8 +262,9 @@ __device__ __forceinline__ void to_steps(const int4_t& a, const int4_t& b, int4_
 // Few rows: the weights are streamed from memory once, straight into the matrix cores'
 // registers. SK waves take a tile of 16 rows of w (16 channels; gated: the gate rows, then the up
 // rows of 8 neurons) and up to 16 NR rows of x, one block of 256 bytes of the length after the
-// other in turn. Two blocks ahead of the products, also across the end of a tile, are always in
-// flight. With enough tiles one wave does a tile alone (SK = 1) and meets nobody; otherwise the
+// other in turn. Three buffers of a block, its weights and its x, take turns: one is refilled,
+// with the block three ahead, also across the end of a tile, as soon as its products are issued
+// (and never copied: a copy would wait for the loads). With enough tiles one wave does a tile alone (SK = 1) and meets nobody; otherwise the
 // sums of the workgroup's W = SK waves are added through LDS, whole numbers, so the split
 // changes nothing.
 // X = void: x is in 8 bits and comes from the caches. Otherwise x is X's rows (at most
@@ -334,8 +335,12 @@ struct RowsToLds {
   }
 };
 
+// waves per SIMD that the registers of the three buffers leave
+template <int NR, typename X>
+constexpr int FEW_WAVES = std::is_void<X>::value ? (NR == 1 ? 3 : 2) : 4;
+
 template <int MODE, int NR, typename X, int W, int SK>
-__global__ __launch_bounds__(W * 64, NR == 1 || W > 8 ? 4 : 2) void k_product_few(ProductArgs a) {
+__global__ __launch_bounds__(W * 64, (FEW_WAVES<NR, X>)) void k_product_few(ProductArgs a) {
   static_assert(SK == 1 || SK == W, "a wave alone or the whole workgroup");
   constexpr bool G = MODE == MODE_ACT_GATED;
   constexpr bool FUSED = !std::is_void<X>::value;
@@ -379,12 +384,20 @@ __global__ __launch_bounds__(W * 64, NR == 1 || W > 8 ? 4 : 2) void k_product_fe
     }
     return t;
   };
+  // this lane's rows of x in a tile
+  auto rows_of = [&](const Tile& q, int (&row)[NR]) {
+#pragma unroll
+    for (int j = 0; j < NR; ++j)
+      row[j] = FUSED || q.id >= total ? 0 : row_of_x<MODE>(a, min(q.r0 + j * 16 + r16, q.r1 - 1));
+  };
   // the stream: next block (tile, block of it) to load
   const int lc = g + 4 * (r16 >> 3);  // chunk of 128 bytes that this lane loads
   Tile ft = tile_from(first);
   int fb = wk;
-  const int8_t* wbase = nullptr;  // first row of that tile, one for all lanes
+  const int8_t* wbase = nullptr;  // first row of w of that tile, one for all lanes
   unsigned wrow[2];               // this lane's two rows from there, in bytes
+  int frow[NR], fnext[NR];        // its rows of x, and those of the tile after it
+  Tile fn = tile_from(ft.id + step);
   auto aim = [&]() {
     const int row0 = G ? 2 * ft.n0 : ft.n0;
     wbase = a.w + (size_t)ft.e * a.w_group + (size_t)row0 * a.ldw;
@@ -395,7 +408,7 @@ __global__ __launch_bounds__(W * 64, NR == 1 || W > 8 ? 4 : 2) void k_product_fe
     }
   };
   struct Block {
-    int4_t w[4];
+    int4_t w[4], x[FUSED ? 1 : 4][NR];
   };
   auto fetch = [&](Block& B) {
     if (ft.id >= total) return;
@@ -408,102 +421,79 @@ __global__ __launch_bounds__(W * 64, NR == 1 || W > 8 ? 4 : 2) void k_product_fe
         B.w[s + q] = __builtin_nontemporal_load(
             reinterpret_cast<const int4_t*>(wbase + (size_t)(wrow[q] + c)));
     }
+    if constexpr (!FUSED) {
+#pragma unroll
+      for (int j = 0; j < NR; ++j) {
+        const int8_t* px = a.x + (size_t)frow[j] * a.ldx + g * 16;
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+          // x's rows are read up to a multiple of 128 bytes: steps past that repeat the last
+          const int c = min(fb * F_BLK + s * 4, (a.kch - 1) / 4 * 4);
+          B.x[s][j] = *reinterpret_cast<const int4_t*>(px + (size_t)c * 16);
+        }
+      }
+    }
     fb += SK;
     if (fb >= nb) {
       fb = wk;
-      ft = tile_from(ft.id + step);
-      if (ft.id < total) aim();
+      ft = fn;
+      if (ft.id < total) {
+        aim();
+        fn = tile_from(ft.id + step);
+#pragma unroll
+        for (int j = 0; j < NR; ++j) frow[j] = fnext[j];
+        rows_of(fn, fnext);
+      }
     }
   };
   Tile t = ft;
   if (SK > 1 && t.id >= total) return;
+  const bool works = wk < nb;  // a wave past the blocks of a row only meets the others
   const int rows_x = MODE == MODE_LINEAR ? a.rows : 1;
   typedef typename std::conditional<FUSED, X, float>::type XT;
   RowsToLds<XT, W> own;
   if constexpr (FUSED) own.load(reinterpret_cast<const XT*>(a.x), a.ldx, rows_x, a.cols, kpad);
-  Block B0, B1, B2;
-  if (wk < nb && t.id < total) {
-    aim();
-    fetch(B0);
-    fetch(B1);
+  const int8_t* fx = s_x + (MODE == MODE_LINEAR ? min(r16, rows_x - 1) : 0) * kpad + g * 16;
+  Block ring[3];
+  float xs[NR];
+  rows_of(ft, frow);
+  rows_of(fn, fnext);
+  if constexpr (!FUSED) {
+#pragma unroll
+    for (int j = 0; j < NR; ++j) xs[j] = t.id < total ? a.xs[frow[j]] : 0.f;
   }
-  float xs_own = 0.f;
+  if (works && t.id < total) {
+    aim();
+#pragma unroll
+    for (int i = 0; i < 3; ++i) fetch(ring[i]);
+  }
   if constexpr (SK > 1)
     for (int i = tid; i < 2 * NR * 256; i += W * 64) (&s_sum[0][0][0][0])[i] = 0;
   if constexpr (FUSED) {
     if (tid < host::kFusedRows) s_max[tid] = 0;
     lds_barrier();
-    xs_own = own.finish(kpad, s_x, s_max);
+    const float s = own.finish(kpad, s_x, s_max);
+#pragma unroll
+    for (int j = 0; j < NR; ++j) xs[j] = s;
   }
   if (SK > 1 || FUSED) lds_barrier();
-  const int8_t* fx = s_x + (MODE == MODE_LINEAR ? min(r16, rows_x - 1) : 0) * kpad + g * 16;
-  for (int par = 0; t.id < total; par ^= 1) {
-    const int8_t* px[NR];
-    float xs[NR];
+
+  int4_t acc[NR];
 #pragma unroll
-    for (int j = 0; j < NR; ++j) {
-      if constexpr (FUSED) {
-        xs[j] = xs_own;
-      } else {
-        const int xr = row_of_x<MODE>(a, min(t.r0 + j * 16 + r16, t.r1 - 1));
-        px[j] = a.x + (size_t)xr * a.ldx + g * 16;
-        xs[j] = a.xs[xr];
-      }
+  for (int j = 0; j < NR; ++j) acc[j] = int4_t{0, 0, 0, 0};
+  int b = wk, par = 0;
+  // rows 16 j .. +15 of the tile; lane: row r16, channels 4 g .. +3 (gated: lanes of g 2 and 3
+  // hold the up sums of those of g 0 and 1)
+  auto finish = [&](int j, float xs_j, const int4_t& v, const int4_t& u) {
+    const int r = t.r0 + j * 16 + r16;
+    unsigned big = 0;
+    if (r < t.r1 && (!G || lane < 32)) big = emit<MODE>(a, t.e, r, xs_j, t.n0 + 4 * g, v, u);
+    if (FUSED && MODE != MODE_LINEAR) {  // the largest |h| of the tile, for the down product
+      for (int o = 16; o <= 32; o <<= 1) big = max(big, (unsigned)__shfl_xor((int)big, o));
+      if (lane == 0) a.tile_max[t.r0 * nnt + t.n0 / NT] = big;
     }
-    int4_t acc[NR];
-#pragma unroll
-    for (int j = 0; j < NR; ++j) acc[j] = int4_t{0, 0, 0, 0};
-    // x one block ahead: its loads are then older than those of the weights two blocks ahead,
-    // which a wait for it leaves in flight
-    struct Rows {
-      int4_t x[4][NR];
-    };
-    auto rows_of = [&](Rows& R, int b) {
-#pragma unroll
-      for (int s = 0; s < 4; ++s)
-#pragma unroll
-        for (int j = 0; j < NR; ++j) {
-          if constexpr (FUSED) {
-            R.x[s][j] = *reinterpret_cast<const int4_t*>(fx + b * (F_BLK * 16) + s * 64);
-          } else {
-            // rows of x are read up to 128 bytes past a.kch only where they have them
-            const int c = b * F_BLK + s * 4;
-            R.x[s][j] = c < a.kch ? *reinterpret_cast<const int4_t*>(px[j] + (size_t)c * 16)
-                                  : int4_t{0, 0, 0, 0};
-          }
-        }
-    };
-    Rows X0, X1;
-    if (wk < nb && !FUSED) rows_of(X0, wk);
-    for (int b = wk; b < nb; b += SK) {
-      if (FUSED) rows_of(X0, b);
-      else if (b + SK < nb) rows_of(X1, b + SK);
-      fetch(B2);
-#pragma unroll
-      for (int s = 0; s < 4; s += 2) {
-        int4_t w[2];
-        to_steps(B0.w[s], B0.w[s + 1], w[0], w[1]);
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int j = 0; j < NR; ++j)
-            acc[j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[h], X0.x[s + h][j], acc[j], 0, 0, 0);
-      }
-      B0 = B1;
-      B1 = B2;
-      if (!FUSED) X0 = X1;
-    }
-    // rows 16 j .. +15 of the tile; lane: row r16, channels 4 g .. +3 (gated: lanes of g 2 and 3
-    // hold the up sums of those of g 0 and 1)
-    auto finish = [&](int j, float xs_j, const int4_t& v, const int4_t& u) {
-      const int r = t.r0 + j * 16 + r16;
-      unsigned big = 0;
-      if (r < t.r1 && (!G || lane < 32)) big = emit<MODE>(a, t.e, r, xs_j, t.n0 + 4 * g, v, u);
-      if (FUSED && MODE != MODE_LINEAR) {  // the largest |h| of the tile, for the down product
-        for (int o = 16; o <= 32; o <<= 1) big = max(big, (unsigned)__shfl_xor((int)big, o));
-        if (lane == 0) a.tile_max[t.r0 * nnt + t.n0 / NT] = big;
-      }
-    };
+  };
+  auto end_tile = [&]() {
     if constexpr (SK == 1) {
 #pragma unroll
       for (int j = 0; j < NR; ++j) {
@@ -515,7 +505,7 @@ __global__ __launch_bounds__(W * 64, NR == 1 || W > 8 ? 4 : 2) void k_product_fe
         finish(j, xs[j], acc[j], u);
       }
     } else {
-      if (wk < nb) {
+      if (works) {
 #pragma unroll
         for (int j = 0; j < NR; ++j)
 #pragma unroll
@@ -539,7 +529,50 @@ __global__ __launch_bounds__(W * 64, NR == 1 || W > 8 ? 4 : 2) void k_product_fe
         finish(j, xs[j], v, u);
       }
     }
+#pragma unroll
+    for (int j = 0; j < NR; ++j) acc[j] = int4_t{0, 0, 0, 0};
+    par ^= 1;
+    b = wk;
     t = tile_from(t.id + step);
+    if (!FUSED && t.id < total) {
+      int row[NR];
+      rows_of(t, row);
+#pragma unroll
+      for (int j = 0; j < NR; ++j) xs[j] = a.xs[row[j]];
+    }
+  };
+  if (!works) {
+    while (t.id < total) end_tile();
+    return;
+  }
+  auto block = [&](Block& B) {
+#pragma unroll
+    for (int s = 0; s < 4; s += 2) {
+      int4_t w[2];
+      to_steps(B.w[s], B.w[s + 1], w[0], w[1]);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        // steps past the row's end repeat earlier ones: their weights do not count
+        if (!FUSED && b * F_BLK + (s + h) * 4 >= a.kch) w[h] = int4_t{0, 0, 0, 0};
+#pragma unroll
+        for (int j = 0; j < NR; ++j) {
+          int4_t x;
+          if constexpr (FUSED) x = *reinterpret_cast<const int4_t*>(fx + b * (F_BLK * 16) + (s + h) * 64);
+          else x = B.x[s + h][j];
+          acc[j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[h], x, acc[j], 0, 0, 0);
+        }
+      }
+    }
+    fetch(B);
+    b += SK;
+    if (b >= nb) end_tile();
+  };
+  while (t.id < total) {
+    block(ring[0]);
+    if (t.id >= total) break;
+    block(ring[1]);
+    if (t.id >= total) break;
+    block(ring[2]);
   }
 }
 
@@ -568,20 +601,24 @@ __global__ __launch_bounds__(TD_W * 64) void k_token_down(ProductArgs a, const f
   const int my = lane < a.k ? a.src[lane] : -1;
   const float my_w = lane < a.k ? weights[lane] : 0.f;
   const int groups = a.k * nq;
+  // quotients by whole multiplication: a.div_nq, a.div_nb are 2^32 / nq, / nb rounded up, and
+  // the numerators stay below 2^15
+  auto by_nq = [&](int i) { return (int)__umulhi((unsigned)i, a.div_nq); };
+  auto by_nb = [&](int i) { return nb > 1 ? (int)__umulhi((unsigned)i, a.div_nb) : i; };
   const bool kept = groups <= KEEP * TH;
   float4_t v[KEEP];
   if (kept) {
 #pragma unroll
     for (int u = 0; u < KEEP; ++u) {
       const int i = tid + u * TH;
-      if (i < groups) v[u] = load4<float, true>(h + (size_t)(i / nq) * a.ldx, i % nq, a.cols);
+      const int s = by_nq(i);
+      if (i < groups) v[u] = load4<float, true>(h + (size_t)s * a.ldx, i - s * nq, a.cols);
     }
   }
   unsigned most = 0;  // this wave's share of slot wave % k's maxima
   const int ms = wave % a.k, mw = wave / a.k, mstep = ((TD_W - 1 - ms) / a.k + 1) * 64;
   const bool shared = a.k <= TD_W;
   if (shared) {
-#pragma unroll 4
     for (int i = mw * 64 + lane; i < a.max_tiles; i += mstep)
       most = max(most, a.tile_max[ms * a.max_tiles + i]);
   }
@@ -601,18 +638,20 @@ __global__ __launch_bounds__(TD_W * 64) void k_token_down(ProductArgs a, const f
   lds_barrier();
   const int units = nv * nb;
   const int nnt = (a.n + 15) / 16;
-  int4_t w0[4], w1[4], w2[4];
-  // the stream: two units (blocks of all slots' lengths) ahead of the products
+  // the stream: units (blocks of all slots' lengths)
+  constexpr int RING = 3;
+  int4_t ring[RING][4];
   int nt = blockIdx.x, fnt = nt, fu = wave;
   auto fetch = [&](int4_t* w) {
     if (fnt >= nnt || fu >= units) return;
-    const int8_t* p = a.w + (size_t)__builtin_amdgcn_readfirstlane(s_e[fu / nb]) * a.w_group +
+    const int slot = by_nb(fu), block = fu - slot * nb;
+    const int8_t* p = a.w + (size_t)__builtin_amdgcn_readfirstlane(s_e[slot]) * a.w_group +
                       (size_t)(fnt * 16) * a.ldw;
     const int rows = a.n - 1 - fnt * 16;
 #pragma unroll
     for (int s = 0; s < 4; ++s) {  // 8 rows x 128 bytes each (see to_steps)
       const int row = min((r16 & 7) + 8 * (s & 1), rows);
-      const int c = min((fu % nb) * F_BLK + (s >> 1) * 8 + g + 4 * (r16 >> 3), a.kch - 1);
+      const int c = min(block * F_BLK + (s >> 1) * 8 + g + 4 * (r16 >> 3), a.kch - 1);
       w[s] = __builtin_nontemporal_load(reinterpret_cast<const int4_t*>(
           p + (size_t)((unsigned)row * (unsigned)a.ldw + (unsigned)c * 16)));
     }
@@ -622,8 +661,8 @@ __global__ __launch_bounds__(TD_W * 64) void k_token_down(ProductArgs a, const f
       fnt += gridDim.x;
     }
   };
-  fetch(w0);
-  fetch(w1);
+#pragma unroll
+  for (int i = 0; i < RING; ++i) fetch(ring[i]);
   if (shared) {
     for (int o = 32; o; o >>= 1) most = max(most, (unsigned)__shfl_xor((int)most, o));
     if (lane == 0) atomicMax(&s_max[ms], most);
@@ -639,7 +678,7 @@ __global__ __launch_bounds__(TD_W * 64) void k_token_down(ProductArgs a, const f
   // slots without an expert have no maximum, and no unit reads their rows
   auto put = [&](int i, const float4_t& x) {
     float r;
-    const float s = row_scale(s_max[i / nq], r);
+    const float s = row_scale(s_max[by_nq(i)], r);
     reinterpret_cast<int*>(s_h)[i] = s > 0.f ? quantize4(x, s, r) : 0;
   };
   if (kept) {
@@ -648,37 +687,12 @@ __global__ __launch_bounds__(TD_W * 64) void k_token_down(ProductArgs a, const f
       if (tid + u * TH < groups) put(tid + u * TH, v[u]);
   } else {
     for (int i = tid; i < groups; i += TH)
-      put(i, load4<float, true>(h + (size_t)(i / nq) * a.ldx, i % nq, a.cols));
+      put(i, load4<float, true>(h + (size_t)by_nq(i) * a.ldx, i - by_nq(i) * nq, a.cols));
   }
   lds_barrier();
-  for (int par = 0; nt < nnt; nt += gridDim.x, par ^= 1) {
-    int4_t acc = {0, 0, 0, 0};
-    for (int u = wave; u < units; u += TD_W) {
-      fetch(w2);
-      const int n = u / nb;
-      const int8_t* f = s_h + (size_t)s_slot[n] * kpad + (u - n * nb) * (F_BLK * 16) + g * 16;
-#pragma unroll
-      for (int s = 0; s < 4; s += 2) {
-        int4_t m[2];
-        to_steps(w0[s], w0[s + 1], m[0], m[1]);
-#pragma unroll
-        for (int q = 0; q < 2; ++q)
-          acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(
-              m[q], *reinterpret_cast<const int4_t*>(f + (s + q) * 64), acc, 0, 0, 0);
-      }
-      if (u + TD_W >= units || (u + TD_W) / nb != n) {
-        if (r16 == 0) {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) atomicAdd(&s_sum[par][n][4 * g + j], acc[j]);
-        }
-        acc = int4_t{0, 0, 0, 0};
-      }
-#pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        w0[s] = w1[s];
-        w1[s] = w2[s];
-      }
-    }
+  int4_t acc = {0, 0, 0, 0};
+  int u = wave, par = 0;
+  auto end_tile = [&]() {
     lds_barrier();
     if (tid < 16) {
       const int c = nt * 16 + tid;
@@ -698,6 +712,45 @@ __global__ __launch_bounds__(TD_W * 64) void k_token_down(ProductArgs a, const f
         else static_cast<__bf16*>(a.out)[c] = (__bf16)y;
       }
     }
+    par ^= 1;
+    u = wave;
+    nt += gridDim.x;
+  };
+  if (wave >= units) {  // nothing of the stream is this wave's
+    while (nt < nnt) end_tile();
+    return;
+  }
+  // one unit, from a buffer that is refilled with the unit RING ahead and never copied (a copy
+  // would wait for the loads)
+  auto unit = [&](int4_t* w) {
+    const int n = by_nb(u);
+    const int8_t* f = s_h + (size_t)s_slot[n] * kpad + (u - n * nb) * (F_BLK * 16) + g * 16;
+#pragma unroll
+    for (int s = 0; s < 4; s += 2) {
+      int4_t m[2];
+      to_steps(w[s], w[s + 1], m[0], m[1]);
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+        acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(
+            m[q], *reinterpret_cast<const int4_t*>(f + (s + q) * 64), acc, 0, 0, 0);
+    }
+    fetch(w);
+    u += TD_W;
+    if (u >= units || by_nb(u) != n) {
+      if (r16 == 0) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) atomicAdd(&s_sum[par][n][4 * g + j], acc[j]);
+      }
+      acc = int4_t{0, 0, 0, 0};
+    }
+    if (u >= units) end_tile();
+  };
+  while (nt < nnt) {
+    unit(ring[0]);
+    if (nt >= nnt) break;
+    unit(ring[1]);
+    if (nt >= nnt) break;
+    unit(ring[2]);
   }
 }
 
@@ -868,14 +921,18 @@ void few_launch(const ProductArgs& a, int64_t tiles, size_t lds, hipStream_t s) 
   k_product_few<MODE, NR, X, W, SK>
       <<<dim3((unsigned)std::min<int64_t>(groups, at_once)), dim3(W * 64), lds, s>>>(a);
 }
-// waves of a tile: one where the tiles give every compute unit ten, else four, else sixteen
+// Waves of a tile. One where rows are short (up to 32 blocks) and the tiles give every compute
+// unit ten: a wave alone waits for nobody (2 of 8 experts' up products at 16 tokens, d 4096,
+// d_ffn 11008: 135 us; four waves 156, eight 170). Else eight, which read a tile's rows in runs
+// of 2 KB (their down products: 72 us; four 74, one 78), or four where more rows of x take the
+// registers (24 tokens x 11008 x 4096: 15.7 us; eight 17.0).
 template <int MODE, int NR, typename X>
 void few_launch(const ProductArgs& a, int64_t row_tiles, size_t lds, hipStream_t s) {
   constexpr int NT = MODE == MODE_ACT_GATED ? 8 : 16;
+  constexpr int SK = NR == 1 ? 8 : 4;
   const int64_t tiles = row_tiles * ((a.n + NT - 1) / NT);
-  if (tiles >= 2560) few_launch<MODE, NR, X, 4, 1>(a, tiles, lds, s);
-  else if (tiles >= 512) few_launch<MODE, NR, X, 4, 4>(a, tiles, lds, s);
-  else few_launch<MODE, NR, X, NR == 1 ? 16 : 8, NR == 1 ? 16 : 8>(a, tiles, lds, s);
+  if (tiles >= 2560 && a.kch <= 32 * F_BLK) few_launch<MODE, NR, X, 4, 1>(a, tiles, lds, s);
+  else few_launch<MODE, NR, X, SK, SK>(a, tiles, lds, s);
 }
 
 template <int MODE>
@@ -940,7 +997,11 @@ hipError_t launch_product_fused(const ProductArgs& a, int x_type, ProductMode mo
 
 int act_tiles(int f, bool gated) { return gated ? (f + 7) / 8 : (f + 15) / 16; }
 
-hipError_t launch_token_down(const ProductArgs& a, const float* weights, hipStream_t s) {
+hipError_t launch_token_down(ProductArgs a, const float* weights, hipStream_t s) {
+  const int nb = (a.kch + F_BLK - 1) / F_BLK, nq = nb * F_BLK * 4;
+  auto inverse = [](int n) { return n > 1 ? (unsigned)((((uint64_t)1 << 32) + n - 1) / n) : 0u; };
+  a.div_nq = inverse(nq);
+  a.div_nb = inverse(nb);
   const size_t lds = (size_t)a.k * host::i8_kpad(a.cols);
   const int at_once = resident(k_token_down, TD_W * 64, lds);
   k_token_down<<<dim3((unsigned)std::min((a.n + 15) / 16, at_once)), dim3(TD_W * 64), lds, s>>>(a, weights);
