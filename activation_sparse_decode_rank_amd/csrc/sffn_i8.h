@@ -49,7 +49,6 @@ struct ProductArgs {
   void* out;
   int64_t ldo;         // elements
   int out_type;
-  int vec_out;         // set by launch_product: out's rows start at multiples of four elements
   int tile;            // rows of a tile (host::i8_tile)
   // groups only
   const int32_t* offs;    // [experts + 1] first sorted row of each expert

@@ -151,13 +151,12 @@ __global__ __launch_bounds__(TPB) void k_pad_rows(const int8_t* __restrict__ x, 
       q[(size_t)row * kpad + j] = j < cols ? x[(size_t)row * ldx + j] : 0;
 }
 
-// Four neighbouring values of a row as T; whole: all four are inside the row and the row's
-// places are multiples of four elements.
+// Four neighbouring values of a row as T, the first `left` of them
 template <typename T>
-__device__ __forceinline__ void store4(void* p, size_t i, const float4_t& v, int left, bool whole) {
-  typedef T vec __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ void store4(void* p, size_t i, const float4_t& v, int left) {
+  typedef T vec __attribute__((ext_vector_type(4), aligned(sizeof(T))));
   T* o = static_cast<T*>(p) + i;
-  if (whole) {
+  if (left >= 4) {
     vec t;
 #pragma unroll
     for (int j = 0; j < 4; ++j) t[j] = (T)v[j];
@@ -169,48 +168,69 @@ __device__ __forceinline__ void store4(void* p, size_t i, const float4_t& v, int
   }
 }
 
-// What becomes of the sums of sorted row (or row) r at channels (neurons) c .. c + 3 of expert
-// e: v, and in the gated form u of the up rows. xs: the scale of the row of x behind r.
-// Returns the largest |h|'s bits (ACT forms).
+// The scales of channels (neurons) c .. c + 3 of expert e, and their biases; in the gated form of
+// the gate and the up rows. Read before the stores of a tile, which they could not pass.
 template <int MODE>
-__device__ __forceinline__ unsigned emit(const ProductArgs& a, int e, int r, float xs, int c,
-                                     const int4_t& v, const int4_t& u) {
+struct Scales {
+  static constexpr bool G = MODE == MODE_ACT_GATED;
+  float4_t s, u, b;
+  __device__ __forceinline__ void load(const ProductArgs& a, int e, int c) {
+    typedef float vec __attribute__((ext_vector_type(4), aligned(4)));
+    const size_t at = (size_t)e * a.n + c;
+    const float* ws = a.ws + (G ? 2 : 1) * at;
+    s = u = b = float4_t{0.f, 0.f, 0.f, 0.f};
+    if (c + 4 <= a.n) {
+      if (G) {
+        const vec lo = *reinterpret_cast<const vec*>(ws), hi = *reinterpret_cast<const vec*>(ws + 4);
+        s = float4_t{lo[0], lo[2], hi[0], hi[2]};
+        u = float4_t{lo[1], lo[3], hi[1], hi[3]};
+      } else {
+        s = *reinterpret_cast<const vec*>(ws);
+      }
+      if (MODE != MODE_DOWN && a.bias) b = *reinterpret_cast<const vec*>(a.bias + at);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (c + j >= a.n) break;
+        s[j] = ws[G ? 2 * j : j];
+        if (G) u[j] = ws[2 * j + 1];
+        if (MODE != MODE_DOWN && a.bias) b[j] = a.bias[at + j];
+      }
+    }
+  }
+};
+
+// What becomes of the sums at channels (neurons) c .. c + 3: v, and in the gated form u of the up
+// rows. xs: the scale of the row of x; ro: the row of out. Returns the largest |h|'s bits (ACT
+// forms).
+template <int MODE>
+__device__ __forceinline__ unsigned emit(const ProductArgs& a, int ro, float xs, int c,
+                                         const Scales<MODE>& S, const int4_t& v, const int4_t& u) {
   if (c >= a.n) return 0;
   unsigned big = 0;
   const int left = a.n - c;
-  const bool whole = left >= 4 && a.vec_out;
+  const size_t o = (size_t)ro * a.ldo + c;
   float4_t y;
   if constexpr (MODE == MODE_ACT || MODE == MODE_ACT_GATED) {
     // h in 64 bits up to its one rounding: it decides between whole numbers afterwards
-    constexpr int M = MODE == MODE_ACT_GATED ? 2 : 1;
-    const float* ws = a.ws + ((size_t)e * a.n + c) * M;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      if (j >= left) break;
-      double h = (double)v[j] * ((double)xs * (double)ws[M * j]);
-      if (a.bias) h += (double)a.bias[(size_t)e * a.n + c + j];
+      double h = (double)v[j] * ((double)xs * (double)S.s[j]) + (double)S.b[j];
       h = h < 0.0 ? 0.0 : h;  // NaN stays
-      if (M == 2) h *= (double)u[j] * ((double)xs * (double)ws[M * j + 1]);
+      if (MODE == MODE_ACT_GATED) h *= (double)u[j] * ((double)xs * (double)S.u[j]);
       y[j] = (float)h;
-      big = max(big, mag(y[j]));
+      if (j < left) big = max(big, mag(y[j]));
     }
-    store4<float>(a.out, (size_t)r * a.ldo + c, y, left, whole);
+    store4<float>(a.out, o, y, left);
   } else {
-    const float* ws = a.ws + (size_t)e * a.n + c;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      if (j >= left) break;
-      y[j] = (float)v[j] * (xs * ws[j]);
-      if (MODE == MODE_LINEAR && a.bias) y[j] += a.bias[c + j];
+      y[j] = (float)v[j] * (xs * S.s[j]);
+      if (MODE == MODE_LINEAR) y[j] += S.b[j];
     }
-    if (MODE == MODE_DOWN) {
-      store4<float>(a.out, (size_t)a.src[r] * a.ldo + c, y, left, whole);
-    } else {
-      const size_t o = (size_t)r * a.ldo + c;
-      if (a.out_type == T_F32) store4<float>(a.out, o, y, left, whole);
-      else if (a.out_type == T_F16) store4<_Float16>(a.out, o, y, left, whole);
-      else store4<__bf16>(a.out, o, y, left, whole);
-    }
+    if (MODE == MODE_DOWN || a.out_type == T_F32) store4<float>(a.out, o, y, left);
+    else if (a.out_type == T_F16) store4<_Float16>(a.out, o, y, left);
+    else store4<__bf16>(a.out, o, y, left);
   }
   return big;
 }
@@ -228,6 +248,12 @@ __device__ __forceinline__ bool tile_rows(const ProductArgs& a, int mt, int& e, 
     r1 = a.offs[e + 1];
   }
   return true;
+}
+
+// row of out that (sorted) row r gives
+template <int MODE>
+__device__ __forceinline__ int row_of_out(const ProductArgs& a, int r) {
+  return MODE == MODE_DOWN ? a.src[r] : r;
 }
 
 // row of x behind (sorted) row r
@@ -455,13 +481,23 @@ __global__ __launch_bounds__(W * 64, (FEW_WAVES<NR, X>)) void k_product_few(Prod
   if constexpr (FUSED) own.load(reinterpret_cast<const XT*>(a.x), a.ldx, rows_x, a.cols, kpad);
   const int8_t* fx = s_x + (MODE == MODE_LINEAR ? min(r16, rows_x - 1) : 0) * kpad + g * 16;
   Block ring[3];
+  // what the end of a tile needs, read at its start
   float xs[NR];
+  int ro[NR];
+  Scales<MODE> sc;
+  auto begin_tile = [&]() {
+    if (t.id >= total) return;
+#pragma unroll
+    for (int j = 0; j < NR; ++j) {
+      const int r = min(t.r0 + j * 16 + r16, t.r1 - 1);
+      ro[j] = row_of_out<MODE>(a, r);
+      if (!FUSED) xs[j] = a.xs[row_of_x<MODE>(a, r)];
+    }
+    sc.load(a, t.e, t.n0 + 4 * (G ? g & 1 : g));
+  };
   rows_of(ft, frow);
   rows_of(fn, fnext);
-  if constexpr (!FUSED) {
-#pragma unroll
-    for (int j = 0; j < NR; ++j) xs[j] = t.id < total ? a.xs[frow[j]] : 0.f;
-  }
+  begin_tile();
   if (works && t.id < total) {
     aim();
 #pragma unroll
@@ -484,10 +520,10 @@ __global__ __launch_bounds__(W * 64, (FEW_WAVES<NR, X>)) void k_product_few(Prod
   int b = wk, par = 0;
   // rows 16 j .. +15 of the tile; lane: row r16, channels 4 g .. +3 (gated: lanes of g 2 and 3
   // hold the up sums of those of g 0 and 1)
-  auto finish = [&](int j, float xs_j, const int4_t& v, const int4_t& u) {
+  auto finish = [&](int j, const int4_t& v, const int4_t& u) {
     const int r = t.r0 + j * 16 + r16;
     unsigned big = 0;
-    if (r < t.r1 && (!G || lane < 32)) big = emit<MODE>(a, t.e, r, xs_j, t.n0 + 4 * g, v, u);
+    if (r < t.r1 && (!G || lane < 32)) big = emit<MODE>(a, ro[j], xs[j], t.n0 + 4 * g, sc, v, u);
     if (FUSED && MODE != MODE_LINEAR) {  // the largest |h| of the tile, for the down product
       for (int o = 16; o <= 32; o <<= 1) big = max(big, (unsigned)__shfl_xor((int)big, o));
       if (lane == 0) a.tile_max[t.r0 * nnt + t.n0 / NT] = big;
@@ -502,7 +538,7 @@ __global__ __launch_bounds__(W * 64, (FEW_WAVES<NR, X>)) void k_product_few(Prod
 #pragma unroll
           for (int c = 0; c < 4; ++c) u[c] = __shfl_xor(acc[j][c], 32);
         }
-        finish(j, xs[j], acc[j], u);
+        finish(j, acc[j], u);
       }
     } else {
       if (works) {
@@ -526,7 +562,7 @@ __global__ __launch_bounds__(W * 64, (FEW_WAVES<NR, X>)) void k_product_few(Prod
         wave_lds_sync();  // another lane reads what this one clears
 #pragma unroll
         for (int c = 0; c < 4; ++c) s_sum[par][j][c][lane] = 0;
-        finish(j, xs[j], v, u);
+        finish(j, v, u);
       }
     }
 #pragma unroll
@@ -534,12 +570,7 @@ __global__ __launch_bounds__(W * 64, (FEW_WAVES<NR, X>)) void k_product_few(Prod
     par ^= 1;
     b = wk;
     t = tile_from(t.id + step);
-    if (!FUSED && t.id < total) {
-      int row[NR];
-      rows_of(t, row);
-#pragma unroll
-      for (int j = 0; j < NR; ++j) xs[j] = a.xs[row[j]];
-    }
+    begin_tile();
   };
   if (!works) {
     while (t.id < total) end_tile();
@@ -754,45 +785,42 @@ __global__ __launch_bounds__(TD_W * 64) void k_token_down(ProductArgs a, const f
   }
 }
 
-// Many rows: a workgroup of 8 waves takes 256 rows of w (channels; gated: 128 neurons, 16 gate
-// rows and their 16 up rows in turn) and TK rows of x over the whole length, in stages of 64
-// bytes. Both operands go from memory straight into LDS (global_load_lds_dwordx4: each lane's
-// 16 bytes land at the next 16 bytes of a 1 KB block), NS stages deep. Within a block, 16 rows
-// of 64 bytes, row r's 16-byte chunk c sits at position (c + r / 4) mod 4 of the row, so that a
-// fragment read (16 rows, one chunk each) touches every LDS bank once. A step waits for the
-// next stage, refills the buffer that was read with the stage NS ahead, and reads the next
-// stage's fragments into registers while the matrix cores take the current ones.
-constexpr int T_CH = 256;   // rows of w per tile
-constexpr int T_K = 64;     // bytes per stage
-constexpr int T_W = 8;      // waves
-
+// Many rows: a workgroup of WC x WT waves takes CH rows of w (channels; gated: CH / 2 neurons, 16
+// gate rows and their 16 up rows in turn) and TK rows of x over the whole length, in stages of
+// 128 bytes, a whole line of every row. Both operands go from memory straight into LDS
+// (global_load_lds_dwordx4: each lane's 16 bytes land at the next 16 bytes of 8 rows x 128
+// bytes), NS stages deep. Row r of 16 holds its 16-byte chunk c at place c ^ (r / 2): the sixteen
+// lanes that LDS serves together in a 16-byte read (0-3, 12-15 and 20-27 of each 32, and the
+// rest) then touch different banks. A stage is two steps of 64 bytes with one barrier between
+// them: the first step's products run while the second step's operands are read; at the barrier
+// every wave is done with the stage's LDS and the next stage has landed; the second step's
+// products run while the freed stage is refilled and the next stage's first operands are read.
+// Reads and loads are issued between the products, not before them.
 // this lane's 16 bytes at src to place 16 * lane of the 1 KB block at dst (LDS)
 __device__ __forceinline__ void load_block(const int8_t* src, int8_t* dst) {
   __builtin_amdgcn_global_load_lds(reinterpret_cast<const u32x4*>(src),
                                    (__attribute__((address_space(3))) void*)dst, 16, 0, 0);
 }
 
-// until at most MOST (FEWER: for waves that load one block less a stage) of this wave's loads
-// are in flight
-template <int MOST, int FEWER>
-__device__ __forceinline__ void wait_loads(bool most) {
-  if (most)
-    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(MOST) : "memory");
-  else
-    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(FEWER) : "memory");
+// until at most N of this wave's loads are in flight
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
 }
 
-template <int MODE, int TK>
-__global__ __launch_bounds__(T_W * 64) void k_product(ProductArgs a) {
+// instruction kinds of __builtin_amdgcn_sched_group_barrier
+constexpr int SG_MFMA = 0x8, SG_LOAD = 0x20, SG_LDS_READ = 0x100;
+
+template <int MODE, int CH, int TK, int WC, int WT, int NS>
+__global__ __launch_bounds__(WC * WT * 64) void k_product(ProductArgs a) {
   constexpr bool G = MODE == MODE_ACT_GATED;
-  constexpr int NT = G ? T_CH / 2 : T_CH;          // channels (neurons) per tile
-  constexpr int WT = TK >= 256 ? 4 : TK >= 128 ? 2 : 1;  // waves along the rows of x
-  constexpr int WC = T_W / WT;                     // waves along the channels
-  constexpr int NI = T_CH / 16 / WC, NJ = TK / 16 / WT;  // 16 x 16 tiles of a wave
-  constexpr int BW = T_CH * T_K, BX = TK * T_K, STAGE = BW + BX;
-  constexpr int NS = 4;
-  constexpr int NG = STAGE / 1024;                 // 1 KB loads a stage
-  constexpr int DPS = (NG + T_W - 1) / T_W;        // most of one wave
+  constexpr int W = WC * WT;
+  constexpr int NT = G ? CH / 2 : CH;                    // channels (neurons) per tile
+  constexpr int NI = CH / 16 / WC, NJ = TK / 16 / WT;    // 16 x 16 tiles of a wave
+  constexpr int STAGE = (CH + TK) * 128;
+  constexpr int UW = CH / 8, NG = (CH + TK) / 8;         // 1 KB loads of w, of both, a stage
+  constexpr int DPS = NG / W;                            // of one wave
+  static_assert(NG % W == 0 && W % 2 == 0 && NI % 2 == 0, "whole loads per wave, pairs of tiles");
   static_assert((NS - 1) * DPS <= 63, "vmcnt range");
   __shared__ __attribute__((aligned(16))) int8_t sbuf[NS * STAGE];
   const int nnt = (a.n + NT - 1) / NT;
@@ -815,34 +843,28 @@ __global__ __launch_bounds__(T_W * 64) void k_product(ProductArgs a) {
   const int nw = G ? 2 * a.n : a.n;
   const int8_t* w = a.w + (size_t)e * a.w_group;
 
-  // the lane's row in a 16-row block and the chunk its place holds
-  const int lr = lane >> 2;
-  const int lc = ((lane & 3) - (lr >> 2)) & 3;
+  const int lc = (lane & 7) ^ ((wave & 1) * 4 + (lane >> 4));  // chunk that this lane loads
   const int8_t* src[DPS];
 #pragma unroll
   for (int v = 0; v < DPS; ++v) {
-    const int u = wave + T_W * v;  // block of the stage, wave-uniform
-    if (u < T_CH / 16) {
-      const int row = G ? 2 * (n0 + (u >> 1) * 16 + lr) + (u & 1) : n0 + u * 16 + lr;
+    const int u = wave + W * v;  // 8 rows of the stage, wave-uniform
+    if (u < UW) {
+      const int R = 8 * u + (lane >> 3);
+      const int row = G ? 2 * (n0 + (R >> 5) * 16 + (R & 15)) + ((R >> 4) & 1) : n0 + R;
       src[v] = w + (size_t)min(row, nw - 1) * a.ldw;
     } else {
-      src[v] = a.x + (size_t)row_of_x<MODE>(a, min(r0 + (u - T_CH / 16) * 16 + lr, r1 - 1)) * a.ldx;
+      src[v] = a.x + (size_t)row_of_x<MODE>(a, min(r0 + 8 * (u - UW) + (lane >> 3), r1 - 1)) * a.ldx;
     }
   }
-  const int nk = (a.kch + 7) / 8 * 2;  // stages: x's rows end in zeros up to 128 bytes
+  const int nk = (a.kch + 7) / 8;  // stages: x's rows end in zeros up to 128 bytes
   auto issue = [&](int st, int buf) {
-    const int kc = st * (T_K / 16) + lc;
+    const int kc = st * 8 + lc;
     const int kw = min(kc, a.kch - 1);  // past w's row x is zero: any chunk will do
 #pragma unroll
     for (int v = 0; v < DPS; ++v) {
-      const int u = wave + T_W * v;
-      if (NG % T_W && u >= NG) break;
-      load_block(src[v] + (size_t)(u < T_CH / 16 ? kw : kc) * 16, sbuf + buf * STAGE + u * 1024);
+      const int u = wave + W * v;
+      load_block(src[v] + (size_t)(u < UW ? kw : kc) * 16, sbuf + buf * STAGE + u * 1024);
     }
-  };
-  auto frag = [&](const int8_t* base, int block) {
-    return *reinterpret_cast<const int4_t*>(base + block * 1024 +
-                                            (r16 * 4 + ((g + (r16 >> 2)) & 3)) * 16);
   };
   int4_t acc[NI][NJ];
 #pragma unroll
@@ -852,12 +874,16 @@ __global__ __launch_bounds__(T_W * 64) void k_product(ProductArgs a) {
   struct Frags {
     int4_t w[NI], x[NJ];
   };
-  auto read_frags = [&](Frags& F, int st) {
-    const int8_t* base = sbuf + (st % NS) * STAGE;
+  // this lane's place in 16 rows, of step 0 and 1
+  const int place0 = r16 * 128 + (g ^ (r16 >> 1)) * 16, place1 = place0 ^ 64;
+  auto read_frags = [&](Frags& F, int buf, int place) {
+    const int8_t* base = sbuf + buf * STAGE + place;
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) F.x[j] = frag(base, T_CH / 16 + wt * NJ + j);
+    for (int j = 0; j < NJ; ++j)
+      F.x[j] = *reinterpret_cast<const int4_t*>(base + (CH / 16 + wt * NJ + j) * 2048);
 #pragma unroll
-    for (int i = 0; i < NI; ++i) F.w[i] = frag(base, wc * NI + i);
+    for (int i = 0; i < NI; ++i)
+      F.w[i] = *reinterpret_cast<const int4_t*>(base + (wc * NI + i) * 2048);
   };
   auto products = [&](const Frags& F) {
 #pragma unroll
@@ -866,41 +892,73 @@ __global__ __launch_bounds__(T_W * 64) void k_product(ProductArgs a) {
       for (int j = 0; j < NJ; ++j)
         acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(F.w[i], F.x[j], acc[i][j], 0, 0, 0);
   };
-  // Past the last stage the refill loads the last stage again (in bounds, never read), so
-  // every step has the same loads in flight and no branch.
-  const bool most = NG % T_W == 0 || wave < NG % T_W;  // else it loads one block less a stage
-  auto step = [&](int st, Frags& Fc, Frags& Fn) {
-    wait_loads<(NS - 2) * DPS, (NS - 2) * (DPS - 1)>(most);
-    __builtin_amdgcn_s_waitcnt(I8_WAIT_LGKM0);  // this wave's reads of stage st are done
+  constexpr int READS = NI + NJ, PER = NI * NJ / READS > 0 ? NI * NJ / READS : 1;
+  auto barrier = [&]() {
+    __builtin_amdgcn_s_waitcnt(I8_WAIT_LGKM0);  // this wave's reads are done
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
-    issue(min(st + NS, nk - 1), st % NS);
-    read_frags(Fn, st + 1);
-    products(Fc);
   };
+  Frags F0, F1;
 #pragma unroll
   for (int st = 0; st < NS; ++st) issue(min(st, nk - 1), st);
-  wait_loads<(NS - 1) * DPS, (NS - 1) * (DPS - 1)>(most);
-  __builtin_amdgcn_s_barrier();
-  asm volatile("" ::: "memory");
-  Frags F0, F1;
-  read_frags(F0, 0);
-  for (int st = 0; st < nk; st += 2) {  // nk is even
-    step(st, F0, F1);
-    step(st + 1, F1, F0);
+  wait_loads<(NS - 1) * DPS>();
+  barrier();
+  read_frags(F0, 0, place0);
+  int buf = 0;
+  for (int st = 0; st < nk; ++st) {
+    read_frags(F1, buf, place1);
+    products(F0);
+#pragma unroll
+    for (int q = 0; q < READS; ++q) {
+      __builtin_amdgcn_sched_group_barrier(SG_LDS_READ, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(SG_MFMA, PER, 0);
+    }
+    // Past the last stage the refill loads the last stage again (in bounds, never read), so
+    // every stage has the same loads in flight and no branch.
+    wait_loads<(NS - 2) * DPS>();
+    barrier();
+    const int next = buf + 1 == NS ? 0 : buf + 1;
+    issue(min(st + NS, nk - 1), buf);
+    read_frags(F0, next, place0);
+    products(F1);
+#pragma unroll
+    for (int q = 0; q < READS; ++q) {
+      __builtin_amdgcn_sched_group_barrier(SG_LDS_READ, 1, 1);
+      if (q < DPS) __builtin_amdgcn_sched_group_barrier(SG_LOAD, 1, 1);
+      __builtin_amdgcn_sched_group_barrier(SG_MFMA, PER, 1);
+    }
+    buf = next;
   }
-  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no load may land in LDS after the loop
+  wait_loads<0>();  // no load may land in LDS after the loop
   // lane holds rows 16 j + r16 and channels 16 i + 4 g .. +3 of the wave's part
+  constexpr int NE = G ? NI / 2 : NI;
+  auto channel = [&](int i) { return n0 + (wc * NE + i) * 16 + 4 * g; };
+  Scales<MODE> sc[NE];
+  float xs[NJ];
+  int ro[NJ];
+#pragma unroll
+  for (int i = 0; i < NE; ++i) sc[i].load(a, e, channel(i));
 #pragma unroll
   for (int j = 0; j < NJ; ++j) {
-    const int r = r0 + (wt * NJ + j) * 16 + r16;
-    if (r >= r1) continue;
-    const float xs = a.xs[row_of_x<MODE>(a, r)];
-#pragma unroll
-    for (int i = 0; i < NI; i += G ? 2 : 1)
-      emit<MODE>(a, e, r, xs, n0 + (G ? (wc * NI + i) / 2 : wc * NI + i) * 16 + 4 * g, acc[i][j],
-                 acc[G ? i + 1 : i][j]);
+    const int r = min(r0 + (wt * NJ + j) * 16 + r16, r1 - 1);
+    xs[j] = a.xs[row_of_x<MODE>(a, r)];
+    ro[j] = row_of_out<MODE>(a, r);
   }
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) {
+    if (r0 + (wt * NJ + j) * 16 + r16 >= r1) continue;
+#pragma unroll
+    for (int i = 0; i < NE; ++i)
+      emit<MODE>(a, ro[j], xs[j], channel(i), sc[i], acc[G ? 2 * i : i][j], acc[G ? 2 * i + 1 : i][j]);
+  }
+}
+
+template <int MODE, int CH, int TK, int WC, int WT, int NS>
+void tile_launch(const ProductArgs& a, int64_t row_tiles, hipStream_t s) {
+  constexpr int NT = MODE == MODE_ACT_GATED ? CH / 2 : CH;
+  const int64_t tiles = row_tiles * ((a.n + NT - 1) / NT);
+  k_product<MODE, CH, TK, WC, WT, NS>
+      <<<dim3((unsigned)((tiles + 7) / 8 * 8)), dim3(WC * WT * 64), 0, s>>>(a);
 }
 
 // workgroups of a kernel that the current device holds at once (asked once per kernel)
@@ -936,20 +994,16 @@ void few_launch(const ProductArgs& a, int64_t row_tiles, size_t lds, hipStream_t
 }
 
 template <int MODE>
-void product_launch(ProductArgs a, hipStream_t s) {
-  a.vec_out = a.ldo % 4 == 0 &&
-              reinterpret_cast<uintptr_t>(a.out) % (a.out_type == T_F32 ? 16 : 8) == 0;
+void product_launch(const ProductArgs& a, hipStream_t s) {
   const int64_t tiles = MODE == MODE_LINEAR ? ((int64_t)a.rows + a.tile - 1) / a.tile : a.max_tiles;
   if (a.tile == 16) {
     few_launch<MODE, 1, void>(a, tiles, 0, s);
   } else if (a.tile == 32) {
     few_launch<MODE, 2, void>(a, tiles, 0, s);
   } else {
-    constexpr int NT = MODE == MODE_ACT_GATED ? T_CH / 2 : T_CH;
-    const dim3 grid((unsigned)((tiles * ((a.n + NT - 1) / NT) + 7) / 8 * 8)), block(T_W * 64);
-    if (a.tile == 64) k_product<MODE, 64><<<grid, block, 0, s>>>(a);
-    else if (a.tile == 128) k_product<MODE, 128><<<grid, block, 0, s>>>(a);
-    else k_product<MODE, 256><<<grid, block, 0, s>>>(a);
+    if (a.tile == 64) tile_launch<MODE, 256, 64, 4, 2, 2>(a, tiles, s);
+    else if (a.tile == 128) tile_launch<MODE, 256, 128, 4, 2, 3>(a, tiles, s);
+    else tile_launch<MODE, 256, 256, 2, 4, 2>(a, tiles, s);
   }
 }
 
@@ -971,9 +1025,7 @@ void quantize_launch(const QuantArgs& a, hipStream_t s) {
 }
 
 template <int MODE, typename X>
-void fused_launch(ProductArgs a, hipStream_t s) {
-  a.vec_out = a.ldo % 4 == 0 &&
-              reinterpret_cast<uintptr_t>(a.out) % (a.out_type == T_F32 ? 16 : 8) == 0;
+void fused_launch(const ProductArgs& a, hipStream_t s) {
   const size_t rows = MODE == MODE_LINEAR ? a.rows : 1;
   few_launch<MODE, 1, X>(a, MODE == MODE_LINEAR ? 1 : a.k,
                                                          rows * host::i8_kpad(a.cols), s);
