@@ -213,14 +213,24 @@ __device__ __forceinline__ unsigned emit(const ProductArgs& a, int ro, float xs,
   float4_t y;
   if constexpr (MODE == MODE_ACT || MODE == MODE_ACT_GATED) {
     // h in 64 bits up to its one rounding: it decides between whole numbers afterwards
+    if (MODE == MODE_ACT_GATED && !a.bias) {
+      // the scales together: two products of 64 bits less for each value
+      const double x2 = (double)xs * (double)xs;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      double h = (double)v[j] * ((double)xs * (double)S.s[j]) + (double)S.b[j];
-      h = h < 0.0 ? 0.0 : h;  // NaN stays
-      if (MODE == MODE_ACT_GATED) h *= (double)u[j] * ((double)xs * (double)S.u[j]);
-      y[j] = (float)h;
-      if (j < left) big = max(big, mag(y[j]));
+      for (int j = 0; j < 4; ++j)
+        y[j] = (float)((double)max(v[j], 0) * (double)u[j] * (x2 * ((double)S.s[j] * (double)S.u[j])));
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        double h = (double)v[j] * ((double)xs * (double)S.s[j]) + (double)S.b[j];
+        h = h < 0.0 ? 0.0 : h;  // NaN stays
+        if (MODE == MODE_ACT_GATED) h *= (double)u[j] * ((double)xs * (double)S.u[j]);
+        y[j] = (float)h;
+      }
     }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (j < left) big = max(big, mag(y[j]));
     store4<float>(a.out, o, y, left);
   } else {
 #pragma unroll

@@ -4,8 +4,15 @@
 //   group worth = the best c_e or the sum of the two best, top groups, top k of c_e,
 //   weights s_e (/ their sum) * scale
 //
-// One wave takes one token, expert e in lane e % 64 as its value e / 64. Scores are compared
-// in 64 bits, so that the choice is that of the exact scores.
+// One wave takes one token, expert e in lane e % 64 as its value e / 64; a choice is a maximum
+// over the wave (DPP) and a ballot for its lowest index. Bound by those instructions: the logits
+// are read once.
+//
+// Without a bias the logits themselves are compared, which is exact; only the chosen experts' (or,
+// where the softmax is not renormalised, all) exponentials are taken. Scores that are compared are
+// computed in 32 bits first, off by at most a known margin; where every comparison that decided
+// was won by more than that, the choice is that of the exact scores, and otherwise the wave does
+// the token again in 64 bits.
 #include <algorithm>
 
 #include "sffn_device.h"
@@ -14,140 +21,346 @@
 namespace sffn {
 namespace {
 
-template <typename T>
-__device__ __forceinline__ float to_f32(T v) {
-  return (float)v;
-}
-
 constexpr int RWAVES = TPB / 64;
 
-// J: experts per lane (E <= 64 J)
-template <typename T, int J>
+template <int CTRL, int ROW_MASK = 0xF>
+__device__ __forceinline__ float dpp_max(float v) {
+  // lanes without a source keep their own value
+  return fmaxf(v, __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(
+                                                __builtin_bit_cast(int, v), __builtin_bit_cast(int, v),
+                                                CTRL, ROW_MASK, 0xF, false)));
+}
+__device__ __forceinline__ float from_lane(float v, int lane) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), lane));
+}
+// largest over the wave, in every lane (one scalar)
+__device__ __forceinline__ float wave_max(float v) {
+  v = dpp_max<DPP_QP_XOR1>(v);
+  v = dpp_max<DPP_QP_XOR2>(v);
+  v = dpp_max<DPP_HALF_MIRROR>(v);
+  v = dpp_max<DPP_MIRROR>(v);
+  v = dpp_max<DPP_BCAST15, 0xA>(v);
+  v = dpp_max<DPP_BCAST31, 0xC>(v);
+  return from_lane(v, 63);
+}
+__device__ __forceinline__ float wave_total(float v) { return from_lane(wave_sum(v), WAVE_SUM_LANE); }
+
+__device__ __forceinline__ double with_words(int lo, int hi) {
+  return __builtin_bit_cast(double, ((uint64_t)(unsigned)hi << 32) | (unsigned)lo);
+}
+__device__ __forceinline__ int low(double v) { return (int)__builtin_bit_cast(uint64_t, v); }
+__device__ __forceinline__ int high(double v) { return (int)(__builtin_bit_cast(uint64_t, v) >> 32); }
+__device__ __forceinline__ double from_lane(double v, int lane) {
+  return with_words(__builtin_amdgcn_readlane(low(v), lane), __builtin_amdgcn_readlane(high(v), lane));
+}
+template <int CTRL, int ROW_MASK = 0xF>
+__device__ __forceinline__ double dpp_of(double v, double other) {
+  return with_words(__builtin_amdgcn_update_dpp(low(other), low(v), CTRL, ROW_MASK, 0xF, false),
+                    __builtin_amdgcn_update_dpp(high(other), high(v), CTRL, ROW_MASK, 0xF, false));
+}
+__device__ __forceinline__ double wave_max(double v) {
+  v = fmax(v, dpp_of<DPP_QP_XOR1>(v, v));
+  v = fmax(v, dpp_of<DPP_QP_XOR2>(v, v));
+  v = fmax(v, dpp_of<DPP_HALF_MIRROR>(v, v));
+  v = fmax(v, dpp_of<DPP_MIRROR>(v, v));
+  v = fmax(v, dpp_of<DPP_BCAST15, 0xA>(v, v));
+  v = fmax(v, dpp_of<DPP_BCAST31, 0xC>(v, v));
+  return from_lane(v, 63);
+}
+__device__ __forceinline__ double wave_total(double v) {
+  v += dpp_of<DPP_QP_XOR1>(v, 0.0);
+  v += dpp_of<DPP_QP_XOR2>(v, 0.0);
+  v += dpp_of<DPP_HALF_MIRROR>(v, 0.0);
+  v += dpp_of<DPP_MIRROR>(v, 0.0);
+  v += dpp_of<DPP_BCAST15, 0xA>(v, 0.0);
+  v += dpp_of<DPP_BCAST31, 0xC>(v, 0.0);
+  return from_lane(v, 63);
+}
+
+__device__ __forceinline__ float infinity(float) { return __builtin_inff(); }
+__device__ __forceinline__ double infinity(double) { return __builtin_inf(); }
+__device__ __forceinline__ float larger(float a, float b) { return fmaxf(a, b); }
+__device__ __forceinline__ double larger(double a, double b) { return fmax(a, b); }
+__device__ __forceinline__ float smaller(float a, float b) { return fminf(a, b); }
+__device__ __forceinline__ double smaller(double a, double b) { return fmin(a, b); }
+
+// The groups that stay, from the values x in s_v (minus infinity: none): a group's worth is its
+// best one, or with `pairs` the sum of its two best. L lanes, a power of two of them, look through
+// a group; bit g L of the result is group g. least, most: the least worth that stays, the most
+// that does not (minus infinity: none).
+template <typename F>
+__device__ __forceinline__ uint64_t groups_kept(const RouteArgs& a, const F* s_v, bool pairs, int L,
+                                                F& least, F& most) {
+  const int lane = threadIdx.x & 63;
+  const F NINF = -infinity(F());
+  const int per = a.E / a.groups, g = lane / L;
+  F b1 = NINF, b2 = NINF;
+  if (g < a.groups)
+    for (int i = lane % L; i < per; i += L) {
+      const F x = s_v[g * per + i];
+      b2 = larger(b2, smaller(b1, x));
+      b1 = larger(b1, x);
+    }
+  for (int o = L / 2; o; o >>= 1) {
+    const F o1 = __shfl_xor(b1, o), o2 = __shfl_xor(b2, o);
+    b2 = larger(larger(b2, o2), smaller(b1, o1));
+    b1 = larger(b1, o1);
+  }
+  const F worth = b1 + (pairs && b2 > NINF ? b2 : F(0));
+  int rank = 0;
+  for (int q = 0; q < a.groups; ++q) {
+    const F o = from_lane(worth, q * L);
+    rank += o > worth || (o == worth && q < g) ? 1 : 0;
+  }
+  const bool in = g < a.groups && rank < a.top_groups;
+  least = -wave_max(in ? -worth : NINF);
+  most = wave_max(g < a.groups && !in ? worth : NINF);
+  return __ballot(in);
+}
+
+// whether expert e's group stays
+__device__ __forceinline__ bool stays(const RouteArgs& a, uint64_t kept, int L, int e) {
+  // (e + 1/2) / per is at least 1 / (2 per) away from a whole number: rounding cannot cross it
+  const int g = (int)(((float)e + 0.5f) * ((float)a.groups / (float)a.E));
+  return e < a.E && ((kept >> (g * L)) & 1);
+}
+
+// Lane and value j of the lowest index that has `best`
+template <int J, typename F>
+__device__ __forceinline__ void lowest(const F (&c)[J], F best, int& lane, int& jat) {
+  uint64_t has = 0;
+  jat = 0;
+#pragma unroll
+  for (int j = 0; j < J; ++j) {
+    if (has == 0) {
+      has = __ballot(c[j] == best);
+      jat = j;
+    }
+  }
+  lane = __builtin_ctzll(has);
+}
+
+// The token's slots in lanes 0 .. k - 1: index (-1: none) and score
+struct Chosen {
+  int idx;
+  double w;
+};
+
+// The token in 64 bits. v: its logits (minus infinity: off); m: the largest of them.
+template <int J>
+__device__ Chosen route_exact(const RouteArgs& a, const float (&v)[J], float m, double* s_c, int L) {
+  const int lane = threadIdx.x & 63;
+  const double NINF = -__builtin_inf();
+  double c[J], sc[J];
+  if (a.score == 0) {
+    double sum = 0.0;
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      sc[j] = v[j] == -__builtin_inff() ? 0.0 : v[j] == m ? 1.0 : exp((double)v[j] - (double)m);
+      sum += sc[j];
+    }
+    sum = fmax(wave_total(sum), 1.0);
+#pragma unroll
+    for (int j = 0; j < J; ++j) sc[j] /= sum;
+  } else {
+#pragma unroll
+    for (int j = 0; j < J; ++j) sc[j] = 1.0 / (1.0 + exp(-(double)v[j]));
+  }
+#pragma unroll
+  for (int j = 0; j < J; ++j) {
+    const int e = lane + 64 * j;
+    double x = (double)v[j];
+    if (a.bias && e < a.E) x = sc[j] + (double)a.bias[e];
+    c[j] = v[j] > -__builtin_inff() && x == x ? x : NINF;
+  }
+  if (a.groups > 1) {
+    const bool pairs = a.group_top == 2;
+    wave_lds_sync();
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+      s_c[lane + 64 * j] = !pairs || a.bias ? c[j] : (c[j] > NINF ? sc[j] : NINF);
+    wave_lds_sync();
+    double least, most;
+    const uint64_t kept = groups_kept(a, s_c, pairs, L, least, most);
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+      if (!stays(a, kept, L, lane + 64 * j)) c[j] = NINF;
+  }
+  Chosen r{-1, 0.0};
+  for (int s = 0; s < a.k; ++s) {
+    double best = c[0];
+#pragma unroll
+    for (int j = 1; j < J; ++j) best = fmax(best, c[j]);
+    best = wave_max(best);
+    if (best == NINF) break;
+    int at, jat;
+    lowest<J>(c, best, at, jat);
+    double x = sc[0];
+#pragma unroll
+    for (int j = 1; j < J; ++j) x = jat == j ? sc[j] : x;
+    x = from_lane(x, at);
+    if (lane == s) {
+      r.idx = at + 64 * jat;
+      r.w = x;
+    }
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+      if (jat == j && lane == at) c[j] = NINF;
+  }
+  return r;
+}
+
+// Margins of 32-bit scores, twice what one is off. A sigmoid: its exponential, the sum and the
+// quotient lose 2^-24 of it each, at most two for the exponential; a bias' sum 2^-24 of 1 + its
+// magnitude: 6 2^-24 in all. A softmax: the argument down to -104 (below, it is zero) makes its
+// exponential off by up to 104 2^-24, but only where it is small: x e^-x is at most 0.37, so
+// 2^-24 of the largest score and those above with the longer sum: 16 2^-24; relative to itself,
+// where scores are compared without a bias, 128 2^-24.
+constexpr float MARGIN_SIGMOID = 0x1p-20f, MARGIN_SOFTMAX = 0x1p-19f;  // of 1 + the larger magnitude
+constexpr float MARGIN_ITSELF = 0x1p-16f;                              // of the larger one
+
+// J: experts per lane (E <= 64 J); BIAS: c = s + b
+template <typename T, int J, bool BIAS>
 __global__ __launch_bounds__(TPB) void k_route(RouteArgs a) {
   __shared__ double s_c[RWAVES][64 * J];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int t = blockIdx.x * RWAVES + wave;
   if (t >= a.T) return;
-  const double NINF = -__builtin_inf();
+  const float NINF = -__builtin_inff();
   const T* l = static_cast<const T*>(a.logits) + (size_t)t * a.ld;
-  double v[J], c[J], sc[J];
-  double m = NINF;
+  float v[J], c[J], sc[J], b[J];
 #pragma unroll
   for (int j = 0; j < J; ++j) {
     const int e = lane + 64 * j;
-    double x = e < a.E ? (double)to_f32(l[e]) : NINF;
+    const float x = e < a.E ? (float)l[e] : NINF;
+    b[j] = BIAS && e < a.E ? a.bias[e] : 0.f;
     v[j] = x == x ? x : NINF;  // NaN: off
-    m = fmax(m, v[j]);
   }
-  if (a.score == 0) {
-    for (int o = 32; o; o >>= 1) m = fmax(m, __shfl_xor(m, o));
-    double sum = 0.0;
+  float m = v[0];
 #pragma unroll
-    for (int j = 0; j < J; ++j) {
-      sc[j] = v[j] == NINF ? 0.0 : v[j] == m ? 1.0 : exp(v[j] - m);
-      sum += sc[j];
+  for (int j = 1; j < J; ++j) m = fmaxf(m, v[j]);
+  m = wave_max(m);
+  const bool soft = a.score == 0;
+  const bool pairs = a.groups > 1 && a.group_top == 2;
+  // all scores, where they are compared or their sum counts
+  float total = 1.f;
+  if (BIAS || pairs || (soft && !a.renorm)) {
+    if (soft) {
+      float sum = 0.f;
+#pragma unroll
+      for (int j = 0; j < J; ++j) {
+        sc[j] = v[j] == NINF ? 0.f : v[j] == m ? 1.f : expf(v[j] - m);
+        sum += sc[j];
+      }
+      total = fmaxf(wave_total(sum), 1.f);
+#pragma unroll
+      for (int j = 0; j < J; ++j) sc[j] = sc[j] / total;
+    } else {
+#pragma unroll
+      for (int j = 0; j < J; ++j) sc[j] = 1.f / (1.f + expf(-v[j]));
     }
-    for (int o = 32; o; o >>= 1) sum += __shfl_xor(sum, o);
-    sum = fmax(sum, 1.0);
-#pragma unroll
-    for (int j = 0; j < J; ++j) sc[j] /= sum;
   } else {
 #pragma unroll
-    for (int j = 0; j < J; ++j) sc[j] = 1.0 / (1.0 + exp(-v[j]));
+    for (int j = 0; j < J; ++j) sc[j] = 0.f;
   }
 #pragma unroll
   for (int j = 0; j < J; ++j) {
-    const int e = lane + 64 * j;
-    double x = v[j];
-    if (a.bias && e < a.E) x = sc[j] + (double)a.bias[e];
+    const float x = BIAS ? sc[j] + b[j] : v[j];
     c[j] = v[j] > NINF && x == x ? x : NINF;
   }
+  bool sure = true;
+  const float margin = soft ? MARGIN_SOFTMAX : MARGIN_SIGMOID;
+  const int L = a.groups > 1 ? 1 << (31 - __builtin_clz(64 / a.groups)) : 64;
   if (a.groups > 1) {
-    const int per = a.E / a.groups;
+    float* s_v = reinterpret_cast<float*>(s_c[wave]);
 #pragma unroll
     for (int j = 0; j < J; ++j)
-      s_c[wave][lane + 64 * j] =
-          a.group_top == 1 || a.bias ? c[j] : (v[j] > NINF ? sc[j] : NINF);
+      s_v[lane + 64 * j] = BIAS || !pairs ? c[j] : (v[j] > NINF ? sc[j] : NINF);
     wave_lds_sync();
-    double worth = NINF;
-    if (lane < a.groups) {
-      double b1 = NINF, b2 = NINF;
-      for (int i = 0; i < per; ++i) {
-        const double x = s_c[wave][lane * per + i];
-        if (x > b1) {
-          b2 = b1;
-          b1 = x;
-        } else if (x > b2) {
-          b2 = x;
-        }
-      }
-      worth = b1;
-      if (a.group_top == 2 && b2 > NINF) worth += b2;
-    }
-    int rank = 0;
-    for (int g = 0; g < a.groups; ++g) {
-      const double o = __shfl(worth, g);
-      rank += o > worth || (o == worth && g < lane) ? 1 : 0;
-    }
-    const uint64_t kept = __ballot(lane < a.groups && rank < a.top_groups);
+    float least, most;
+    const uint64_t kept = groups_kept(a, s_v, pairs, L, least, most);
+    if (BIAS) sure = most == NINF || least - most > 2.f * margin * (1.f + fabsf(most));
+    else if (pairs) sure = most == NINF || least - most > MARGIN_ITSELF * least;
 #pragma unroll
-    for (int j = 0; j < J; ++j) {
-      const int e = lane + 64 * j;
-      if (e < a.E && !((kept >> (e / per)) & 1)) c[j] = NINF;
-    }
+    for (int j = 0; j < J; ++j)
+      if (!stays(a, kept, L, lane + 64 * j)) c[j] = NINF;
   }
-  // the score of a chosen expert is read back by its slot's lane
-  wave_lds_sync();
-#pragma unroll
-  for (int j = 0; j < J; ++j) s_c[wave][lane + 64 * j] = sc[j];
-  wave_lds_sync();
   int mine = -1;
-  double w = 0.0;
-  for (int s = 0; s < a.k; ++s) {
-    double best = NINF;
-    int at = 0;
+  float won = 0.f;  // its logit, or with a bias its score
+  float before = __builtin_inff();
+  // with a bias one more than k: the last choice must be clear of the best one left out
+  const int rounds = BIAS ? a.k + 1 : a.k;
+  for (int s = 0; s < rounds; ++s) {
+    float best = c[0];
 #pragma unroll
-    for (int j = 0; j < J; ++j)
-      if (c[j] > best) {
-        best = c[j];
-        at = lane + 64 * j;
-      }
-    for (int o = 32; o; o >>= 1) {
-      const double ob = __shfl_xor(best, o);
-      const int oa = __shfl_xor(at, o);
-      if (ob > best || (ob == best && oa < at)) {
-        best = ob;
-        at = oa;
-      }
-    }
+    for (int j = 1; j < J; ++j) best = fmaxf(best, c[j]);
+    best = wave_max(best);
     if (best == NINF) break;
+    if (BIAS) {
+      if (s > 0 && !(before - best > margin * (1.f + fabsf(best)))) sure = false;
+      before = best;
+      if (!sure || s == a.k) break;
+    }
+    int at, jat;
+    lowest<J>(c, best, at, jat);
+    float val = best;
+    if (BIAS) {
+      float x = sc[0];
+#pragma unroll
+      for (int j = 1; j < J; ++j) x = jat == j ? sc[j] : x;
+      val = from_lane(x, at);
+    }
     if (lane == s) {
-      mine = at;
-      w = s_c[wave][at];
+      mine = at + 64 * jat;
+      won = val;
     }
 #pragma unroll
     for (int j = 0; j < J; ++j)
-      if (at == lane + 64 * j) c[j] = NINF;
+      if (jat == j && lane == at) c[j] = NINF;
   }
+  float w = won, sum = 1.f;
+  if (!BIAS) w = !soft ? 1.f / (1.f + expf(-won)) : won == m ? 1.f : expf(won - m);
+  if (!BIAS && soft && !a.renorm) w = w / total;
+  if (mine < 0) w = 0.f;
   if (a.renorm) {
-    double sum = w;
-    for (int o = 32; o; o >>= 1) sum += __shfl_xor(sum, o);
-    w = sum > 0.0 ? w / sum : 0.0;
+    sum = wave_total(w);
+    // scores that 32 bits do not hold beside each other: their quotients may still count
+    if (sum < 0x1p-20f && -wave_max(mine >= 0 ? -w : NINF) < 0x1p-100f) sure = false;
+  }
+  if (sure) {
+    if (a.renorm) w = sum > 0.f ? w / sum : 0.f;
+    w *= a.scale;
+  } else {
+    const Chosen r = route_exact<J>(a, v, m, s_c[wave], L);
+    mine = r.idx;
+    double x = r.w;
+    if (a.renorm) {
+      const double all = wave_total(x);
+      x = all > 0.0 ? x / all : 0.0;
+    }
+    w = (float)(x * (double)a.scale);
   }
   if (lane < a.k) {
     a.idx[(size_t)t * a.k + lane] = mine;
-    a.weights[(size_t)t * a.k + lane] = (float)(w * (double)a.scale);
+    a.weights[(size_t)t * a.k + lane] = w;
   }
+}
+
+template <typename T, int J>
+void route_launch(const RouteArgs& a, hipStream_t s) {
+  const dim3 grid((unsigned)(((int64_t)a.T + RWAVES - 1) / RWAVES)), block(TPB);
+  if (a.bias) k_route<T, J, true><<<grid, block, 0, s>>>(a);
+  else k_route<T, J, false><<<grid, block, 0, s>>>(a);
 }
 
 template <typename T>
 void route_launch(const RouteArgs& a, hipStream_t s) {
-  const dim3 grid((unsigned)(((int64_t)a.T + RWAVES - 1) / RWAVES)), block(TPB);
-  if (a.E <= 64) k_route<T, 1><<<grid, block, 0, s>>>(a);
-  else if (a.E <= 128) k_route<T, 2><<<grid, block, 0, s>>>(a);
-  else if (a.E <= 256) k_route<T, 4><<<grid, block, 0, s>>>(a);
-  else if (a.E <= 512) k_route<T, 8><<<grid, block, 0, s>>>(a);
-  else k_route<T, 16><<<grid, block, 0, s>>>(a);
+  if (a.E <= 64) route_launch<T, 1>(a, s);
+  else if (a.E <= 128) route_launch<T, 2>(a, s);
+  else if (a.E <= 192) route_launch<T, 3>(a, s);
+  else if (a.E <= 256) route_launch<T, 4>(a, s);
+  else if (a.E <= 512) route_launch<T, 8>(a, s);
+  else route_launch<T, 16>(a, s);
 }
 
 }  // namespace
