@@ -16,45 +16,69 @@ namespace {
 constexpr int DTPB = 1024;
 
 // sorted rows: offs[e] = first row of expert e (offs[E] = rows in all), src[row] = slot, and
-// the tile table (expert, first row), n_tiles
+// the tile table (expert, first row), n_tiles. One workgroup; a slot's place in its expert is what
+// the count of the expert gave it, kept in a register for the first KEEP slots of a thread.
 __global__ __launch_bounds__(DTPB) void k_sort(const int32_t* __restrict__ idx, int R, int E,
                                                int tile, int32_t* __restrict__ offs,
                                                int32_t* __restrict__ src,
                                                int32_t* __restrict__ tiles,
                                                int32_t* __restrict__ n_tiles) {
-  __shared__ int s_cnt[1024], s_at[1024], s_tile[1024];
-  const int tid = threadIdx.x;
+  constexpr int KEEP = 8;
+  __shared__ int s_cnt[1024], s_at[1024];
+  __shared__ int s_sum[2][DTPB / 64];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   s_cnt[tid] = 0;
   __syncthreads();
-  for (int i = tid; i < R; i += DTPB) {
-    const int e = idx[i];
-    if ((unsigned)e < (unsigned)E) atomicAdd(&s_cnt[e], 1);
+  int e[KEEP], rank[KEEP];
+#pragma unroll
+  for (int u = 0; u < KEEP; ++u) {
+    const int i = tid + u * DTPB;
+    e[u] = i < R ? idx[i] : -1;
+  }
+#pragma unroll
+  for (int u = 0; u < KEEP; ++u)
+    if ((unsigned)e[u] < (unsigned)E) rank[u] = atomicAdd(&s_cnt[e[u]], 1);
+  __syncthreads();
+  const int kept = s_cnt[tid];  // of the slots whose places are known
+  __syncthreads();
+  for (int i = tid + KEEP * DTPB; i < R; i += DTPB) {
+    const int q = idx[i];
+    if ((unsigned)q < (unsigned)E) atomicAdd(&s_cnt[q], 1);
   }
   __syncthreads();
-  if (tid == 0) {
-    int o = 0, t = 0;
-    for (int e = 0; e < E; ++e) {
-      s_at[e] = o;
-      s_tile[e] = t;
-      offs[e] = o;
-      o += s_cnt[e];
-      t += (s_cnt[e] + tile - 1) / tile;
-    }
-    offs[E] = o;
-    *n_tiles = t;
+  // running sums of rows and tiles over the experts
+  const int n = s_cnt[tid], nt = (n + tile - 1) / tile;
+  const int rows = wave_incl_scan(n), tls = wave_incl_scan(nt);
+  if (lane == 63) {
+    s_sum[0][wave] = rows;
+    s_sum[1][wave] = tls;
   }
   __syncthreads();
+  int o = rows - n, t = tls - nt;
+  for (int w = 0; w < wave; ++w) {
+    o += s_sum[0][w];
+    t += s_sum[1][w];
+  }
   if (tid < E) {
-    const int n = (s_cnt[tid] + tile - 1) / tile;
-    for (int i = 0; i < n; ++i) {
-      tiles[2 * (s_tile[tid] + i)] = tid;
-      tiles[2 * (s_tile[tid] + i) + 1] = s_at[tid] + i * tile;
+    offs[tid] = o;
+    for (int i = 0; i < nt; ++i) {
+      tiles[2 * (t + i)] = tid;
+      tiles[2 * (t + i) + 1] = o + i * tile;
     }
   }
+  if (tid == E - 1) {
+    offs[E] = o + n;
+    *n_tiles = t + nt;
+  }
+  s_at[tid] = o;
+  s_cnt[tid] = o + kept;  // where the slots that are counted again go on
   __syncthreads();
-  for (int i = tid; i < R; i += DTPB) {
-    const int e = idx[i];
-    if ((unsigned)e < (unsigned)E) src[atomicAdd(&s_at[e], 1)] = i;
+#pragma unroll
+  for (int u = 0; u < KEEP; ++u)
+    if ((unsigned)e[u] < (unsigned)E) src[s_at[e[u]] + rank[u]] = tid + u * DTPB;
+  for (int i = tid + KEEP * DTPB; i < R; i += DTPB) {
+    const int q = idx[i];
+    if ((unsigned)q < (unsigned)E) src[atomicAdd(&s_cnt[q], 1)] = i;
   }
 }
 
@@ -157,8 +181,7 @@ hipError_t run_experts(const ExpertsArgs& a, const void* x, int x_type, int64_t 
     const char* xc = static_cast<const char*>(x) + (size_t)t0 * ldx * esize(x_type);
     char* yc = static_cast<char*>(y) + (size_t)t0 * ldy * esize(y_type);
 
-    if (Tc == 1 && host::token_fused(a.d, a.f, k) &&
-        reinterpret_cast<uintptr_t>(xc) % (4 * esize(x_type)) == 0) {
+    if (Tc == 1 && host::token_fused(a.d, a.f, k)) {
       const hipError_t e = run_token(a, xc, x_type, ic, wc, k, yc, y_type, p, c, s);
       if (e != hipSuccess) return e;
       continue;

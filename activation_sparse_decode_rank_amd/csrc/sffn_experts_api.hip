@@ -88,7 +88,7 @@ size_t sparse_ffn_i8_matmul_work_bytes(int32_t x_dtype, int32_t M, int32_t N, in
   if ((!float_type(x_dtype) && x_dtype != SFFN_I8) || M < 0 || N < 1 || K < 1 ||
       K > SFFN_I8_MAX_K)
     return (size_t)-1;
-  if (M == 0) return 0;
+  if (M == 0 || (x_dtype != SFFN_I8 && sffn::host::i8_fused((size_t)M, K))) return 0;
   return sffn::host::i8_matmul_carve((size_t)M, K).bytes;
 }
 
@@ -109,15 +109,10 @@ int sparse_ffn_i8_matmul(const void* x, int32_t x_dtype, const float* x_scale, i
   if (!aligned(x, type_size(x_dtype)) || !aligned(y, type_size(y_dtype)) || !aligned(x_scale, 4) ||
       !aligned(w_scale, 4) || !aligned(bias, 4))
     return SFFN_ERR_INVALID;
-  const sffn::host::I8MatmulCarve c = sffn::host::i8_matmul_carve((size_t)M, K);
-  if (!work || !aligned(work, 256) || work_bytes < c.bytes) return SFFN_ERR_INVALID;
-  hipStream_t s = static_cast<hipStream_t>(stream);
-  char* p = static_cast<char*>(work);
-  const int kpad = sffn::host::i8_kpad(K);
   sffn::ProductArgs a{};
   a.cols = K;
   a.rows = M;
-  a.tile = sffn::host::i8_tile((size_t)M, 1);
+  a.tile = sffn::host::i8_tile((size_t)M, 1, (size_t)N);
   a.w = w;
   a.ldw = ldw;
   a.ws = w_scale;
@@ -127,13 +122,17 @@ int sparse_ffn_i8_matmul(const void* x, int32_t x_dtype, const float* x_scale, i
   a.out = y;
   a.ldo = ldy;
   a.out_type = y_dtype;
+  hipStream_t s = static_cast<hipStream_t>(stream);
   // few rows: held in 8 bits by the product's own workgroups
-  if (!i8 && sffn::host::i8_fused((size_t)M, K) && ldx % 4 == 0 &&
-      aligned(x, 4 * type_size(x_dtype))) {
+  if (!i8 && sffn::host::i8_fused((size_t)M, K)) {
     a.x = static_cast<const int8_t*>(x);
     a.ldx = ldx;
     return status(sffn::launch_product_fused(a, x_dtype, sffn::MODE_LINEAR, s));
   }
+  const sffn::host::I8MatmulCarve c = sffn::host::i8_matmul_carve((size_t)M, K);
+  if (!work || !aligned(work, 256) || work_bytes < c.bytes) return SFFN_ERR_INVALID;
+  char* p = static_cast<char*>(work);
+  const int kpad = sffn::host::i8_kpad(K);
   if (i8) {
     // rows on 16 bytes that need no zeros behind them: read in place, otherwise copied
     if (K % sffn::host::kI8Read == 0 && ldx % 16 == 0 && aligned(x, 16)) {

@@ -62,8 +62,7 @@ struct ProductArgs {
   int64_t w_group;        // bytes from an expert's w to the next one's
 };
 hipError_t launch_product(const ProductArgs& a, ProductMode mode, hipStream_t s);
-// The same where a.x holds rows of x_type values (a.cols of them, a.ldx elements apart, at
-// places of 4 elements), which the kernel holds in 8 bits itself (host::i8_fused). LINEAR: a.rows
+// The same where a.x holds rows of x_type values (a.cols of them, a.ldx elements apart), which the kernel holds in 8 bits itself (host::i8_fused). LINEAR: a.rows
 // rows. ACT, ACT_GATED: one token, a.src is its idx [k] and slot s gives row s of out.
 hipError_t launch_product_fused(const ProductArgs& a, int x_type, ProductMode mode, hipStream_t s);
 // One token's down products and their weighted sum: a.x holds fp32 rows h (a.cols values, a.ldx

@@ -59,14 +59,13 @@ __device__ __forceinline__ unsigned wg_max(unsigned v, unsigned* s_max) {
   return v;
 }
 
-// Four values of a row from element 4 i on, and past `cols` zeros. VEC: the row starts at a
-// multiple of four elements' size.
-template <typename T, bool VEC>
+// Four values of a row from element 4 i on, and past `cols` zeros
+template <typename T>
 __device__ __forceinline__ float4_t load4(const T* x, int i, int cols) {
-  typedef T vec __attribute__((ext_vector_type(4)));
+  typedef T vec __attribute__((ext_vector_type(4), aligned(sizeof(T))));
   float4_t v = {0.f, 0.f, 0.f, 0.f};
-  if (VEC && 4 * i + 4 <= cols) {
-    const vec t = reinterpret_cast<const vec*>(x)[i];
+  if (4 * i + 4 <= cols) {
+    const vec t = *reinterpret_cast<const vec*>(x + 4 * i);
 #pragma unroll
     for (int e = 0; e < 4; ++e) v[e] = (float)t[e];
   } else {
@@ -101,7 +100,7 @@ __device__ __forceinline__ int quantize4(const float4_t& v, float s, float r) {
 
 // A workgroup of W waves takes a row. NV groups of four values per thread stay in registers
 // between the maximum and the rounding, so the row is read once (NV = 0: longer rows, twice).
-template <typename T, bool VEC, int W, int NV>
+template <typename T, int W, int NV>
 __global__ __launch_bounds__(W * 64) void k_quantize(QuantArgs a) {
   constexpr int TH = W * 64;
   __shared__ unsigned s_max[W];
@@ -115,14 +114,14 @@ __global__ __launch_bounds__(W * 64) void k_quantize(QuantArgs a) {
     float4_t v[NV > 0 ? NV : 1];
     if constexpr (NV > 0) {
 #pragma unroll
-      for (int u = 0; u < NV; ++u) v[u] = load4<T, VEC>(x, threadIdx.x + u * TH, a.cols);
+      for (int u = 0; u < NV; ++u) v[u] = load4<T>(x, threadIdx.x + u * TH, a.cols);
 #pragma unroll
       for (int u = 0; u < NV; ++u)
 #pragma unroll
         for (int e = 0; e < 4; ++e) m = max(m, mag(v[u][e]));
     } else {
       for (int i = threadIdx.x; i < nq; i += TH) {
-        const float4_t t = load4<T, VEC>(x, i, a.cols);
+        const float4_t t = load4<T>(x, i, a.cols);
 #pragma unroll
         for (int e = 0; e < 4; ++e) m = max(m, mag(t[e]));
       }
@@ -138,7 +137,7 @@ __global__ __launch_bounds__(W * 64) void k_quantize(QuantArgs a) {
       }
     } else {
       for (int i = threadIdx.x; i < nq; i += TH)
-        q[i] = s > 0.f ? quantize4(load4<T, VEC>(x, i, a.cols), s, r) : 0;
+        q[i] = s > 0.f ? quantize4(load4<T>(x, i, a.cols), s, r) : 0;
     }
   }
 }
@@ -330,7 +329,7 @@ struct RowsToLds {
     kept = nq <= KEEP * step;
     if (kept && row < M) {
 #pragma unroll
-      for (int u = 0; u < KEEP; ++u) v[u] = load4<X, true>(xr, i0 + u * step, cols);
+      for (int u = 0; u < KEEP; ++u) v[u] = load4<X>(xr, i0 + u * step, cols);
     }
   }
   // s_q [M][kpad]; s_max: M cleared words; returns the scale of row lane % 16 (row 0 past the last)
@@ -346,7 +345,7 @@ struct RowsToLds {
           for (int e = 0; e < 4; ++e) m = max(m, mag(v[u][e]));
       } else {
         for (int i = i0; i < nq; i += step) {
-          const float4_t t = load4<X, true>(xr, i, cols);
+          const float4_t t = load4<X>(xr, i, cols);
 #pragma unroll
           for (int e = 0; e < 4; ++e) m = max(m, mag(t[e]));
         }
@@ -364,7 +363,7 @@ struct RowsToLds {
           if (i0 + u * step < nq) q[i0 + u * step] = s > 0.f ? quantize4(v[u], s, r) : 0;
       } else {
         for (int i = i0; i < nq; i += step)
-          q[i] = s > 0.f ? quantize4(load4<X, true>(xr, i, cols), s, r) : 0;
+          q[i] = s > 0.f ? quantize4(load4<X>(xr, i, cols), s, r) : 0;
       }
     }
     return row_scale(s_max[(lane & 15) < M ? lane & 15 : 0], r);
@@ -653,7 +652,7 @@ __global__ __launch_bounds__(TD_W * 64) void k_token_down(ProductArgs a, const f
     for (int u = 0; u < KEEP; ++u) {
       const int i = tid + u * TH;
       const int s = by_nq(i);
-      if (i < groups) v[u] = load4<float, true>(h + (size_t)s * a.ldx, i - s * nq, a.cols);
+      if (i < groups) v[u] = load4<float>(h + (size_t)s * a.ldx, i - s * nq, a.cols);
     }
   }
   unsigned most = 0;  // this wave's share of slot wave % k's maxima
@@ -728,7 +727,7 @@ __global__ __launch_bounds__(TD_W * 64) void k_token_down(ProductArgs a, const f
       if (tid + u * TH < groups) put(tid + u * TH, v[u]);
   } else {
     for (int i = tid; i < groups; i += TH)
-      put(i, load4<float, true>(h + (size_t)by_nq(i) * a.ldx, i - by_nq(i) * nq, a.cols));
+      put(i, load4<float>(h + (size_t)by_nq(i) * a.ldx, i - by_nq(i) * nq, a.cols));
   }
   lds_barrier();
   int4_t acc = {0, 0, 0, 0};
@@ -1011,27 +1010,25 @@ void product_launch(const ProductArgs& a, hipStream_t s) {
   } else if (a.tile == 32) {
     few_launch<MODE, 2, void>(a, tiles, 0, s);
   } else {
-    if (a.tile == 64) tile_launch<MODE, 256, 64, 4, 2, 2>(a, tiles, s);
+    // Channels of a tile of 64 rows: 128, or 64 where those would leave compute units without work
+    // (333 x 1013 x 1101: 6.6 us, 9.0 with 128, 14.8 with 256 x 128; 64 experts of 65 rows, d 2048,
+    // d_ffn 1408: 104 + 61 us with 128, 121 + 68 with 64, 111 + 67 with 256 x 128).
+    const int rows_w = a.n * (MODE == MODE_ACT_GATED ? 2 : 1);
+    if (a.tile == 64 && tiles * ((rows_w + 127) / 128) < 512) tile_launch<MODE, 64, 64, 2, 2, 4>(a, tiles, s);
+    else if (a.tile == 64) tile_launch<MODE, 128, 64, 2, 2, 3>(a, tiles, s);
     else if (a.tile == 128) tile_launch<MODE, 256, 128, 4, 2, 3>(a, tiles, s);
     else tile_launch<MODE, 256, 256, 2, 4, 2>(a, tiles, s);
   }
 }
 
-template <typename T, bool VEC>
-void quantize_rows(const QuantArgs& a, hipStream_t s) {
-  const dim3 grid((unsigned)std::min(a.rows, 1 << 20));
-  const int nq = a.kpad / 4;
-  if (nq <= 4 * 64) k_quantize<T, VEC, 1, 4><<<grid, dim3(64), 0, s>>>(a);
-  else if (nq <= 4 * 256) k_quantize<T, VEC, 4, 4><<<grid, dim3(256), 0, s>>>(a);
-  else if (nq <= 4 * 1024) k_quantize<T, VEC, 16, 4><<<grid, dim3(1024), 0, s>>>(a);
-  else k_quantize<T, VEC, 16, 0><<<grid, dim3(1024), 0, s>>>(a);
-}
-
 template <typename T>
 void quantize_launch(const QuantArgs& a, hipStream_t s) {
-  const bool vec = reinterpret_cast<uintptr_t>(a.x) % (4 * sizeof(T)) == 0 && a.ldx % 4 == 0;
-  if (vec) quantize_rows<T, true>(a, s);
-  else quantize_rows<T, false>(a, s);
+  const dim3 grid((unsigned)std::min(a.rows, 1 << 20));
+  const int nq = a.kpad / 4;
+  if (nq <= 4 * 64) k_quantize<T, 1, 4><<<grid, dim3(64), 0, s>>>(a);
+  else if (nq <= 4 * 256) k_quantize<T, 4, 4><<<grid, dim3(256), 0, s>>>(a);
+  else if (nq <= 4 * 1024) k_quantize<T, 16, 4><<<grid, dim3(1024), 0, s>>>(a);
+  else k_quantize<T, 16, 0><<<grid, dim3(1024), 0, s>>>(a);
 }
 
 template <int MODE, typename X>

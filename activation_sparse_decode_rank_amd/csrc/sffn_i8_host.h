@@ -17,10 +17,18 @@ constexpr int kI8Read = 128;
 inline int i8_kpad(int K) { return (int)up_to((size_t)K, kI8Step); }
 
 // Rows of a product tile, from the mean rows of a group (of the whole product where there are
-// no groups).
-inline int i8_tile(size_t rows, size_t groups) {
+// no groups) and the rows of w. Up to 32 the weights are streamed past them; above, the largest
+// tile that still gives the device's 256 compute units (half of it, at most, idle at the end) two
+// rounds of work, since larger tiles read less.
+inline int i8_tile(size_t rows, size_t groups, size_t rows_w) {
   const size_t mean = (rows + groups - 1) / groups;
-  return mean <= 16 ? 16 : mean <= 32 ? 32 : mean <= 64 ? 64 : mean <= 512 ? 128 : 256;
+  if (mean <= 32) return mean <= 16 ? 16 : 32;
+  auto tiles = [&](size_t t, size_t ch) {
+    return groups * ((mean + t - 1) / t) * ((rows_w + ch - 1) / ch);
+  };
+  if (mean > 192 && tiles(256, 256) >= 512) return 256;
+  if (mean > 96 && tiles(128, 256) >= 512) return 128;
+  return 64;
 }
 
 // Whether M rows of K values are held in 8 bits by the product itself: every workgroup does it
@@ -74,7 +82,7 @@ inline ExpertsCarve experts_carve(int E, int d, int f, size_t T, size_t k) {
     o += up_to(bytes, 256);
     return at;
   };
-  c.tile = i8_tile(R, std::min(R, (size_t)E));
+  c.tile = i8_tile(R, std::min(R, (size_t)E), (size_t)std::min(f, d));
   c.max_tiles = (int)experts_max_tiles(R, (size_t)E, c.tile);
   c.ldh = up_to((size_t)f, 64);
   c.ldp = up_to((size_t)d, 64);

@@ -19,46 +19,57 @@ from . import _native as N
 _TYPES = {torch.float32: N.SFFN_F32, torch.float16: N.SFFN_F16, torch.bfloat16: N.SFFN_BF16}
 _SCORES = {"softmax": N.SFFN_SCORE_SOFTMAX, "sigmoid": N.SFFN_SCORE_SIGMOID}
 _CHUNK_ROWS = 32768  # slots whose scratch is allocated at once when the caller passes none
+# the handle of a device's current stream, without the object around it where torch offers that
+_current = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+_I32, _F32, _I8, _U8 = torch.int32, torch.float32, torch.int8, torch.uint8
 
 
 class _on:
     """The device of a tensor made current for a call, and the stream the call goes to: the
     given one (of that device) or the device's current one. Tensors that the call allocates on
-    another stream's pool are marked as used on this one (`own`)."""
+    another stream's pool are marked as used on this one (`own`). Closed by `done`."""
+
+    __slots__ = ("device", "handle", "_back", "_other")
 
     def __init__(self, t: torch.Tensor, stream):
-        if not t.is_cuda:
+        self.device = dev = t.device
+        if dev.type != "cuda":
             raise ValueError("device tensors are needed")
-        self.device = t.device
         here = torch.cuda.current_device()
-        self._back = here if here != t.device.index else None
-        if self._back is not None:
-            torch.cuda.set_device(t.device)
+        self._back = self._other = None
+        if stream is not None and stream.device != dev:
+            raise ValueError(f"a stream of {stream.device} for tensors on {dev}")
+        if here != dev.index:
+            self._back = here
+            torch.cuda.set_device(dev)
         if stream is None:
-            self.stream, self._other = torch.cuda.current_stream(), None
+            self.handle = _current(dev.index)
         else:
-            if stream.device != t.device:
-                self.__exit__()
-                raise ValueError(f"a stream of {stream.device} for tensors on {t.device}")
-            self.stream, self._other = stream, stream
+            self.handle = stream.cuda_stream
+            if stream != torch.cuda.current_stream(dev):
+                self._other = stream
 
     def own(self, t: torch.Tensor) -> torch.Tensor:
-        if self._other is not None and self._other != torch.cuda.current_stream():
+        if self._other is not None:
             t.record_stream(self._other)
         return t
+
+    def empty(self, shape, dtype) -> torch.Tensor:
+        t = torch.empty(shape, dtype=dtype, device=self.device)
+        if self._other is not None:
+            t.record_stream(self._other)
+        return t
+
+    def done(self):
+        if self._back is not None:
+            torch.cuda.set_device(self._back)
 
     def __enter__(self):
         return self
 
     def __exit__(self, *exc):
-        if self._back is not None:
-            torch.cuda.set_device(self._back)
-
-
-def _same_device(dev, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, not on {dev}")
+        self.done()
 
 
 def _rows(t: torch.Tensor, name: str) -> Tuple[int, int]:
@@ -66,47 +77,49 @@ def _rows(t: torch.Tensor, name: str) -> Tuple[int, int]:
     if t.dim() != 2:
         raise ValueError(f"{name} must have two dimensions")
     R, K = t.shape
-    if K > 1 and t.stride(1) != 1:
+    ld, one = t.stride()
+    if one != 1 and K > 1:
         raise ValueError(f"the rows of {name} must be contiguous")
-    if R > 1:
-        ld = t.stride(0)
-        if ld < K:
-            raise ValueError(f"the rows of {name} overlap")
-    else:
-        ld = K
+    if R <= 1:
+        return R, K
+    if ld < K:
+        raise ValueError(f"the rows of {name} overlap")
     return R, ld
 
 
-def _float(t: torch.Tensor, name: str) -> int:
-    if t.dtype not in _TYPES:
+def _type(t: torch.Tensor, name: str) -> int:
+    dt = _TYPES.get(t.dtype)
+    if dt is None:
         raise ValueError(f"{name} must be float32, float16 or bfloat16")
-    return _TYPES[t.dtype]
+    return dt
 
 
-def _vector(t: Optional[torch.Tensor], shape, dtype, name: str) -> Optional[int]:
+def _vector(t: Optional[torch.Tensor], shape, dtype, dev, name: str) -> Optional[int]:
     if t is None:
         return None
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}")
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or t.device != dev:
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {dev}")
     return t.data_ptr()
 
 
-def _i8_rows(w: torch.Tensor, name: str) -> int:
+def _i8_rows(w: torch.Tensor, dev, name: str) -> int:
     """The row distance of an int8 tensor [..., K] whose rows all lie the same distance
     apart, at multiples of 16 bytes, with room to the next multiple behind the last one."""
-    if w.dtype != torch.int8:
-        raise ValueError(f"{name} must be int8")
-    K = w.shape[-1]
+    if w.dtype != _I8 or w.device != dev:
+        raise ValueError(f"{name} must be int8 on {dev}")
+    shape, strides = w.shape, w.stride()
+    K = shape[-1]
     need = (K + 15) // 16 * 16
-    if K > 1 and w.stride(-1) != 1:
+    if strides[-1] != 1 and K > 1:
         raise ValueError(f"the rows of {name} must be contiguous")
     ld, rows = None, 1
-    for n, st in zip(reversed(w.shape[:-1]), reversed(w.stride()[:-1])):
+    for i in range(len(shape) - 2, -1, -1):
+        n = shape[i]
         if n == 1:
             continue
         if ld is None:
-            ld = st // rows if st % rows == 0 else -1
-        if st != ld * rows:
+            ld = strides[i]
+        elif strides[i] != ld * rows:
             raise ValueError(f"the rows of {name} must lie the same distance apart")
         rows *= n
     if ld is None:
@@ -114,27 +127,33 @@ def _i8_rows(w: torch.Tensor, name: str) -> int:
     if ld % 16 or ld < need or w.data_ptr() % 16:
         raise ValueError(f"the rows of {name} must begin at multiples of 16 bytes "
                          "(quantize_rows lays them out so)")
-    last = w.storage_offset() + (rows - 1) * ld + need
-    if last > w.untyped_storage().nbytes():
+    if K != need and w.storage_offset() + (rows - 1) * ld + need > w.untyped_storage().nbytes():
         raise ValueError(f"{name} ends inside a 16-byte block: its rows need room up to the "
                          "next multiple of 16 (quantize_rows lays them out so)")
     return ld
 
 
-def _out(given, shape, dtype, dev, name):
+def _out(given, on, shape, dtype, name):
     if given is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
-    if given.dtype != dtype or tuple(given.shape) != tuple(shape):
-        raise ValueError(f"{name} must be {dtype} of shape {tuple(shape)}")
-    return given
+        return on.empty(shape, dtype)
+    if given.dtype != dtype or given.shape != shape or given.device != on.device:
+        raise ValueError(f"{name} must be {dtype} of shape {tuple(shape)} on {on.device}")
+    return on.own(given)
 
 
-def _work(given, nbytes, dev):
-    if given is None:
-        return torch.empty(nbytes, dtype=torch.uint8, device=dev)
-    if given.dtype != torch.uint8 or given.dim() != 1 or not given.is_contiguous():
-        raise ValueError("work must be a contiguous uint8 tensor")
-    return given
+def _work(given, on):
+    if given.dtype != _U8 or given.dim() != 1 or not given.is_contiguous() or given.device != on.device:
+        raise ValueError(f"work must be a contiguous uint8 tensor on {on.device}")
+    return on.own(given)
+
+
+def _out_dtype(out_dtype, y, default):
+    if out_dtype is None:
+        out_dtype = default if y is None else y.dtype
+    dt = _TYPES.get(out_dtype)
+    if dt is None:
+        raise ValueError("out_dtype must be float32, float16 or bfloat16")
+    return out_dtype, dt
 
 
 def route(logits: torch.Tensor, k: int, *, score: str = "softmax",
@@ -149,21 +168,20 @@ def route(logits: torch.Tensor, k: int, *, score: str = "softmax",
     neighbouring experts, each worth its best score (group_top 1) or the sum of its two best
     (2); renormalize: divide the chosen scores by their sum; scale: times this. Experts at
     minus infinity or NaN are never chosen; slots without an expert hold -1 and weight 0."""
-    dt = _float(logits, "logits")
+    dt = _type(logits, "logits")
     T, ld = _rows(logits, "logits")
     E = logits.shape[1]
-    if score not in _SCORES:
+    how = _SCORES.get(score)
+    if how is None:
         raise ValueError("score must be 'softmax' or 'sigmoid'")
     with _on(logits, stream) as on:
-        _same_device(on.device, bias=bias, idx=idx, weights=weights)
-        b = _vector(bias, (E,), torch.float32, "bias")
-        idx = on.own(_out(idx, (T, k), torch.int32, on.device, "idx"))
-        weights = on.own(_out(weights, (T, k), torch.float32, on.device, "weights"))
+        b = None if bias is None else _vector(bias, (E,), _F32, on.device, "bias")
+        idx = _out(idx, on, (T, k), _I32, "idx")
+        weights = _out(weights, on, (T, k), _F32, "weights")
         if not idx.is_contiguous() or not weights.is_contiguous():
             raise ValueError("idx and weights must be contiguous")
-        N.sparse_ffn_route(logits.data_ptr(), dt, ld, T, E, k, _SCORES[score], b, groups,
-                           top_groups, group_top, int(bool(renormalize)), scale, idx.data_ptr(),
-                           weights.data_ptr(), on.stream.cuda_stream)
+        N.sparse_ffn_route(logits.data_ptr(), dt, ld, T, E, k, how, b, groups, top_groups, group_top,
+                           1 if renormalize else 0, scale, idx.data_ptr(), weights.data_ptr(), on.handle)
     return idx, weights
 
 
@@ -171,19 +189,24 @@ def quantize_rows(x: torch.Tensor, stream=None) -> Tuple[torch.Tensor, torch.Ten
     """The rows of x ([..., K]) held in 8 bits: whole numbers q (int8, same shape) and scales
     (fp32 [...]) with x about q * scale (sparse_ffn_quantize_rows). q's rows begin at
     multiples of 16 bytes, as the products want them."""
-    dt = _float(x, "x")
+    dt = _type(x, "x")
     if x.dim() < 1 or x.shape[-1] < 1:
         raise ValueError("x must have rows of at least one value")
     K = x.shape[-1]
     ldq = (K + 15) // 16 * 16
     with _on(x, stream) as on:
-        with torch.cuda.stream(on.stream):  # a copy, where x's rows need one, is made there
-            flat = on.own((x if x.dim() == 2 and x.stride(1) == 1 else x.contiguous()).reshape(-1, K))
+        flat = x if x.dim() == 2 and x.stride(1) == 1 else None
+        if flat is None:
+            if x.is_contiguous():
+                flat = x.view(-1, K)
+            else:  # the copy is made where the call runs
+                with torch.cuda.stream(stream):
+                    flat = x.contiguous().view(-1, K)
         R, ld = _rows(flat, "x")
-        q = on.own(torch.empty((*x.shape[:-1], ldq), dtype=torch.int8, device=on.device))
-        scale = on.own(torch.empty(x.shape[:-1], dtype=torch.float32, device=on.device))
+        q = on.empty((*x.shape[:-1], ldq), _I8)
+        scale = on.empty(x.shape[:-1], _F32)
         N.sparse_ffn_quantize_rows(flat.data_ptr(), dt, ld, R, K, q.data_ptr(), ldq,
-                                   scale.data_ptr(), on.stream.cuda_stream)
+                                   scale.data_ptr(), on.handle)
     return q[..., :K], scale
 
 
@@ -196,61 +219,60 @@ def i8_matmul(x: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor, *,
     holds in 8 bits first, or int8 rows with x_scale fp32 [M]. out_dtype: float32, float16 or
     bfloat16 (default: x's type; float32 for int8 rows). work: uint8 scratch (allocated here
     when None); calls that share one must be ordered."""
-    i8 = x.dtype == torch.int8
+    i8 = x.dtype == _I8
     if i8 != (x_scale is not None):
         raise ValueError("x_scale belongs to int8 rows, and they need it")
-    dt = N.SFFN_I8 if i8 else _float(x, "x")
+    dt = N.SFFN_I8 if i8 else _type(x, "x")
     M, ldx = _rows(x, "x")
     K = x.shape[1]
     if w.dim() != 2 or w.shape[1] != K:
         raise ValueError(f"w must be [N, {K}]")
     n = w.shape[0]
-    ldw = _i8_rows(w, "w")
-    if y is not None:
-        out_dtype = y.dtype if out_dtype is None else out_dtype
-    elif out_dtype is None:
-        out_dtype = torch.float32 if i8 else x.dtype
-    if out_dtype not in _TYPES:
-        raise ValueError("out_dtype must be float32, float16 or bfloat16")
+    out_dtype, yt = _out_dtype(out_dtype, y, _F32 if i8 else x.dtype)
     with _on(x, stream) as on:
-        _same_device(on.device, w=w, w_scale=w_scale, x_scale=x_scale, bias=bias, y=y, work=work)
-        ws = _vector(w_scale, (n,), torch.float32, "w_scale")
-        xs = _vector(x_scale, (M,), torch.float32, "x_scale")
-        b = _vector(bias, (n,), torch.float32, "bias")
-        y = on.own(_out(y, (M, n), out_dtype, on.device, "y"))
-        ldy = _rows(y, "y")[1]
-        need = N.sparse_ffn_i8_matmul_work_bytes(dt, M, n, K)
-        if need > 1 << 62:
-            raise N.SparseFFNError(N.SFFN_ERR_UNSUPPORTED, "sparse_ffn_i8_matmul")
-        if work is not None or need:
-            work = on.own(_work(work, need, on.device))
+        dev = on.device
+        ldw = _i8_rows(w, dev, "w")
+        ws = _vector(w_scale, (n,), _F32, dev, "w_scale")
+        xs = None if x_scale is None else _vector(x_scale, (M,), _F32, dev, "x_scale")
+        b = None if bias is None else _vector(bias, (n,), _F32, dev, "bias")
+        if y is None:
+            y, ldy = on.empty((M, n), out_dtype), n
+        else:
+            y = _out(y, on, (M, n), out_dtype, "y")
+            ldy = _rows(y, "y")[1]
+        if work is None:
+            need = N.sparse_ffn_i8_matmul_work_bytes(dt, M, n, K)
+            if need > 1 << 62:
+                raise N.SparseFFNError(N.SFFN_ERR_UNSUPPORTED, "sparse_ffn_i8_matmul")
+            if need:
+                work = on.empty(need, _U8)
+        else:
+            work = _work(work, on)
         N.sparse_ffn_i8_matmul(x.data_ptr(), dt, xs, ldx, M, K, w.data_ptr(), ldw, ws, b, n,
-                               y.data_ptr(), _TYPES[out_dtype], ldy,
-                               None if work is None else work.data_ptr(),
-                               0 if work is None else work.numel(), on.stream.cuda_stream)
+                               y.data_ptr(), yt, ldy, None if work is None else work.data_ptr(),
+                               0 if work is None else work.numel(), on.handle)
     return y
 
 
 def _experts_desc(w_act, act_scale, w_down, down_scale, b_act) -> N.SffnExpertsDesc:
-    if w_act.dim() not in (3, 4) or (w_act.dim() == 4 and w_act.shape[2] != 2):
+    shape = w_act.shape
+    gated = len(shape) == 4
+    if len(shape) not in (3, 4) or (gated and shape[2] != 2):
         raise ValueError("w_act must be [E, d_ffn, d], or [E, d_ffn, 2, d] for the gated form")
-    E, f, d = w_act.shape[0], w_act.shape[1], w_act.shape[-1]
-    if tuple(w_down.shape) != (E, d, f):
+    E, f, d = shape[0], shape[1], shape[-1]
+    if w_down.shape != (E, d, f):
         raise ValueError(f"w_down must be {(E, d, f)}")
-    _same_device(w_act.device, act_scale=act_scale, w_down=w_down, down_scale=down_scale,
-                 b_act=b_act)
-    D = N.SffnExpertsDesc()
-    D.experts, D.d, D.d_ffn, D.gated = E, d, f, int(w_act.dim() == 4)
-    D.w_act, D.ld_act = w_act.data_ptr(), _i8_rows(w_act, "w_act")
-    D.act_scale = _vector(act_scale, w_act.shape[:-1], torch.float32, "act_scale")
-    D.b_act = _vector(b_act, (E, f), torch.float32, "b_act")
-    D.w_down, D.ld_down = w_down.data_ptr(), _i8_rows(w_down, "w_down")
-    D.down_scale = _vector(down_scale, (E, d), torch.float32, "down_scale")
-    return D
+    dev = w_act.device
+    return N.SffnExpertsDesc(
+        E, d, f, gated, w_act.data_ptr(), _i8_rows(w_act, dev, "w_act"),
+        _vector(act_scale, shape[:-1], _F32, dev, "act_scale"),
+        None if b_act is None else _vector(b_act, (E, f), _F32, dev, "b_act"),
+        w_down.data_ptr(), _i8_rows(w_down, dev, "w_down"),
+        _vector(down_scale, (E, d), _F32, dev, "down_scale"))
 
 
-def _experts_call(D, x, idx, weights, out_dtype, y, work, stream):
-    dt = _float(x, "x")
+def _experts_call(D, w_device, x, idx, weights, out_dtype, y, work, stream):
+    dt = _type(x, "x")
     T, ldx = _rows(x, "x")
     d = D.d
     if x.shape[1] != d:
@@ -258,28 +280,28 @@ def _experts_call(D, x, idx, weights, out_dtype, y, work, stream):
     if idx.dim() != 2 or idx.shape[0] != T:
         raise ValueError(f"idx must be [{T}, k]")
     k = idx.shape[1]
-    if y is not None:
-        out_dtype = y.dtype if out_dtype is None else out_dtype
-    elif out_dtype is None:
-        out_dtype = x.dtype
-    if out_dtype not in _TYPES:
-        raise ValueError("out_dtype must be float32, float16 or bfloat16")
+    out_dtype, yt = _out_dtype(out_dtype, y, x.dtype)
     with _on(x, stream) as on:
-        _same_device(on.device, idx=idx, weights=weights, y=y, work=work)
-        ip = _vector(idx, (T, k), torch.int32, "idx")
-        wp = _vector(weights, (T, k), torch.float32, "weights")
-        y = on.own(_out(y, (T, d), out_dtype, on.device, "y"))
-        ldy = _rows(y, "y")[1]
-        if work is None and T:
+        dev = on.device
+        if dev != w_device:
+            raise ValueError(f"x is on {dev}, the experts on {w_device}")
+        ip = _vector(idx, (T, k), _I32, dev, "idx")
+        wp = _vector(weights, (T, k), _F32, dev, "weights")
+        if y is None:
+            y, ldy = on.empty((T, d), out_dtype), d
+        else:
+            y = _out(y, on, (T, d), out_dtype, "y")
+            ldy = _rows(y, "y")[1]
+        if work is not None:
+            work = _work(work, on)
+        elif T:
             need = N.sparse_ffn_experts_work_bytes(D, min(T, max(1, _CHUNK_ROWS // max(k, 1))), k)
             if need == 0:
                 raise N.SparseFFNError(N.SFFN_ERR_UNSUPPORTED, "sparse_ffn_experts")
-            work = on.own(torch.empty(need, dtype=torch.uint8, device=on.device))
-        elif work is not None:
-            work = on.own(_work(work, 0, on.device))
-        N.sparse_ffn_experts(D, x.data_ptr(), dt, ldx, T, ip, wp, k, y.data_ptr(),
-                             _TYPES[out_dtype], ldy, None if work is None else work.data_ptr(),
-                             0 if work is None else work.numel(), on.stream.cuda_stream)
+            work = on.empty(need, _U8)
+        N.sparse_ffn_experts(D, x.data_ptr(), dt, ldx, T, ip, wp, k, y.data_ptr(), yt, ldy,
+                             None if work is None else work.data_ptr(),
+                             0 if work is None else work.numel(), on.handle)
     return y
 
 
@@ -296,8 +318,7 @@ def experts(x: torch.Tensor, idx: torch.Tensor, weights: torch.Tensor, w_act: to
     b_act fp32 [E, d_ffn]: bias inside the ReLU. out_dtype: default x's type. work: scratch
     from experts_work (allocated here when None); calls that share one must be ordered."""
     D = _experts_desc(w_act, act_scale, w_down, down_scale, b_act)
-    _same_device(x.device, w_act=w_act)
-    return _experts_call(D, x, idx, weights, out_dtype, y, work, stream)
+    return _experts_call(D, w_act.device, x, idx, weights, out_dtype, y, work, stream)
 
 
 def experts_work(w_act: torch.Tensor, w_down: torch.Tensor, tokens: int, k: int) -> torch.Tensor:
@@ -343,14 +364,13 @@ class ExpertFFN:
         return experts_work(self.w_act, self.w_down, tokens, k)
 
     def __call__(self, x, idx, weights, *, out_dtype=None, y=None, work=None, stream=None):
-        _same_device(x.device, w_act=self.w_act)
-        return _experts_call(self.desc, x, idx, weights, out_dtype, y, work, stream)
+        return _experts_call(self.desc, self.w_act.device, x, idx, weights, out_dtype, y, work, stream)
 
     def dense(self, x, *, out_dtype=None, y=None, work=None, stream=None):
         """The FFN of the layer's one expert for every row of x (E = 1)."""
         if self.n_experts != 1:
             raise ValueError("dense needs a layer of one expert")
-        with _on(x, stream) as on, torch.cuda.stream(on.stream):
+        with _on(x, stream), torch.cuda.stream(stream):
             idx = torch.zeros((x.shape[0], 1), dtype=torch.int32, device=x.device)
             one = torch.ones((x.shape[0], 1), dtype=torch.float32, device=x.device)
             return self(x, idx, one, out_dtype=out_dtype, y=y, work=work, stream=stream)

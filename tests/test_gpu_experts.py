@@ -320,7 +320,7 @@ def test_matmul_refusals(P):
     with pytest.raises(ValueError):  # no room behind the last row
         P.i8_matmul(x[:, :30], torch.zeros(8 * 32 - 2, dtype=torch.int8, device="cuda").as_strided((8, 30), (32, 1)), ws)
     with pytest.raises(P.SparseFFNError):  # scratch too small
-        P.i8_matmul(x, w, ws, work=torch.empty(16, dtype=torch.uint8, device="cuda"))
+        P.i8_matmul(x.repeat(3, 1), w, ws, work=torch.empty(16, dtype=torch.uint8, device="cuda"))
     assert P.i8_matmul(x[:0], w, ws).shape == (0, 8)
 
 
