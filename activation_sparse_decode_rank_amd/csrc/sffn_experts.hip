@@ -13,75 +13,6 @@
 namespace sffn {
 namespace {
 
-constexpr int DTPB = 1024;
-
-// sorted rows: offs[e] = first row of expert e (offs[E] = rows in all), src[row] = slot, and
-// the tile table (expert, first row), n_tiles. One workgroup; a slot's place in its expert is what
-// the count of the expert gave it, kept in a register for the first KEEP slots of a thread.
-__global__ __launch_bounds__(DTPB) void k_sort(const int32_t* __restrict__ idx, int R, int E,
-                                               int tile, int32_t* __restrict__ offs,
-                                               int32_t* __restrict__ src,
-                                               int32_t* __restrict__ tiles,
-                                               int32_t* __restrict__ n_tiles) {
-  constexpr int KEEP = 8;
-  __shared__ int s_cnt[1024], s_at[1024];
-  __shared__ int s_sum[2][DTPB / 64];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  s_cnt[tid] = 0;
-  __syncthreads();
-  int e[KEEP], rank[KEEP];
-#pragma unroll
-  for (int u = 0; u < KEEP; ++u) {
-    const int i = tid + u * DTPB;
-    e[u] = i < R ? idx[i] : -1;
-  }
-#pragma unroll
-  for (int u = 0; u < KEEP; ++u)
-    if ((unsigned)e[u] < (unsigned)E) rank[u] = atomicAdd(&s_cnt[e[u]], 1);
-  __syncthreads();
-  const int kept = s_cnt[tid];  // of the slots whose places are known
-  __syncthreads();
-  for (int i = tid + KEEP * DTPB; i < R; i += DTPB) {
-    const int q = idx[i];
-    if ((unsigned)q < (unsigned)E) atomicAdd(&s_cnt[q], 1);
-  }
-  __syncthreads();
-  // running sums of rows and tiles over the experts
-  const int n = s_cnt[tid], nt = (n + tile - 1) / tile;
-  const int rows = wave_incl_scan(n), tls = wave_incl_scan(nt);
-  if (lane == 63) {
-    s_sum[0][wave] = rows;
-    s_sum[1][wave] = tls;
-  }
-  __syncthreads();
-  int o = rows - n, t = tls - nt;
-  for (int w = 0; w < wave; ++w) {
-    o += s_sum[0][w];
-    t += s_sum[1][w];
-  }
-  if (tid < E) {
-    offs[tid] = o;
-    for (int i = 0; i < nt; ++i) {
-      tiles[2 * (t + i)] = tid;
-      tiles[2 * (t + i) + 1] = o + i * tile;
-    }
-  }
-  if (tid == E - 1) {
-    offs[E] = o + n;
-    *n_tiles = t + nt;
-  }
-  s_at[tid] = o;
-  s_cnt[tid] = o + kept;  // where the slots that are counted again go on
-  __syncthreads();
-#pragma unroll
-  for (int u = 0; u < KEEP; ++u)
-    if ((unsigned)e[u] < (unsigned)E) src[s_at[e[u]] + rank[u]] = tid + u * DTPB;
-  for (int i = tid + KEEP * DTPB; i < R; i += DTPB) {
-    const int q = idx[i];
-    if ((unsigned)q < (unsigned)E) src[atomicAdd(&s_cnt[q], 1)] = i;
-  }
-}
-
 // y_t = sum over slots s in order of weights[t][s] * part[t k + s], slots without an expert
 // left out; a thread takes four channels
 template <typename T>
@@ -186,7 +117,7 @@ hipError_t run_experts(const ExpertsArgs& a, const void* x, int x_type, int64_t 
       if (e != hipSuccess) return e;
       continue;
     }
-    k_sort<<<dim3(1), dim3(DTPB), 0, s>>>(ic, R, a.E, c.tile, offs, src, tiles, count);
+    const SortArgs sort{ic, R, a.E, c.tile, offs, src, tiles, count};
     QuantArgs qx{};
     qx.x = xc;
     qx.ldx = ldx;
@@ -196,7 +127,7 @@ hipError_t run_experts(const ExpertsArgs& a, const void* x, int x_type, int64_t 
     qx.q = reinterpret_cast<int8_t*>(p + c.xq);
     qx.ldq = qx.kpad;
     qx.scale = reinterpret_cast<float*>(p + c.xs);
-    hipError_t e = launch_quantize(qx, x_type, s);
+    hipError_t e = launch_sort_and_quantize(sort, qx, x_type, s);
     if (e != hipSuccess) return e;
 
     ProductArgs up = act_product(a);

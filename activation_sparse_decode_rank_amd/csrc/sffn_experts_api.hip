@@ -22,7 +22,8 @@ bool i8_matrix_ok(const void* w, int64_t ld, int64_t K) {
 int check_experts(const sffn_experts_desc* d) {
   if (!d || d->experts < 1 || d->d < 1 || d->d_ffn < 1) return SFFN_ERR_INVALID;
   if (d->gated != 0 && d->gated != 1) return SFFN_ERR_INVALID;
-  if (d->experts > SFFN_MAX_EXPERTS || d->d > SFFN_I8_MAX_K || d->d_ffn > SFFN_I8_MAX_K)
+  if (d->experts > SFFN_MAX_EXPERTS || d->d > SFFN_I8_MAX_K || d->d_ffn > SFFN_I8_MAX_K ||
+      d->ld_act > sffn::host::kI8MaxLd || d->ld_down > sffn::host::kI8MaxLd)
     return SFFN_ERR_UNSUPPORTED;
   return SFFN_OK;
 }
@@ -100,7 +101,7 @@ int sparse_ffn_i8_matmul(const void* x, int32_t x_dtype, const float* x_scale, i
   const bool i8 = x_dtype == SFFN_I8;
   if ((!float_type(x_dtype) && !i8) || !float_type(y_dtype)) return SFFN_ERR_INVALID;
   if (M < 0 || N < 1 || K < 1 || ldx < K || ldy < N) return SFFN_ERR_INVALID;
-  if (K > SFFN_I8_MAX_K) return SFFN_ERR_UNSUPPORTED;
+  if (K > SFFN_I8_MAX_K || ldw > sffn::host::kI8MaxLd) return SFFN_ERR_UNSUPPORTED;
   if ((((int64_t)M + 63) / 64) * (((int64_t)N + 15) / 16) >= (int64_t)1 << 31)
     return SFFN_ERR_UNSUPPORTED;
   if (M == 0) return SFFN_OK;

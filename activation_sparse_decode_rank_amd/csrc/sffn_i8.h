@@ -26,6 +26,16 @@ struct QuantArgs {
 };
 hipError_t launch_quantize(const QuantArgs& a, int dtype, hipStream_t s);
 
+// The slots [0, R) of a chunk that name an expert (idx in [0, E)), sorted by expert: the tables
+// of ProductArgs. With the tokens' rows into 8 bits in one launch.
+struct SortArgs {
+  const int32_t* idx;
+  int R, E, tile;
+  int32_t *offs, *src, *tiles, *n_tiles;
+};
+hipError_t launch_sort_and_quantize(const SortArgs& sort, const QuantArgs& a, int dtype,
+                                    hipStream_t s);
+
 // What a product does with its sums. LINEAR: y = sum * (sx * sw) + bias in out_type.
 // ACT / ACT_GATED: h = relu(...) of an expert, fp32. DOWN: fp32 part rows of an expert.
 enum ProductMode : int { MODE_LINEAR = 0, MODE_ACT = 1, MODE_ACT_GATED = 2, MODE_DOWN = 3 };

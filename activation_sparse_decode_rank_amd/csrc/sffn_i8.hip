@@ -142,6 +142,125 @@ __global__ __launch_bounds__(W * 64) void k_quantize(QuantArgs a) {
   }
 }
 
+constexpr int DTPB = 1024;
+
+// sorted rows: offs[e] = first row of expert e (offs[E] = rows in all), src[row] = slot, and
+// the tile table (expert, first row), n_tiles. One workgroup of DTPB; a slot's place in its expert is what
+// the count of the expert gave it, kept in a register for the first KEEP slots of a thread.
+__device__ void sort_slots(const SortArgs& a) {
+  const int32_t* __restrict__ idx = a.idx;
+  const int R = a.R, E = a.E, tile = a.tile;
+  int32_t *offs = a.offs, *src = a.src, *tiles = a.tiles, *n_tiles = a.n_tiles;
+  constexpr int KEEP = 8;
+  __shared__ int s_cnt[1024], s_at[1024];
+  __shared__ int s_sum[2][DTPB / 64];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  s_cnt[tid] = 0;
+  __syncthreads();
+  int e[KEEP], rank[KEEP];
+#pragma unroll
+  for (int u = 0; u < KEEP; ++u) {
+    const int i = tid + u * DTPB;
+    e[u] = i < R ? idx[i] : -1;
+  }
+#pragma unroll
+  for (int u = 0; u < KEEP; ++u)
+    if ((unsigned)e[u] < (unsigned)E) rank[u] = atomicAdd(&s_cnt[e[u]], 1);
+  __syncthreads();
+  const int kept = s_cnt[tid];  // of the slots whose places are known
+  __syncthreads();
+  for (int i = tid + KEEP * DTPB; i < R; i += DTPB) {
+    const int q = idx[i];
+    if ((unsigned)q < (unsigned)E) atomicAdd(&s_cnt[q], 1);
+  }
+  __syncthreads();
+  // running sums of rows and tiles over the experts
+  const int n = s_cnt[tid], nt = (n + tile - 1) / tile;
+  const int rows = wave_incl_scan(n), tls = wave_incl_scan(nt);
+  if (lane == 63) {
+    s_sum[0][wave] = rows;
+    s_sum[1][wave] = tls;
+  }
+  __syncthreads();
+  int o = rows - n, t = tls - nt;
+  for (int w = 0; w < wave; ++w) {
+    o += s_sum[0][w];
+    t += s_sum[1][w];
+  }
+  if (tid < E) {
+    offs[tid] = o;
+    for (int i = 0; i < nt; ++i) {
+      tiles[2 * (t + i)] = tid;
+      tiles[2 * (t + i) + 1] = o + i * tile;
+    }
+  }
+  if (tid == E - 1) {
+    offs[E] = o + n;
+    *n_tiles = t + nt;
+  }
+  s_at[tid] = o;
+  s_cnt[tid] = o + kept;  // where the slots that are counted again go on
+  __syncthreads();
+#pragma unroll
+  for (int u = 0; u < KEEP; ++u)
+    if ((unsigned)e[u] < (unsigned)E) src[s_at[e[u]] + rank[u]] = tid + u * DTPB;
+  for (int i = tid + KEEP * DTPB; i < R; i += DTPB) {
+    const int q = idx[i];
+    if ((unsigned)q < (unsigned)E) src[atomicAdd(&s_cnt[q], 1)] = i;
+  }
+}
+
+__global__ __launch_bounds__(DTPB) void k_sort(SortArgs a) { sort_slots(a); }
+
+// The sort (first workgroup) beside the tokens' rows into 8 bits, RW waves a row: neither needs
+// the other, and each alone leaves most of the device idle for a few microseconds.
+template <typename T, int RW>
+__global__ __launch_bounds__(DTPB) void k_prepare(SortArgs sort, QuantArgs a) {
+  constexpr int NV = 4, WAVES = DTPB / 64;
+  __shared__ unsigned s_max[WAVES];
+  if (blockIdx.x == 0) {
+    sort_slots(sort);
+    return;
+  }
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, group = wave / RW;
+  const int64_t at = (int64_t)(blockIdx.x - 1) * (WAVES / RW) + group;
+  const int row = (int)min<int64_t>(at, a.rows - 1);
+  const int i0 = (wave % RW) * 64 + lane, nq = a.kpad / 4;
+  const T* x = static_cast<const T*>(a.x) + (size_t)row * a.ldx;
+  float4_t v[NV];
+  unsigned m = 0;
+#pragma unroll
+  for (int u = 0; u < NV; ++u) v[u] = load4<T>(x, i0 + u * RW * 64, a.cols);
+#pragma unroll
+  for (int u = 0; u < NV; ++u)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) m = max(m, mag(v[u][e]));
+  for (int o = 32; o; o >>= 1) m = max(m, (unsigned)__shfl_xor((int)m, o));
+  if (lane == 0) s_max[wave] = m;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < RW; ++w) m = max(m, s_max[group * RW + w]);
+  if (at >= a.rows) return;
+  float r;
+  const float s = row_scale(m, r);
+  if (wave % RW == 0 && lane == 0) a.scale[row] = s;
+  int* q = reinterpret_cast<int*>(a.q + (size_t)row * a.ldq);
+#pragma unroll
+  for (int u = 0; u < NV; ++u) {
+    const int i = i0 + u * RW * 64;
+    if (i < nq) q[i] = s > 0.f ? quantize4(v[u], s, r) : 0;
+  }
+}
+
+template <typename T>
+void prepare_launch(const SortArgs& sort, const QuantArgs& a, hipStream_t s) {
+  const int nq = a.kpad / 4;
+  auto grid = [&](int rows) { return dim3((unsigned)(1 + ((int64_t)a.rows + rows - 1) / rows)); };
+  if (nq <= 4 * 64) k_prepare<T, 1><<<grid(16), dim3(DTPB), 0, s>>>(sort, a);
+  else if (nq <= 4 * 256) k_prepare<T, 4><<<grid(4), dim3(DTPB), 0, s>>>(sort, a);
+  else k_prepare<T, 16><<<grid(1), dim3(DTPB), 0, s>>>(sort, a);
+}
+
 __global__ __launch_bounds__(TPB) void k_pad_rows(const int8_t* __restrict__ x, int64_t ldx,
                                                   int rows, int cols, int8_t* __restrict__ q,
                                                   int kpad) {
@@ -989,14 +1108,14 @@ void few_launch(const ProductArgs& a, int64_t tiles, size_t lds, hipStream_t s) 
       <<<dim3((unsigned)std::min<int64_t>(groups, at_once)), dim3(W * 64), lds, s>>>(a);
 }
 // Waves of a tile. One where rows are short (up to 32 blocks) and the tiles give every compute
-// unit ten: a wave alone waits for nobody (2 of 8 experts' up products at 16 tokens, d 4096,
-// d_ffn 11008: 135 us; four waves 156, eight 170). Else eight, which read a tile's rows in runs
-// of 2 KB (their down products: 72 us; four 74, one 78), or four where more rows of x take the
-// registers (24 tokens x 11008 x 4096: 15.7 us; eight 17.0).
+// unit ten: a wave alone waits for nobody (16 tokens' up products through 8 experts, d 4096,
+// d_ffn 11008: 125 us; four waves 156, eight 170). Else four (16 tokens through the whole layer
+// 203 us, with eight for the down products 213), or eight where the workgroups hold x in 8 bits
+// themselves and fewer of them do it (1 token x 4096 x 11008: 11.5 us, 12.0 with four).
 template <int MODE, int NR, typename X>
 void few_launch(const ProductArgs& a, int64_t row_tiles, size_t lds, hipStream_t s) {
   constexpr int NT = MODE == MODE_ACT_GATED ? 8 : 16;
-  constexpr int SK = NR == 1 ? 8 : 4;
+  constexpr int SK = std::is_void<X>::value ? 4 : 8;
   const int64_t tiles = row_tiles * ((a.n + NT - 1) / NT);
   if (tiles >= 2560 && a.kch <= 32 * F_BLK) few_launch<MODE, NR, X, 4, 1>(a, tiles, lds, s);
   else few_launch<MODE, NR, X, SK, SK>(a, tiles, lds, s);
@@ -1071,6 +1190,18 @@ hipError_t launch_quantize(const QuantArgs& a, int dtype, hipStream_t s) {
   if (dtype == T_F32) quantize_launch<float>(a, s);
   else if (dtype == T_F16) quantize_launch<_Float16>(a, s);
   else quantize_launch<__bf16>(a, s);
+  return hipGetLastError();
+}
+
+hipError_t launch_sort_and_quantize(const SortArgs& sort, const QuantArgs& a, int dtype,
+                                    hipStream_t s) {
+  if (a.kpad > 4 * 4 * DTPB) {  // longer than a workgroup's registers hold
+    k_sort<<<dim3(1), dim3(DTPB), 0, s>>>(sort);
+    return launch_quantize(a, dtype, s);
+  }
+  if (dtype == T_F32) prepare_launch<float>(sort, a, s);
+  else if (dtype == T_F16) prepare_launch<_Float16>(sort, a, s);
+  else prepare_launch<__bf16>(sort, a, s);
   return hipGetLastError();
 }
 

@@ -102,6 +102,8 @@ inline ExpertsCarve experts_carve(int E, int d, int f, size_t T, size_t k) {
 
 // most rows one chunk may have: 32-bit row numbers, and grids below 2^31 workgroups
 constexpr size_t kExpertsMaxRows = (size_t)1 << 24;
+// The products reach up to 32 rows of w with 32-bit offsets.
+constexpr int64_t kI8MaxLd = (int64_t)1 << 24;
 
 // tokens per chunk that work_bytes holds (0: not even one), at most T
 inline int experts_chunk(int E, int d, int f, int T, int k, size_t work_bytes) {

@@ -23,7 +23,7 @@
  *
  * Layout: int8 matrices are row-major with one row per output channel; a row starts at a
  * multiple of 16 bytes and `ld` bytes after the one before it (ld a multiple of 16, at least
- * the row length rounded up to 16). Bytes between a row's end and the next multiple of 16 are
+ * the row length rounded up to 16; above 2^24 SFFN_ERR_UNSUPPORTED). Bytes between a row's end and the next multiple of 16 are
  * read and have no effect.
  */
 #ifndef SPARSE_FFN_EXPERTS_H

@@ -256,6 +256,24 @@ def test_matmul_large(P, M, K, N, xt, yt):
     check_matmul(P, M, K, N, xt, yt, True)
 
 
+@pytest.mark.parametrize("M,K", [(1, 65536), (1, 65537), (2, 32768), (3, 20000), (4, 16384), (4, 16385), (5, 300)])
+def test_matmul_around_what_lds_holds(P, M, K):
+    """Rows that the product holds in 8 bits itself, up to the most it takes, and just above."""
+    say("matmul lds", M, K)
+    for xt in ("f32", "bf16"):
+        check_matmul(P, M, K, 40, xt, "f32", True)
+
+
+@pytest.mark.parametrize("k,f", [(1, 65536), (2, 32768), (2, 32769), (4, 16384), (16, 4096), (17, 300), (64, 1024)])
+def test_experts_one_token_around_what_lds_holds(P, k, f):
+    say("experts lds", k, f)
+    E = min(k, 5)
+    ffn = make_experts(P, E, 48, f, True, False)
+    idx, w = tables(1, E, k, dropped=0.3)
+    x = dev(rng(37, k, f).standard_normal((1, 48)), torch.float16)
+    check_experts(P, ffn, x, idx, w, torch.float32)
+
+
 def test_matmul_extreme_values(P):
     """Every product at its largest: the sums stay in 32 bits up to the longest row."""
     K = 131071
@@ -479,6 +497,34 @@ def test_experts_refusals(P):
         P.ExpertFFN(w_act=ffn.w_act, act_scale=ffn.act_scale, w_down=ffn.w_down[:, :, :47],
                     down_scale=ffn.down_scale)
     assert ffn(x[:0], idx[:0], w[:0]).shape == (0, 64)
+
+
+def test_matmul_activations_past_32_bits(P):
+    """int8 rows in place, 4.7 GB of them."""
+    M, K, N = 36_000, 131_072 - 128, 8
+    x = torch.zeros((M, K), dtype=torch.int8, device="cuda")
+    g = rng(35)
+    pick = [0, 5000, 32_767, 32_768, 32_769, 35_999]
+    rows = g.integers(-127, 128, (len(pick), K)).astype(np.int8)
+    x[pick] = torch.from_numpy(rows).to("cuda")
+    w = torch.from_numpy(g.integers(-127, 128, (N, K)).astype(np.int8)).to("cuda")
+    ws, xs = torch.rand(N, device="cuda"), torch.rand(M, device="cuda")
+    y = P.i8_matmul(x, w, ws, x_scale=xs)
+    want, mag = ref.matmul(rows, f64(xs[pick]), f64(w), f64(ws))
+    check(y[pick], want, 4 * U * mag, torch.float32)
+    assert int((y != 0).any(1).sum()) == len(pick)
+
+
+def test_experts_many_slots(P):
+    """More slots than the sort keeps in registers, very uneven, several thousand dropped."""
+    T, E, k = 6001, 9, 3
+    ffn = make_experts(P, E, 32, 48, True, False)
+    g = rng(36)
+    idx = np.minimum(g.geometric(0.5, (T, k)) - 1, E).astype(np.int32)  # E: no expert
+    idx[g.random((T, k)) < 0.15] = -1
+    idx, w = dev(idx, torch.int32), dev(g.random((T, k)))
+    x = dev(g.standard_normal((T, 32)))
+    check_experts(P, ffn, x, idx, w, torch.float32)
 
 
 def test_experts_offsets_past_32_bits(P):
