@@ -4,6 +4,7 @@
 // of two such rows is the exact whole-number sum of q_j w_j (at most 131071 products of two
 // 8-bit values fit 32 bits), times the two rows' scales.
 #include <algorithm>
+#include <atomic>
 
 #include "sffn_device.h"
 #include "sffn_i8.h"
@@ -1089,21 +1090,28 @@ void tile_launch(const ProductArgs& a, int64_t row_tiles, hipStream_t s) {
       <<<dim3((unsigned)((tiles + 7) / 8 * 8)), dim3(WC * WT * 64), 0, s>>>(a);
 }
 
-// workgroups of a kernel that the current device holds at once (asked once per kernel)
-template <typename K>
-int resident(K kernel, int threads, size_t lds) {
+// Workgroups of a kernel that the current device holds at once. The last answer is kept: device,
+// dynamic LDS (below 2^24) and number in one word.
+template <auto Kernel>
+int resident(int threads, size_t lds) {
+  static std::atomic<uint64_t> kept{0};
   int dev = 0, cus = 0, per = 0;
-  if (hipGetDevice(&dev) != hipSuccess ||
-      hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess ||
-      hipOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, threads, lds) != hipSuccess)
+  if (hipGetDevice(&dev) != hipSuccess) return 512;
+  const uint64_t key = ((uint64_t)(dev + 1) << 48) | ((uint64_t)lds << 24);
+  const uint64_t last = kept.load(std::memory_order_relaxed);
+  if ((last & ~(uint64_t)0xFFFFFF) == key) return (int)(last & 0xFFFFFF);
+  if (hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess ||
+      hipOccupancyMaxActiveBlocksPerMultiprocessor(&per, Kernel, threads, lds) != hipSuccess)
     return 512;
-  return std::max(1, cus * per);
+  const int n = std::min(std::max(1, cus * per), 0xFFFFFF);
+  kept.store(key | (uint64_t)n, std::memory_order_relaxed);
+  return n;
 }
 
 template <int MODE, int NR, typename X, int W, int SK>
 void few_launch(const ProductArgs& a, int64_t tiles, size_t lds, hipStream_t s) {
   const int64_t groups = SK == 1 ? (tiles + W - 1) / W : tiles;
-  const int at_once = resident(k_product_few<MODE, NR, X, W, SK>, W * 64, lds);
+  const int at_once = resident<k_product_few<MODE, NR, X, W, SK>>(W * 64, lds);
   k_product_few<MODE, NR, X, W, SK>
       <<<dim3((unsigned)std::min<int64_t>(groups, at_once)), dim3(W * 64), lds, s>>>(a);
 }
@@ -1181,7 +1189,7 @@ hipError_t launch_token_down(ProductArgs a, const float* weights, hipStream_t s)
   a.div_nq = inverse(nq);
   a.div_nb = inverse(nb);
   const size_t lds = (size_t)a.k * host::i8_kpad(a.cols);
-  const int at_once = resident(k_token_down, TD_W * 64, lds);
+  const int at_once = resident<k_token_down>(TD_W * 64, lds);
   k_token_down<<<dim3((unsigned)std::min((a.n + 15) / 16, at_once)), dim3(TD_W * 64), lds, s>>>(a, weights);
   return hipGetLastError();
 }
