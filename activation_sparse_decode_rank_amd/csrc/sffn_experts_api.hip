@@ -104,6 +104,7 @@ int sparse_ffn_i8_matmul(const void* x, int32_t x_dtype, const float* x_scale, i
   if (K > SFFN_I8_MAX_K || ldw > sffn::host::kI8MaxLd) return SFFN_ERR_UNSUPPORTED;
   if ((((int64_t)M + 63) / 64) * (((int64_t)N + 15) / 16) >= (int64_t)1 << 31)
     return SFFN_ERR_UNSUPPORTED;
+  if (M > INT32_MAX - 1024) return SFFN_ERR_UNSUPPORTED;  // tiles round rows up in 32 bits
   if (M == 0) return SFFN_OK;
   if (!x || (i8 != (x_scale != nullptr)) || !w_scale || !y || !i8_matrix_ok(w, ldw, K))
     return SFFN_ERR_INVALID;

@@ -224,7 +224,7 @@ template <typename T, int J, bool BIAS>
 __global__ __launch_bounds__(TPB) void k_route(RouteArgs a) {
   __shared__ double s_c[RWAVES][64 * J];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int t = blockIdx.x * RWAVES + wave;
+  const int64_t t = (int64_t)blockIdx.x * RWAVES + wave;
   if (t >= a.T) return;
   const float NINF = -__builtin_inff();
   const T* l = static_cast<const T*>(a.logits) + (size_t)t * a.ld;

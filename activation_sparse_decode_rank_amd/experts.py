@@ -27,8 +27,8 @@ _I32, _F32, _I8, _U8 = torch.int32, torch.float32, torch.int8, torch.uint8
 
 class _on:
     """The device of a tensor made current for a call, and the stream the call goes to: the
-    given one (of that device) or the device's current one. Tensors that the call allocates on
-    another stream's pool are marked as used on this one (`own`). Closed by `done`."""
+    given one (of that device) or the device's current one. What the call allocates comes from
+    that stream's memory (`empty`): another stream's might still be in use there."""
 
     __slots__ = ("device", "handle", "_back", "_other")
 
@@ -50,16 +50,11 @@ class _on:
             if stream != torch.cuda.current_stream(dev):
                 self._other = stream
 
-    def own(self, t: torch.Tensor) -> torch.Tensor:
-        if self._other is not None:
-            t.record_stream(self._other)
-        return t
-
     def empty(self, shape, dtype) -> torch.Tensor:
-        t = torch.empty(shape, dtype=dtype, device=self.device)
-        if self._other is not None:
-            t.record_stream(self._other)
-        return t
+        if self._other is None:
+            return torch.empty(shape, dtype=dtype, device=self.device)
+        with torch.cuda.stream(self._other):
+            return torch.empty(shape, dtype=dtype, device=self.device)
 
     def done(self):
         if self._back is not None:
@@ -138,13 +133,13 @@ def _out(given, on, shape, dtype, name):
         return on.empty(shape, dtype)
     if given.dtype != dtype or given.shape != shape or given.device != on.device:
         raise ValueError(f"{name} must be {dtype} of shape {tuple(shape)} on {on.device}")
-    return on.own(given)
+    return given
 
 
 def _work(given, on):
     if given.dtype != _U8 or given.dim() != 1 or not given.is_contiguous() or given.device != on.device:
         raise ValueError(f"work must be a contiguous uint8 tensor on {on.device}")
-    return on.own(given)
+    return given
 
 
 def _out_dtype(out_dtype, y, default):

@@ -12,7 +12,8 @@
  * Conventions of sparse_ffn.h hold: device pointers owned by the caller, `stream` a
  * hipStream_t of the current device, nothing synchronizes or allocates, every argument is
  * checked on the host before anything is enqueued, and every result is bitwise reproducible.
- * Calls can be captured in a HIP graph. Calls that share a `work` buffer must be ordered, and
+ * Outputs and work must not overlap each other or the inputs (sparse_ffn_experts may write its y
+ * over its x). Calls can be captured in a HIP graph. Calls that share a `work` buffer must be ordered, and
  * so must the replays of graphs that hold such calls.
  *
  * 8-bit rows. A row r of numbers is held as q and s: s is max|r| times the 32-bit float

@@ -121,6 +121,7 @@ def test_matmul_unsupported(N):
     assert experts(N, desc(N, ld_act=(1 << 24) + 16)) == N.SFFN_ERR_UNSUPPORTED
     assert experts(N, desc(N, ld_down=1 << 40)) == N.SFFN_ERR_UNSUPPORTED
     n = (1 << 31) - 1
+    assert matmul(N, M=n) == N.SFFN_ERR_UNSUPPORTED
     assert matmul(N, M=n, N=n, ldy=n) == N.SFFN_ERR_UNSUPPORTED
     wb = N.sparse_ffn_i8_matmul_work_bytes
     none = C.c_size_t(-1).value

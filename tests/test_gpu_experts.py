@@ -632,6 +632,42 @@ def test_another_stream(P):
             assert torch.equal(a, b)
 
 
+def test_another_stream_takes_no_memory_that_this_one_still_uses(P):
+    """A tensor that is freed here while a queued copy still reads it: a call on another stream
+    that does not wait for this one must not get its memory."""
+    ffn = make_experts(P, 2, 1024, 64, True, False)
+    idx, w = tables(512, 2, 1, dropped=0.0)
+    x = dev(rng(38).standard_normal((512, 1024)))
+    l = dev(rng(39).standard_normal((512, 2)))
+    s = torch.cuda.Stream()
+    want = ffn(x, idx, w)
+    torch.cuda.synchronize()
+    for _ in range(3):
+        a = torch.full((512, 1024), 3.0, device="cuda")
+        a2 = torch.full((512, 1), 7, dtype=torch.int32, device="cuda")
+        torch.cuda.synchronize()
+        torch.cuda._sleep(20_000_000)
+        b, b2 = a.clone(), a2.clone()
+        del a, a2
+        y = ffn(x, idx, w, stream=s)
+        P.route(l, 1, stream=s)
+        s.synchronize()
+        torch.cuda.synchronize()
+        assert bool((b == 3.0).all()) and bool((b2 == 7).all())
+        assert torch.equal(y, want)
+
+
+def test_output_over_the_input(P):
+    ffn = make_experts(P, 3, 128, 96, True, False)
+    for T in (1, 5, 100):
+        idx, w = tables(T, 3, 2)
+        x = dev(rng(40, T).standard_normal((T, 128)))
+        want = ffn(x, idx, w)
+        x2 = x.clone()
+        ffn(x2, idx, w, y=x2)
+        assert torch.equal(x2, want)
+
+
 def test_same_values_every_time(P):
     ffn = make_experts(P, 8, 512, 700, True, False)
     for T in (3, 500):
