@@ -289,6 +289,24 @@ __device__ __forceinline__ void store4(void* p, size_t i, const float4_t& v, int
   }
 }
 
+// Eight neighbouring values of a row as T, the first `left` of them
+template <typename T>
+__device__ __forceinline__ void store8(void* p, size_t i, const float4_t& a, const float4_t& b, int left) {
+  typedef T vec __attribute__((ext_vector_type(8), aligned(sizeof(T))));
+  if (left >= 8) {
+    vec t;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      t[j] = (T)a[j];
+      t[4 + j] = (T)b[j];
+    }
+    *reinterpret_cast<vec*>(static_cast<T*>(p) + i) = t;
+  } else {
+    store4<T>(p, i, a, left);
+    store4<T>(p, i + 4, b, left - 4);
+  }
+}
+
 // The scales of channels (neurons) c .. c + 3 of expert e, and their biases; in the gated form of
 // the gate and the up rows. Read before the stores of a tile, which they could not pass.
 template <int MODE>
@@ -364,6 +382,23 @@ __device__ __forceinline__ unsigned emit(const ProductArgs& a, int ro, float xs,
     else store4<__bf16>(a.out, o, y, left);
   }
   return big;
+}
+
+// The same for channels c .. c + 7 of a plain product
+__device__ __forceinline__ void emit8(const ProductArgs& a, int ro, float xs, int c,
+                                      const Scales<MODE_LINEAR>& S0, const Scales<MODE_LINEAR>& S1,
+                                      const int4_t& v0, const int4_t& v1) {
+  if (c >= a.n) return;
+  const size_t o = (size_t)ro * a.ldo + c;
+  float4_t y0, y1;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    y0[j] = (float)v0[j] * (xs * S0.s[j]) + S0.b[j];
+    y1[j] = (float)v1[j] * (xs * S1.s[j]) + S1.b[j];
+  }
+  if (a.out_type == T_F32) store8<float>(a.out, o, y0, y1, a.n - c);
+  else if (a.out_type == T_F16) store8<_Float16>(a.out, o, y0, y1, a.n - c);
+  else store8<__bf16>(a.out, o, y0, y1, a.n - c);
 }
 
 // The rows that tile mt stands for: [r0, r1) of expert e; false: no such tile.
@@ -929,9 +964,8 @@ __global__ __launch_bounds__(TD_W * 64) void k_token_down(ProductArgs a, const f
 // every wave is done with the stage's LDS and the next stage has landed; the second step's
 // products run while the freed stage is refilled and the next stage's first operands are read.
 // Reads and loads are issued between the products, not before them.
-// Bound by the matrix cores and what surrounds a tile's products: 4096 x 4096 x 11008 in 188 us
-// (1.97 POP/s, matrix cores 44% busy); of a 256 x 256 tile's 62 us about 15 are its first loads
-// and its stores. 256 rows of w and of x need 64 KB a stage, a 128 x 64 part for each of 8 waves
+// Bound by the matrix cores and what surrounds a tile's products: 4096 x 4096 x 11008 in 173 us
+// (2.13 POP/s); of a 256 x 256 tile's 57 us about 10 are its first loads and its stores. 256 rows of w and of x need 64 KB a stage, a 128 x 64 part for each of 8 waves
 // 24 KB of LDS reads against 32 products' 1024 cycles; 256 x 128 tiles take 7% longer, 128 x 128
 // 20%, 32 x 32 products 5%, four waves 45%.
 // this lane's 16 bytes at src to place 16 * lane of the 1 KB block at dst (LDS)
@@ -952,6 +986,9 @@ constexpr int SG_MFMA = 0x8, SG_LOAD = 0x20, SG_LDS_READ = 0x100;
 template <int MODE, int CH, int TK, int WC, int WT, int NS>
 __global__ __launch_bounds__(WC * WT * 64) void k_product(ProductArgs a) {
   constexpr bool G = MODE == MODE_ACT_GATED;
+  // rows of w in an order that gives a lane 8 neighbouring channels in two tiles: 16-bit outputs
+  // leave in 64-byte pieces of a row, not 32 (182 -> 173 us at 4096 x 4096 x 11008)
+  constexpr bool PAIRS = MODE == MODE_LINEAR;
   constexpr int W = WC * WT;
   constexpr int NT = G ? CH / 2 : CH;                    // channels (neurons) per tile
   constexpr int NI = CH / 16 / WC, NJ = TK / 16 / WT;    // 16 x 16 tiles of a wave
@@ -963,14 +1000,14 @@ __global__ __launch_bounds__(WC * WT * 64) void k_product(ProductArgs a) {
   __shared__ __attribute__((aligned(16))) int8_t sbuf[NS * STAGE];
   const int nnt = (a.n + NT - 1) / NT;
   const int nmt = MODE == MODE_LINEAR ? (a.rows + TK - 1) / TK : *a.n_tiles;
-  // Tiles in runs of 8 row tiles, channels outer: 32 neighbours share 8 row tiles and 4 channel
-  // tiles. Workgroups 8 apart run on one XCD; each XCD takes a run of neighbours.
+  // Tiles in runs of 4 row tiles, channels outer: 32 neighbours share 4 row tiles and 8 channel
+  // tiles (4096 x 4096 x 11008: 4% less than with 8 and 4, 10% less than 16 and 2). Workgroups 8 apart run on one XCD; each XCD takes a run of neighbours.
   const int total = nmt * nnt, per = (total + 7) / 8;
   const int id = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
   if ((int)(blockIdx.x >> 3) >= per || id >= total) return;
-  const int run = id / (8 * nnt), in = id % (8 * nnt);
-  const int rm = min(8, nmt - run * 8);
-  const int mt = run * 8 + in % rm, nt = in / rm;
+  const int run = id / (4 * nnt), in = id % (4 * nnt);
+  const int rm = min(4, nmt - run * 4);
+  const int mt = run * 4 + in % rm, nt = in / rm;
   int e, r0, r1;
   if (!tile_rows<MODE>(a, mt, e, r0, r1)) return;
   r1 = min(r1, r0 + TK);
@@ -988,7 +1025,8 @@ __global__ __launch_bounds__(WC * WT * 64) void k_product(ProductArgs a) {
     const int u = wave + W * v;  // 8 rows of the stage, wave-uniform
     if (u < UW) {
       const int R = 8 * u + (lane >> 3);
-      const int row = G ? 2 * (n0 + (R >> 5) * 16 + (R & 15)) + ((R >> 4) & 1) : n0 + R;
+      const int row = G ? 2 * (n0 + (R >> 5) * 16 + (R & 15)) + ((R >> 4) & 1)
+                    : PAIRS ? n0 + (R & ~31) + 8 * ((R >> 2) & 3) + 4 * ((R >> 4) & 1) + (R & 3) : n0 + R;
       src[v] = w + (size_t)min(row, nw - 1) * a.ldw;
     } else {
       src[v] = a.x + (size_t)row_of_x<MODE>(a, min(r0 + 8 * (u - UW) + (lane >> 3), r1 - 1)) * a.ldx;
@@ -1068,9 +1106,13 @@ __global__ __launch_bounds__(WC * WT * 64) void k_product(ProductArgs a) {
     buf = next;
   }
   wait_loads<0>();  // no load may land in LDS after the loop
-  // lane holds rows 16 j + r16 and channels 16 i + 4 g .. +3 of the wave's part
+  // lane holds rows 16 j + r16 and channels 16 i + 4 g .. +3 (PAIRS: 16 i + 8 g .. +3 in even
+  // tiles i, the four after them in the next one) of the wave's part
   constexpr int NE = G ? NI / 2 : NI;
-  auto channel = [&](int i) { return n0 + (wc * NE + i) * 16 + 4 * g; };
+  auto channel = [&](int i) {
+    const int t = wc * NE + i;
+    return PAIRS ? n0 + (t & ~1) * 16 + 8 * g + 4 * (t & 1) : n0 + t * 16 + 4 * g;
+  };
   Scales<MODE> sc[NE];
   float xs[NJ];
   int ro[NJ];
@@ -1085,9 +1127,15 @@ __global__ __launch_bounds__(WC * WT * 64) void k_product(ProductArgs a) {
 #pragma unroll
   for (int j = 0; j < NJ; ++j) {
     if (r0 + (wt * NJ + j) * 16 + r16 >= r1) continue;
+    if constexpr (PAIRS) {
 #pragma unroll
-    for (int i = 0; i < NE; ++i)
-      emit<MODE>(a, ro[j], xs[j], channel(i), sc[i], acc[G ? 2 * i : i][j], acc[G ? 2 * i + 1 : i][j]);
+      for (int i = 0; i < NE; i += 2)
+        emit8(a, ro[j], xs[j], channel(i), sc[i], sc[i + 1], acc[i][j], acc[i + 1][j]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < NE; ++i)
+        emit<MODE>(a, ro[j], xs[j], channel(i), sc[i], acc[G ? 2 * i : i][j], acc[G ? 2 * i + 1 : i][j]);
+    }
   }
 }
 
