@@ -287,6 +287,24 @@ def test_matmul_extreme_values(P):
         assert (np.abs(f64(y) - want) <= U * np.abs(want)).all()
 
 
+@pytest.mark.parametrize("M,K,N", [(4100, 48, 7931), (4099, 40, 7934), (1100, 80, 14597), (200, 33, 16389),
+                                   (65, 70, 1013)])
+@pytest.mark.parametrize("yt", ["f32", "f16", "bf16"])
+def test_matmul_tiles_write_only_their_rows(P, M, K, N, yt):
+    """Each of the tiles of many rows, rows and channels that end inside one, a window of a
+    larger output at an odd column."""
+    say("matmul tiles", M, K, N, yt)
+    w, ws = weights_of(P, N, K)
+    x, xs = P.quantize_rows(dev(rng(38, M, K).standard_normal((M, K))))
+    b = dev(rng(39, N).standard_normal(N))
+    out = torch.full((M + 2, N + 9), -7.0, dtype=DT[yt], device="cuda")
+    P.i8_matmul(x, w, ws, x_scale=xs, bias=b, y=out[1:-1, 3:3 + N])
+    want, mag = ref.matmul(f64(x), f64(xs), f64(w), f64(ws), f64(b))
+    check(out[1:-1, 3:3 + N], want, 4 * U * mag, DT[yt])
+    out[1:-1, 3:3 + N] = -7.0
+    assert (out == -7.0).all()
+
+
 def test_matmul_strides_and_untouched_memory(P):
     M, K, N = 37, 200, 77
     g = rng(9)
