@@ -215,9 +215,13 @@ __device__ Chosen route_exact(const RouteArgs& a, const float (&v)[J], float m, 
 // magnitude: 6 2^-24 in all. A softmax: the argument down to -104 (below, it is zero) makes its
 // exponential off by up to 104 2^-24, but only where it is small: x e^-x is at most 0.37, so
 // 2^-24 of the largest score and those above with the longer sum: 16 2^-24; relative to itself,
-// where scores are compared without a bias, 128 2^-24.
+// where scores are compared without a bias, 128 2^-24. That holds for normal numbers only: below
+// 2^-126 a score is off by up to 2^-149, and a sigmoid whose exponential overflows (logits below
+// -88.7) by all of itself, less than 2^-126. Neither counts beside a worth of at least
+// SMALLEST_WORTH, of which the margin is 2^-116; smaller ones are compared in 64 bits.
 constexpr float MARGIN_SIGMOID = 0x1p-20f, MARGIN_SOFTMAX = 0x1p-19f;  // of 1 + the larger magnitude
 constexpr float MARGIN_ITSELF = 0x1p-16f;                              // of the larger one
+constexpr float SMALLEST_WORTH = 0x1p-100f;
 
 // J: experts per lane (E <= 64 J); BIAS: c = s + b
 template <typename T, int J, bool BIAS>
@@ -282,7 +286,7 @@ __global__ __launch_bounds__(TPB) void k_route(RouteArgs a) {
     float least, most;
     const uint64_t kept = groups_kept(a, s_v, pairs, L, least, most);
     if (BIAS) sure = most == NINF || least - most > 2.f * margin * (1.f + fabsf(most));
-    else if (pairs) sure = most == NINF || least - most > MARGIN_ITSELF * least;
+    else if (pairs) sure = most == NINF || (least > SMALLEST_WORTH && least - most > MARGIN_ITSELF * least);
 #pragma unroll
     for (int j = 0; j < J; ++j)
       if (!stays(a, kept, L, lane + 64 * j)) c[j] = NINF;

@@ -1,0 +1,43 @@
+"""GPU tests of the router's choice of groups where 32-bit scores cannot decide it: scores that
+fp32 holds as subnormal numbers or not at all, and groups whose two scores cancel. The choice is
+the 64-bit one (tests/experts_ref.py); weights as in test_gpu_experts.py."""
+import numpy as np
+import pytest
+import torch
+
+from gpu_util import say
+from test_gpu_experts import P, check_route, dev, rng  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+INF = float("inf")
+
+
+@pytest.mark.parametrize("score,logits,top_groups", [
+    # exact worths of the last two groups 7.43e-44 and 7.52e-44; as fp32 scores 7.6e-44, 7.4e-44
+    ("softmax", [[100, 0], [-0.001, -0.001], [0.03, -0.01]], 2),
+    # 3.0e-39 and 5.8e-39; as fp32 scores 3.0e-39 and 0, e^88.73 being past the largest fp32 number
+    ("sigmoid", [[-88.70, -95], [-88.73, -88.73]], 1),
+    ("sigmoid", [[1, 1], [-88.5, -INF], [-88.8, -88.8]], 2),
+    # both scores of both groups are below the smallest fp32 number
+    ("softmax", [[0, -200], [-130, -130], [-129.5, -INF]], 2),
+])
+def test_pairs_of_scores_below_the_normal_numbers(P, score, logits, top_groups):  # noqa: F811
+    say("pairs", score, logits)
+    l = dev(np.array(logits, np.float32).reshape(1, -1))
+    G = len(logits)
+    for renorm in (True, False):
+        check_route(P, l, 2 * G, score=score, groups=G, top_groups=top_groups, group_top=2, renormalize=renorm)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,groups,top_groups", [(16, 8, 3), (64, 8, 2), (256, 32, 5)])
+def test_pairs_of_low_scores(P, score, E, groups, top_groups):  # noqa: F811
+    """Worths a few per cent apart where a last place of an fp32 score is as much (a softmax
+    whose first group alone is not that far down), or where e^-l passes the largest fp32 number."""
+    say("pairs of low scores", score, E, groups)
+    T, per = 400, E // groups
+    l = (-100 if score == "softmax" else -88.72) + 0.05 * rng(50, E, groups).standard_normal((T, E))
+    if score == "softmax":
+        l[:, :per] = rng(51, E).uniform(-1, 0, (T, per))
+        l[:, 0] = 0
+    check_route(P, dev(l), 2 * per, score=score, groups=groups, top_groups=top_groups, group_top=2)
