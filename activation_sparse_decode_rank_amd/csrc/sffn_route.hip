@@ -81,16 +81,19 @@ __device__ __forceinline__ float infinity(float) { return __builtin_inff(); }
 __device__ __forceinline__ double infinity(double) { return __builtin_inf(); }
 __device__ __forceinline__ float larger(float a, float b) { return fmaxf(a, b); }
 __device__ __forceinline__ double larger(double a, double b) { return fmax(a, b); }
+__device__ __forceinline__ float magnitude(float a) { return fabsf(a); }
+__device__ __forceinline__ double magnitude(double a) { return fabs(a); }
 __device__ __forceinline__ float smaller(float a, float b) { return fminf(a, b); }
 __device__ __forceinline__ double smaller(double a, double b) { return fmin(a, b); }
 
 // The groups that stay, from the values x in s_v (minus infinity: none): a group's worth is its
 // best one, or with `pairs` the sum of its two best. L lanes, a power of two of them, look through
 // a group; bit g L of the result is group g. least, most: the least worth that stays, the most
-// that does not (minus infinity: none).
+// that does not (minus infinity: none). addends (if not null): the largest sum of the magnitudes
+// that a group's worth is made of.
 template <typename F>
 __device__ __forceinline__ uint64_t groups_kept(const RouteArgs& a, const F* s_v, bool pairs, int L,
-                                                F& least, F& most) {
+                                                F& least, F& most, F* addends) {
   const int lane = threadIdx.x & 63;
   const F NINF = -infinity(F());
   const int per = a.E / a.groups, g = lane / L;
@@ -106,7 +109,9 @@ __device__ __forceinline__ uint64_t groups_kept(const RouteArgs& a, const F* s_v
     b2 = larger(larger(b2, o2), smaller(b1, o1));
     b1 = larger(b1, o1);
   }
-  const F worth = b1 + (pairs && b2 > NINF ? b2 : F(0));
+  const F more = pairs && b2 > NINF ? b2 : F(0);
+  const F worth = b1 + more;
+  if (addends) *addends = wave_max(worth > NINF ? magnitude(b1) + magnitude(more) : F(0));
   int rank = 0;
   for (int q = 0; q < a.groups; ++q) {
     const F o = from_lane(worth, q * L);
@@ -181,7 +186,7 @@ __device__ Chosen route_exact(const RouteArgs& a, const float (&v)[J], float m, 
       s_c[lane + 64 * j] = !pairs || a.bias ? c[j] : (c[j] > NINF ? sc[j] : NINF);
     wave_lds_sync();
     double least, most;
-    const uint64_t kept = groups_kept(a, s_c, pairs, L, least, most);
+    const uint64_t kept = groups_kept(a, s_c, pairs, L, least, most, static_cast<double*>(nullptr));
 #pragma unroll
     for (int j = 0; j < J; ++j)
       if (!stays(a, kept, L, lane + 64 * j)) c[j] = NINF;
@@ -212,13 +217,14 @@ __device__ Chosen route_exact(const RouteArgs& a, const float (&v)[J], float m, 
 
 // Margins of 32-bit scores, twice what one is off. A sigmoid: its exponential, the sum and the
 // quotient lose 2^-24 of it each, at most two for the exponential; a bias' sum 2^-24 of 1 + its
-// magnitude: 6 2^-24 in all. A softmax: the argument down to -104 (below, it is zero) makes its
-// exponential off by up to 104 2^-24, but only where it is small: x e^-x is at most 0.37, so
-// 2^-24 of the largest score and those above with the longer sum: 16 2^-24; relative to itself,
-// where scores are compared without a bias, 128 2^-24. That holds for normal numbers only: below
-// 2^-126 a score is off by up to 2^-149, and a sigmoid whose exponential overflows (logits below
-// -88.7) by all of itself, less than 2^-126. Neither counts beside a worth of at least
-// SMALLEST_WORTH, of which the margin is 2^-116; smaller ones are compared in 64 bits.
+// magnitude: 6 2^-24 in all (a worth of two: twice that, and 2^-24 of what is added). A softmax:
+// the argument down to -104 (below, it is zero) makes its exponential off by up to 104 2^-24, but
+// only where it is small: x e^-x is at most 0.37, so 2^-24 of the largest score and those above
+// with the longer sum: 16 2^-24; relative to itself, where scores are compared without a bias,
+// 128 2^-24. That holds for normal numbers only: below 2^-126 a score is off by up to 2^-149, and
+// a sigmoid whose exponential overflows (logits below -88.7) by all of itself, less than 2^-126.
+// Neither counts beside a worth of at least SMALLEST_WORTH, of which the margin is 2^-116; smaller
+// ones are compared in 64 bits.
 constexpr float MARGIN_SIGMOID = 0x1p-20f, MARGIN_SOFTMAX = 0x1p-19f;  // of 1 + the larger magnitude
 constexpr float MARGIN_ITSELF = 0x1p-16f;                              // of the larger one
 constexpr float SMALLEST_WORTH = 0x1p-100f;
@@ -283,9 +289,10 @@ __global__ __launch_bounds__(TPB) void k_route(RouteArgs a) {
     for (int j = 0; j < J; ++j)
       s_v[lane + 64 * j] = BIAS || !pairs ? c[j] : (v[j] > NINF ? sc[j] : NINF);
     wave_lds_sync();
-    float least, most;
-    const uint64_t kept = groups_kept(a, s_v, pairs, L, least, most);
-    if (BIAS) sure = most == NINF || least - most > 2.f * margin * (1.f + fabsf(most));
+    float least, most, addends;
+    const uint64_t kept = groups_kept(a, s_v, pairs, L, least, most, BIAS ? &addends : nullptr);
+    // two scores a side, which may cancel: the margin goes by what was added, not by the sums
+    if (BIAS) sure = most == NINF || least - most > 2.f * margin * (1.f + addends);
     else if (pairs) sure = most == NINF || (least > SMALLEST_WORTH && least - most > MARGIN_ITSELF * least);
 #pragma unroll
     for (int j = 0; j < J; ++j)

@@ -41,3 +41,16 @@ def test_pairs_of_low_scores(P, score, E, groups, top_groups):  # noqa: F811
         l[:, :per] = rng(51, E).uniform(-1, 0, (T, per))
         l[:, 0] = 0
     check_route(P, dev(l), 2 * per, score=score, groups=groups, top_groups=top_groups, group_top=2)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("big", [1.0, 100.0, 1000.0, 3e4])
+def test_pairs_whose_biases_cancel(P, score, big):  # noqa: F811
+    """A group's two scores carry biases of opposite sign: what fp32 loses in each is many times
+    what the groups' worths lie apart."""
+    say("cancelling biases", score, big)
+    T, E, G = 500, 16, 8
+    l = 1e-3 * rng(52, int(big)).standard_normal((T, E))
+    bias = dev(np.tile(np.array([big, -big], np.float32), G))
+    check_route(P, dev(l), 6, score=score, bias=bias, groups=G, top_groups=3, group_top=2)
+    check_route(P, dev(l), 6, score=score, bias=bias, groups=G, top_groups=3, group_top=1)
