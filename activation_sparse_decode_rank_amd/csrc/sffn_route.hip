@@ -111,7 +111,7 @@ __device__ __forceinline__ uint64_t groups_kept(const RouteArgs& a, const F* s_v
   }
   const F more = pairs && b2 > NINF ? b2 : F(0);
   const F worth = b1 + more;
-  if (addends) *addends = wave_max(worth > NINF ? magnitude(b1) + magnitude(more) : F(0));
+  if (addends) *addends = wave_max(b1 > NINF ? magnitude(b1) + magnitude(more) : F(0));
   int rank = 0;
   for (int q = 0; q < a.groups; ++q) {
     const F o = from_lane(worth, q * L);
@@ -292,7 +292,9 @@ __global__ __launch_bounds__(TPB) void k_route(RouteArgs a) {
     float least, most, addends;
     const uint64_t kept = groups_kept(a, s_v, pairs, L, least, most, BIAS ? &addends : nullptr);
     // two scores a side, which may cancel: the margin goes by what was added, not by the sums
-    if (BIAS) sure = most == NINF || least - most > 2.f * margin * (1.f + addends);
+    // (an infinity there: a bias, or a sum that 32 bits cannot hold)
+    if (BIAS)
+      sure = addends < __builtin_inff() && (most == NINF || least - most > 2.f * margin * (1.f + addends));
     else if (pairs) sure = most == NINF || (least > SMALLEST_WORTH && least - most > MARGIN_ITSELF * least);
 #pragma unroll
     for (int j = 0; j < J; ++j)

@@ -54,3 +54,16 @@ def test_pairs_whose_biases_cancel(P, score, big):  # noqa: F811
     bias = dev(np.tile(np.array([big, -big], np.float32), G))
     check_route(P, dev(l), 6, score=score, bias=bias, groups=G, top_groups=3, group_top=2)
     check_route(P, dev(l), 6, score=score, bias=bias, groups=G, top_groups=3, group_top=1)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_pairs_at_the_lowest_value(P, score):  # noqa: F811
+    """Biases of the type's lowest value (experts switched off so): a group of two of them is worth
+    -6.8e38, which fp32 cannot hold, and still more than a group without any expert."""
+    say("lowest biases", score)
+    low = float(torch.finfo(torch.float32).min)
+    l = dev(np.array([[1, 2, -INF, -INF, 0.5, 1, 1, 2]] * 3, np.float32))
+    bias = dev(np.array([0, 0, 0, 0, low, low, low, low], np.float32))
+    for group_top in (1, 2):
+        for top_groups in (1, 2, 3):
+            check_route(P, l, 6, score=score, bias=bias, groups=4, top_groups=top_groups, group_top=group_top)
