@@ -313,6 +313,7 @@ template <int MODE>
 struct Scales {
   static constexpr bool G = MODE == MODE_ACT_GATED;
   float4_t s, u, b;
+  bool together;  // gated: relu of a sum times its scale is relu of the sum, times its scale
   __device__ __forceinline__ void load(const ProductArgs& a, int e, int c) {
     typedef float vec __attribute__((ext_vector_type(4), aligned(4)));
     const size_t at = (size_t)e * a.n + c;
@@ -336,6 +337,11 @@ struct Scales {
         if (MODE != MODE_DOWN && a.bias) b[j] = a.bias[at + j];
       }
     }
+    if (G) {
+      together = !a.bias;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) together = together && s[j] >= 0.f && s[j] < __builtin_inff();
+    }
   }
 };
 
@@ -352,8 +358,9 @@ __device__ __forceinline__ unsigned emit(const ProductArgs& a, int ro, float xs,
   float4_t y;
   if constexpr (MODE == MODE_ACT || MODE == MODE_ACT_GATED) {
     // h in 64 bits up to its one rounding: it decides between whole numbers afterwards
-    if (MODE == MODE_ACT_GATED && !a.bias) {
-      // the scales together: two products of 64 bits less for each value
+    if (MODE == MODE_ACT_GATED && S.together) {
+      // the scales together: two products of 64 bits less for each value (not where a gate's
+      // scale is negative, an infinity or NaN)
       const double x2 = (double)xs * (double)xs;
 #pragma unroll
       for (int j = 0; j < 4; ++j)
