@@ -70,6 +70,7 @@ int sparse_ffn_quantize_rows(const void* x, int32_t dtype, int64_t ldx, int32_t 
   if (!float_type(dtype) || rows < 0 || cols < 1 || ldx < cols || ldq % 16 != 0 ||
       ldq < row16(cols))
     return SFFN_ERR_INVALID;
+  if (cols > sffn::host::kI8MaxCount) return SFFN_ERR_UNSUPPORTED;  // rounded up in 32 bits
   if (rows == 0) return SFFN_OK;
   if (!x || !q || !scale || !aligned(x, type_size(dtype)) || !aligned(q, 16) || !aligned(scale, 4))
     return SFFN_ERR_INVALID;
@@ -104,7 +105,10 @@ int sparse_ffn_i8_matmul(const void* x, int32_t x_dtype, const float* x_scale, i
   if (K > SFFN_I8_MAX_K || ldw > sffn::host::kI8MaxLd) return SFFN_ERR_UNSUPPORTED;
   if ((((int64_t)M + 63) / 64) * (((int64_t)N + 15) / 16) >= (int64_t)1 << 31)
     return SFFN_ERR_UNSUPPORTED;
-  if (M > INT32_MAX - 1024) return SFFN_ERR_UNSUPPORTED;  // tiles round rows up in 32 bits
+  // tiles round rows and channels up in 32 bits; a launch holds less than 2^32 threads
+  if (M > sffn::host::kI8MaxCount || N > sffn::host::kI8MaxCount ||
+      !sffn::host::i8_launches((size_t)M, (size_t)N))
+    return SFFN_ERR_UNSUPPORTED;
   if (M == 0) return SFFN_OK;
   if (!x || (i8 != (x_scale != nullptr)) || !w_scale || !y || !i8_matrix_ok(w, ldw, K))
     return SFFN_ERR_INVALID;

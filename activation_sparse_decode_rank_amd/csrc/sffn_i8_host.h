@@ -31,6 +31,18 @@ inline int i8_tile(size_t rows, size_t groups, size_t rows_w) {
   return 64;
 }
 
+// most rows, channels or columns of one call: they are rounded up to tiles in 32 bits
+constexpr int kI8MaxCount = INT32_MAX - 1023;  // 2^31 - 1024
+
+// Whether the tiles of M rows and N channels fit one launch, of less than 2^32 threads. Up to 32
+// rows the grid goes by the device instead.
+inline bool i8_launches(size_t M, size_t N) {
+  const size_t t = (size_t)i8_tile(M, 1, N);
+  if (t <= 32) return true;
+  const size_t ch = t == 64 ? 128 : 256, threads = t == 64 ? 256 : 512;  // 64 channels: few tiles only
+  return (((M + t - 1) / t) * ((N + ch - 1) / ch) + 8) * threads < (size_t)1 << 32;
+}
+
 // Whether M rows of K values are held in 8 bits by the product itself: every workgroup does it
 // for all rows, so few of them, and within the LDS that leaves two workgroups a compute unit.
 constexpr int kFusedRows = 4;

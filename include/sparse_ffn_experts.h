@@ -72,7 +72,7 @@ int sparse_ffn_route(const void* logits, int32_t dtype, int64_t ld, int32_t T, i
  * per token). x: device, `rows` rows of `cols` values (SFFN_F32, SFFN_F16 or SFFN_BF16), ldx
  * elements apart; q: device, 16-byte aligned, ldq a multiple of 16 and at least cols rounded
  * up to 16 (the bytes from cols to that multiple are written as zeros); scale: device fp32
- * [rows]. rows >= 0. */
+ * [rows]. rows >= 0; cols above 2^31 - 1024: SFFN_ERR_UNSUPPORTED. */
 int sparse_ffn_quantize_rows(const void* x, int32_t dtype, int64_t ldx, int32_t rows,
                              int32_t cols, int8_t* q, int64_t ldq, float* scale, void* stream);
 
@@ -86,8 +86,9 @@ int sparse_ffn_quantize_rows(const void* x, int32_t dtype, int64_t ldx, int32_t 
  * values of y_dtype (SFFN_F32, SFFN_F16, SFFN_BF16), ldy elements apart; what lies between
  * the rows is left as it was. work: device scratch, 256-byte aligned, of at least
  * sparse_ffn_i8_matmul_work_bytes() (0 bytes: may be NULL). M >= 0, 1 <= K <= SFFN_I8_MAX_K.
- * SFFN_ERR_UNSUPPORTED: K above that, or more than 2^31 tiles of output. The size query
- * returns (size_t)-1 for an argument it cannot size. */
+ * SFFN_ERR_UNSUPPORTED: K above that, M or N above 2^31 - 1024, or more tiles of output than one
+ * launch holds (possible from 2^36 outputs on). The size query returns (size_t)-1 for an argument
+ * it cannot size. */
 size_t sparse_ffn_i8_matmul_work_bytes(int32_t x_dtype, int32_t M, int32_t N, int32_t K);
 int sparse_ffn_i8_matmul(const void* x, int32_t x_dtype, const float* x_scale, int64_t ldx,
                          int32_t M, int32_t K, const int8_t* w, int64_t ldw,
