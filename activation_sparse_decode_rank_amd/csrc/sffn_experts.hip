@@ -98,8 +98,10 @@ hipError_t run_token(const ExpertsArgs& a, const void* x, int x_type, const int3
 hipError_t run_experts(const ExpertsArgs& a, const void* x, int x_type, int64_t ldx, int T,
                        const int32_t* idx, const float* weights, int k, void* y, int y_type,
                        int64_t ldy, void* work, int chunk, hipStream_t s) {
-  for (int t0 = 0; t0 < T; t0 += chunk) {
-    const int Tc = std::min(chunk, T - t0);
+  const host::Chunks chunks(T, chunk);
+  for (int64_t i = 0; i < chunks.count; ++i) {
+    const int64_t t0 = chunks.first(i);
+    const int Tc = chunks.tokens(i);
     const int R = Tc * k;
     const host::ExpertsCarve c = host::experts_carve(a.E, a.d, a.f, (size_t)Tc, (size_t)k);
     char* p = static_cast<char*>(work);

@@ -130,5 +130,14 @@ inline int experts_chunk(int E, int d, int f, int T, int k, size_t work_bytes) {
   return (int)lo;
 }
 
+// The chunks of a call of T tokens, `size` tokens each but the last. 64 bits: the last one's end
+// may pass 32.
+struct Chunks {
+  int64_t T, size, count;
+  Chunks(int T_, int size_) : T(T_), size(size_), count((T + size - 1) / size) {}
+  int64_t first(int64_t i) const { return i * size; }
+  int tokens(int64_t i) const { return (int)std::min(size, T - first(i)); }
+};
+
 }  // namespace host
 }  // namespace sffn

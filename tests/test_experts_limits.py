@@ -26,3 +26,46 @@ def test_products_past_one_launch_are_refused(N):  # noqa: F811
     for M in (65, 96):
         assert matmul(N, M=M, N=1 << 30, ldy=1 << 30) == N.SFFN_ERR_UNSUPPORTED
     assert matmul(N, M=1 << 20, N=1 << 20, ldy=1 << 20) == N.SFFN_ERR_UNSUPPORTED
+
+
+def build_and_run(tmp_path, body):
+    """A C++ program over the host plan (csrc/sffn_i8_host.h), with its arithmetic checked."""
+    src = r'''
+#include <climits>
+#include <cstdio>
+#include <cstdlib>
+#include <random>
+#include <vector>
+#include "sffn_i8_host.h"
+using namespace sffn::host;
+#define CHECK(c) do { if (!(c)) { std::printf("failed: %s line %d\n", #c, __LINE__); std::exit(1); } } while (0)
+int main() {
+''' + body + r'''
+  std::puts("ok");
+  return 0;
+}
+'''
+    (tmp_path / "limits.cpp").write_text(src)
+    exe = str(tmp_path / "limits")
+    subprocess.run(["g++", "-std=c++17", "-O1", "-Wall", "-fsanitize=undefined", "-fno-sanitize-recover=all",
+                    "-I", os.path.join(ROOT, "activation_sparse_decode_rank_amd", "csrc"),
+                    str(tmp_path / "limits.cpp"), "-o", exe], check=True)
+    r = subprocess.run([exe], capture_output=True, text=True, timeout=120)
+    assert r.returncode == 0 and "ok" in r.stdout, r.stdout + r.stderr
+
+
+def test_chunks_of_the_most_tokens(tmp_path):
+    """The chunks of a call follow each other, without a gap, up to 2^31 - 1 tokens."""
+    build_and_run(tmp_path, r'''
+  for (int T : {1, 2, 1000, INT_MAX - 1, INT_MAX})
+    for (int size : {1 << 24, (1 << 21) - 1, 12345678, 32768 / 3}) {
+      if (T / size > 3000000) continue;
+      const Chunks c(T, size);
+      int64_t at = 0;
+      for (int64_t i = 0; i < c.count; ++i) {
+        CHECK(c.first(i) == at && c.tokens(i) >= 1 && c.tokens(i) <= size);
+        at += c.tokens(i);
+      }
+      CHECK(at == T);
+    }
+''')
