@@ -490,11 +490,22 @@ void route_launch(const RouteArgs& a, hipStream_t s) {
 
 }  // namespace
 
+// In pieces: a launch holds less than 2^32 threads, and a token takes up to 64.
 hipError_t launch_route(const RouteArgs& a, int dtype, hipStream_t s) {
-  if (dtype == T_F32) route_launch<float>(a, s);
-  else if (dtype == T_F16) route_launch<_Float16>(a, s);
-  else route_launch<__bf16>(a, s);
-  return hipGetLastError();
+  constexpr int PIECE = 1 << 25;
+  for (int64_t t0 = 0; t0 < a.T; t0 += PIECE) {
+    RouteArgs p = a;
+    p.T = (int)std::min<int64_t>(PIECE, a.T - t0);
+    p.logits = static_cast<const char*>(a.logits) + (size_t)t0 * a.ld * (dtype == T_F32 ? 4 : 2);
+    p.idx = a.idx + (size_t)t0 * a.k;
+    p.weights = a.weights + (size_t)t0 * a.k;
+    if (dtype == T_F32) route_launch<float>(p, s);
+    else if (dtype == T_F16) route_launch<_Float16>(p, s);
+    else route_launch<__bf16>(p, s);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 }  // namespace sffn

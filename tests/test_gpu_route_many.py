@@ -1,0 +1,31 @@
+"""GPU tests of the router at more tokens than one launch holds: every token is written, and the
+choice is the one that 64-bit scores give."""
+import pytest
+import torch
+
+from gpu_util import say
+from test_gpu_experts import P  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("T,biased", [((1 << 26) + 7, True), ((1 << 27) + 7, False)])
+def test_more_tokens_than_one_launch_holds(P, T, biased):  # noqa: F811
+    say("route", T, biased)
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(T)
+    l = torch.empty((T, 2), device="cuda", dtype=torch.float16).normal_(generator=gen)
+    bias = torch.tensor([0.25, 0.0], device="cuda") if biased else None
+    idx = torch.full((T, 1), -9, dtype=torch.int32, device="cuda")
+    w = torch.full((T, 1), -9.0, device="cuda")
+    P.route(l, 1, score="sigmoid", bias=bias, renormalize=False, idx=idx, weights=w)
+    for part in range(0, T, 1 << 24):
+        s = l[part:part + (1 << 24)].double()
+        s = 1 / (1 + torch.exp(-s))
+        c = s if bias is None else s + bias.double()
+        want = (c[:, 1] > c[:, 0]).to(torch.int32)
+        got = idx[part:part + (1 << 24), 0]
+        assert bool((got == want).all()), part
+        # |l| is below 8: the exponent's argument and the exponential 10 u, the sum and quotient 2 u
+        d = (w[part:part + (1 << 24), 0].double() / s.gather(1, want.long().unsqueeze(1))[:, 0] - 1).abs()
+        assert float(d.max()) <= 12 * 2.0 ** -24
