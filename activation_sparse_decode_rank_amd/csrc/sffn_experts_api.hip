@@ -173,8 +173,8 @@ int sparse_ffn_i8_matmul(const void* x, int32_t x_dtype, const float* x_scale, i
 
 size_t sparse_ffn_experts_work_bytes(const sffn_experts_desc* desc, int32_t tokens, int32_t k) {
   if (check_experts(desc) != SFFN_OK || tokens < 1 || k < 1 || k > SFFN_MAX_TOPK) return 0;
-  // a chunk never holds more rows than this
-  const size_t most = sffn::host::kExpertsMaxRows / (size_t)k;
+  // a chunk never holds more tokens than this
+  const size_t most = sffn::host::experts_max_tokens(desc->d, k);
   const size_t T = (size_t)tokens < most ? (size_t)tokens : most;
   return sffn::host::experts_carve(desc->experts, desc->d, desc->d_ffn, T, (size_t)k).bytes;
 }

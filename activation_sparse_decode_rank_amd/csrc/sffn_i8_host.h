@@ -112,14 +112,19 @@ inline ExpertsCarve experts_carve(int E, int d, int f, size_t T, size_t k) {
   return c;
 }
 
-// most rows one chunk may have: 32-bit row numbers, and grids below 2^31 workgroups
-constexpr size_t kExpertsMaxRows = (size_t)1 << 24;
+// Most rows one chunk may have, and most tokens: the rows' and the sums' launches stay below 2^32
+// threads (1024 a token at most where it is held in 8 bits, 256 for each 1024 channels of its sum).
+constexpr size_t kExpertsMaxRows = (size_t)1 << 21;
+inline size_t experts_max_tokens(int d, int k) {
+  const size_t blocks = ((size_t)d + 1023) / 1024;
+  return std::max<size_t>(1, std::min(kExpertsMaxRows / (size_t)k, ((size_t)1 << 23) / blocks));
+}
 // The products reach up to 32 rows of w with 32-bit offsets.
 constexpr int64_t kI8MaxLd = (int64_t)1 << 24;
 
 // tokens per chunk that work_bytes holds (0: not even one), at most T
 inline int experts_chunk(int E, int d, int f, int T, int k, size_t work_bytes) {
-  size_t lo = 0, hi = std::min((size_t)T, std::max<size_t>(1, kExpertsMaxRows / (size_t)k));
+  size_t lo = 0, hi = std::min((size_t)T, experts_max_tokens(d, k));
   while (lo < hi) {
     const size_t mid = (lo + hi + 1) / 2;
     if (experts_carve(E, d, f, mid, (size_t)k).bytes <= work_bytes)

@@ -69,3 +69,19 @@ def test_chunks_of_the_most_tokens(tmp_path):
       CHECK(at == T);
     }
 ''')
+
+
+def test_launches_of_a_chunk_stay_below_32_bits_of_threads(tmp_path):
+    """The rows into 8 bits (a workgroup of 1024 threads holds 16, 4 or 1 of them) and the sums
+    over the slots (256 threads, four channels each), whatever scratch there is."""
+    build_and_run(tmp_path, r'''
+  for (int d : {1, 64, 1024, 1025, 4096, 4097, 16384, 70000, 131071})
+    for (int k : {1, 2, 8, 64})
+      for (int T : {1, 5000000, INT_MAX}) {
+        const size_t c = experts_chunk(8, d, 64, T, k, (size_t)-1);
+        CHECK(c >= 1 && c * k <= kExpertsMaxRows);
+        const size_t rows = i8_kpad(d) <= 1024 ? 16 : i8_kpad(d) <= 4096 ? 4 : 1;
+        CHECK((1 + (c + rows - 1) / rows) * 1024 < (size_t)1 << 32);
+        CHECK(c * ((d + 1023) / 1024) * 256 < (size_t)1 << 32);
+      }
+''')
