@@ -97,9 +97,10 @@ hipError_t run_token(const ExpertsArgs& a, const void* x, int x_type, const int3
 
 hipError_t run_experts(const ExpertsArgs& a, const void* x, int x_type, int64_t ldx, int T,
                        const int32_t* idx, const float* weights, int k, void* y, int y_type,
-                       int64_t ldy, void* work, int chunk, hipStream_t s) {
+                       int64_t ldy, void* work, int chunk, bool backward, hipStream_t s) {
   const host::Chunks chunks(T, chunk);
-  for (int64_t i = 0; i < chunks.count; ++i) {
+  for (int64_t n = 0; n < chunks.count; ++n) {
+    const int64_t i = backward ? chunks.count - 1 - n : n;
     const int64_t t0 = chunks.first(i);
     const int Tc = chunks.tokens(i);
     const int R = Tc * k;

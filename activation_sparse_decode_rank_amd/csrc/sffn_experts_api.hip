@@ -201,6 +201,11 @@ int sparse_ffn_experts(const sffn_experts_desc* desc, const void* x, int32_t x_d
   const int chunk =
       sffn::host::experts_chunk(desc->experts, desc->d, desc->d_ffn, T, k, work_bytes);
   if (chunk < 1) return SFFN_ERR_INVALID;
+  const int64_t xe = (int64_t)type_size(x_dtype), ye = (int64_t)type_size(y_dtype);
+  const sffn::host::ChunkOrder order = sffn::host::chunk_order(
+      sffn::host::Chunks(T, chunk), reinterpret_cast<uintptr_t>(x), ldx * xe, desc->d * xe,
+      reinterpret_cast<uintptr_t>(y), ldy * ye, desc->d * ye);
+  if (order == sffn::host::ChunkOrder::None) return SFFN_ERR_INVALID;
   sffn::ExpertsArgs a{};
   a.E = desc->experts;
   a.d = desc->d;
@@ -214,7 +219,8 @@ int sparse_ffn_experts(const sffn_experts_desc* desc, const void* x, int32_t x_d
   a.ld_down = desc->ld_down;
   a.down_scale = desc->down_scale;
   return status(sffn::run_experts(a, x, x_dtype, ldx, T, idx, weights, k, y, y_dtype, ldy, work,
-                                  chunk, static_cast<hipStream_t>(stream)));
+                                  chunk, order == sffn::host::ChunkOrder::Backward,
+                                  static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -106,8 +106,9 @@ struct ExpertsArgs {
   int64_t ld_down;
   const float* down_scale;
 };
+// backward: the last chunk first (host::chunk_order)
 hipError_t run_experts(const ExpertsArgs& a, const void* x, int x_type, int64_t ldx, int T,
                        const int32_t* idx, const float* weights, int k, void* y, int y_type,
-                       int64_t ldy, void* work, int chunk, hipStream_t s);
+                       int64_t ldy, void* work, int chunk, bool backward, hipStream_t s);
 
 }  // namespace sffn

@@ -144,5 +144,32 @@ struct Chunks {
   int tokens(int64_t i) const { return (int)std::min(size, T - first(i)); }
 };
 
+// The order in which chunks can go whose outputs may lie over inputs: a chunk reads its rows of x
+// before it writes its rows of y, so no y row may meet an x row of a chunk that comes after its
+// own. Rows of x: xb bytes, xp apart from x on; rows of y likewise.
+enum class ChunkOrder { Forward, Backward, None };
+inline ChunkOrder chunk_order(const Chunks& c, uintptr_t x, int64_t xp, int64_t xb, uintptr_t y,
+                              int64_t yp, int64_t yb) {
+  typedef __int128 I;
+  const I T = c.T, at = (I)x - (I)y;  // bytes from y on: x's row t at at + t xp, y's at t yp
+  if (c.count == 1 || at >= (T - 1) * yp + yb || at + (T - 1) * xp + xb <= 0) return ChunkOrder::Forward;
+  auto floor_div = [](I a, I b) { return a >= 0 ? a / b : -((-a + b - 1) / b); };
+  bool later = false, earlier = false;  // a y row meets an x row of a later (an earlier) chunk
+  if (xp == yp) {  // the y rows that meet x's row t are t + lo .. t + hi, for every t
+    const I lo = floor_div(at - yb, yp) + 1, hi = floor_div(at + xb - 1, yp);
+    later = lo <= -1 && std::min<I>(hi, -1) > -T && lo <= hi;
+    earlier = hi >= 1 && std::max<I>(lo, 1) < T && lo <= hi;
+  } else {
+    for (int64_t t = 0; t < c.T && !(later && earlier); ++t) {
+      const I lo = std::max<I>(floor_div(at + t * (I)xp - yb, yp) + 1, 0);
+      const I hi = std::min<I>(floor_div(at + t * (I)xp + xb - 1, yp), T - 1);
+      if (lo > hi) continue;
+      later |= lo / c.size < t / c.size;
+      earlier |= hi / c.size > t / c.size;
+    }
+  }
+  return !later ? ChunkOrder::Forward : !earlier ? ChunkOrder::Backward : ChunkOrder::None;
+}
+
 }  // namespace host
 }  // namespace sffn

@@ -124,7 +124,9 @@ typedef struct {
  * ldy elements apart, fully overwritten (what lies between the rows is left as it was). work:
  * device scratch, 256-byte aligned, of work_bytes >= sparse_ffn_experts_work_bytes(desc, 1,
  * k): the tokens go through in chunks of the most that fit, so pass the size for T tokens
- * where memory allows. T >= 0, 1 <= k <= SFFN_MAX_TOPK, d and d_ffn at most SFFN_I8_MAX_K.
+ * where memory allows. y may lie over x, in rows of any distance; where the tokens go through in
+ * chunks and no order of them would keep the inputs of later ones, SFFN_ERR_INVALID (an order is
+ * found whenever y begins where x does). T >= 0, 1 <= k <= SFFN_MAX_TOPK, d and d_ffn at most SFFN_I8_MAX_K.
  * The size query returns 0 for an argument it cannot size. */
 size_t sparse_ffn_experts_work_bytes(const sffn_experts_desc* desc, int32_t tokens, int32_t k);
 int sparse_ffn_experts(const sffn_experts_desc* desc, const void* x, int32_t x_dtype,

@@ -85,3 +85,36 @@ def test_launches_of_a_chunk_stay_below_32_bits_of_threads(tmp_path):
         CHECK(c * ((d + 1023) / 1024) * 256 < (size_t)1 << 32);
       }
 ''')
+
+
+def test_order_of_chunks_by_trying_every_row(tmp_path):
+    """Outputs over inputs: the order found is one that keeps the inputs, and one is found
+    whenever there is one (forward first)."""
+    build_and_run(tmp_path, r'''
+  std::mt19937 g(11);
+  auto pick = [&](int lo, int hi) { return lo + (int)(g() % (unsigned)(hi - lo + 1)); };
+  int found[3] = {0, 0, 0};
+  for (int it = 0; it < 200000; ++it) {
+    const int T = pick(1, 40), size = pick(1, 12);
+    const int xb = pick(1, 9), yb = pick(1, 9);
+    const int xp = xb + pick(0, 9), yp = it % 3 ? yb + pick(0, 9) : std::max(xp, yb);
+    const int64_t x = 1000 + pick(-200, 200), y = it % 5 ? 1000 + pick(-200, 200) : x;
+    const Chunks c(T, size);
+    bool later = false, earlier = false;
+    for (int t = 0; t < T; ++t)
+      for (int u = 0; u < T; ++u) {  // y's row t, x's row u
+        const int64_t ya = y + (int64_t)t * yp, xa = x + (int64_t)u * xp;
+        if (ya < xa + xb && xa < ya + yb) {
+          later |= u / size > t / size;
+          earlier |= u / size < t / size;
+        }
+      }
+    const ChunkOrder want = !later ? ChunkOrder::Forward : !earlier ? ChunkOrder::Backward : ChunkOrder::None;
+    CHECK(chunk_order(c, x, xp, xb, y, yp, yb) == want);
+    if (x == y) CHECK(want != ChunkOrder::None);
+    found[(int)want]++;
+  }
+  CHECK(found[0] > 1000 && found[1] > 1000 && found[2] > 1000);
+  const Chunks most(INT_MAX, 7);  // rows as far apart as 64 bits hold
+  CHECK(chunk_order(most, 4096, LLONG_MAX, 64, 4096, LLONG_MAX, 64) == ChunkOrder::Forward);
+''')
