@@ -227,32 +227,47 @@ def sparse_ffn_up_probe(w_up, layout, d, d_ffn, x, idx, count, words, u, work, w
                                  work_bytes, stream), "sparse_ffn_up_probe")
 
 
+def _fits(bits: int, what: str) -> None:
+    """bits: the whole numbers of a call, or-ed together. Those that are not in [0, 2^31) are
+    refused here: ctypes would cut them to 32 bits."""
+    if bits >> 31:
+        raise SparseFFNError(SFFN_ERR_INVALID if bits < 0 else SFFN_ERR_UNSUPPORTED, what)
+
+
 def sparse_ffn_route(logits, dtype, ld, T, E, k, score, bias, groups, top_groups, group_top,
                      renormalize, scale, idx, weights, stream) -> None:
+    _fits(T | E | k | score | groups | top_groups | group_top | renormalize, "sparse_ffn_route")
     _ck(_lib.sparse_ffn_route(logits, dtype, ld, T, E, k, score, bias, groups, top_groups, group_top,
                               renormalize, scale, idx, weights, stream), "sparse_ffn_route")
 
 
 def sparse_ffn_quantize_rows(x, dtype, ldx, rows, cols, q, ldq, scale, stream) -> None:
+    _fits(rows | cols, "sparse_ffn_quantize_rows")
     _ck(_lib.sparse_ffn_quantize_rows(x, dtype, ldx, rows, cols, q, ldq, scale, stream),
         "sparse_ffn_quantize_rows")
 
 
 def sparse_ffn_i8_matmul_work_bytes(x_dtype, M, N, K) -> int:
+    if (M | N | K) >> 31:
+        return C.c_size_t(-1).value
     return int(_lib.sparse_ffn_i8_matmul_work_bytes(x_dtype, M, N, K))
 
 
 def sparse_ffn_i8_matmul(x, x_dtype, x_scale, ldx, M, K, w, ldw, w_scale, bias, N, y, y_dtype, ldy,
                          work, work_bytes, stream) -> None:
+    _fits(M | N | K, "sparse_ffn_i8_matmul")
     _ck(_lib.sparse_ffn_i8_matmul(x, x_dtype, x_scale, ldx, M, K, w, ldw, w_scale, bias, N, y,
                                   y_dtype, ldy, work, work_bytes, stream), "sparse_ffn_i8_matmul")
 
 
 def sparse_ffn_experts_work_bytes(desc: SffnExpertsDesc, tokens, k) -> int:
+    if (tokens | k) >> 31:
+        return 0
     return int(_lib.sparse_ffn_experts_work_bytes(C.byref(desc), tokens, k))
 
 
 def sparse_ffn_experts(desc: SffnExpertsDesc, x, x_dtype, ldx, T, idx, weights, k, y, y_dtype, ldy,
                        work, work_bytes, stream) -> None:
+    _fits(T | k, "sparse_ffn_experts")
     _ck(_lib.sparse_ffn_experts(C.byref(desc), x, x_dtype, ldx, T, idx, weights, k, y, y_dtype, ldy,
                                 work, work_bytes, stream), "sparse_ffn_experts")

@@ -255,6 +255,8 @@ def _experts_desc(w_act, act_scale, w_down, down_scale, b_act) -> N.SffnExpertsD
     if len(shape) not in (3, 4) or (gated and shape[2] != 2):
         raise ValueError("w_act must be [E, d_ffn, d], or [E, d_ffn, 2, d] for the gated form")
     E, f, d = shape[0], shape[1], shape[-1]
+    if (E | f | d) >> 31:  # the descriptor's fields would cut them
+        raise ValueError(f"w_act's sizes {tuple(shape)} do not fit 32 bits")
     if w_down.shape != (E, d, f):
         raise ValueError(f"w_down must be {(E, d, f)}")
     dev = w_act.device
@@ -319,6 +321,8 @@ def experts(x: torch.Tensor, idx: torch.Tensor, weights: torch.Tensor, w_act: to
 def experts_work(w_act: torch.Tensor, w_down: torch.Tensor, tokens: int, k: int) -> torch.Tensor:
     """Scratch for `experts` in chunks of `tokens` tokens of k slots (a uint8 device tensor)."""
     D = N.SffnExpertsDesc()
+    if (w_act.shape[0] | w_act.shape[1] | w_act.shape[-1]) >> 31:
+        raise ValueError(f"w_act's sizes {tuple(w_act.shape)} do not fit 32 bits")
     D.experts, D.d, D.d_ffn = w_act.shape[0], w_act.shape[-1], w_act.shape[1]
     D.gated = int(w_act.dim() == 4)
     nb = N.sparse_ffn_experts_work_bytes(D, int(tokens), int(k))

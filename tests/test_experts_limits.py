@@ -118,3 +118,43 @@ def test_order_of_chunks_by_trying_every_row(tmp_path):
   const Chunks most(INT_MAX, 7);  // rows as far apart as 64 bits hold
   CHECK(chunk_order(most, 4096, LLONG_MAX, 64, 4096, LLONG_MAX, 64) == ChunkOrder::Forward);
 ''')
+
+
+BIG = 1 << 32
+
+
+@pytest.mark.parametrize("name,args,at", [
+    ("route", [A, 1, 64, 4, 64, 8, 0, None, 1, 1, 1, 1, 1.0, A, A, None], (3, 4, 5, 6, 8, 9, 10)),
+    ("quantize_rows", [A, 1, 32, 4, 32, A, 32, A, None], (3, 4)),
+    ("i8_matmul", [A, 1, None, 64, 3, 64, A, 64, A, None, 16, A, 0, 16, None, 0, None], (4, 5, 10)),
+    ("experts", [None, A, 1, 64, 3, A, A, 2, A, 1, 64, A, 1 << 24, None], (4, 7)),
+])
+def test_python_does_not_cut_integers_to_32_bits(N, name, args, at):  # noqa: F811
+    """Numbers that fit the call's 32 bits only when cut to them are refused, not cut."""
+    call = getattr(N, "sparse_ffn_" + name)
+    if name == "experts":
+        args[0] = desc(N)
+    for i in at:
+        for v, status in ((args[i] + BIG, N.SFFN_ERR_UNSUPPORTED), (args[i] - BIG, N.SFFN_ERR_INVALID)):
+            wrong = list(args)
+            wrong[i] = v
+            with pytest.raises(N.SparseFFNError) as e:
+                call(*wrong)
+            assert e.value.status == status, (i, v)
+
+
+def test_size_queries_do_not_cut_integers_to_32_bits(N):  # noqa: F811
+    none = C.c_size_t(-1).value
+    for sizes in ((4 + BIG, 16, 64), (4, 16 + BIG, 64), (4, 16, 64 + BIG), (4 - BIG, 16, 64)):
+        assert N.sparse_ffn_i8_matmul_work_bytes(3, *sizes) == none
+    wb = N.sparse_ffn_experts_work_bytes
+    assert wb(desc(N), 4 + BIG, 2) == wb(desc(N), 4, 2 + BIG) == wb(desc(N), 4 - BIG, 2) == 0
+
+
+def test_shapes_past_32_bits_are_refused():
+    import torch
+    import activation_sparse_decode_rank_amd as P
+    many = torch.empty((5, 1), dtype=torch.int8).as_strided((1, BIG + 2, 1), (0, 0, 1))
+    one = torch.ones((1, 1))
+    with pytest.raises(ValueError, match="32 bits"):
+        P.experts(one, one.int(), one, many, one, many, one)
