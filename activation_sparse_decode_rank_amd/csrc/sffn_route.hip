@@ -228,6 +228,8 @@ __device__ Chosen route_exact(const RouteArgs& a, const float (&v)[J], float m, 
 constexpr float MARGIN_SIGMOID = 0x1p-20f, MARGIN_SOFTMAX = 0x1p-19f;  // of 1 + the larger magnitude
 constexpr float MARGIN_ITSELF = 0x1p-16f;                              // of the larger one
 constexpr float SMALLEST_WORTH = 0x1p-100f;
+// From here down e^-l passes the largest 64-bit number, and the score is zero in 64 bits.
+constexpr float ZERO_SIGMOID = -709.7827f;
 
 // J: experts per lane (E <= 64 J); BIAS: c = s + b
 template <typename T, int J, bool BIAS>
@@ -446,6 +448,7 @@ __global__ __launch_bounds__(TPB) void k_route_pair(RouteArgs a) {
     // them in range
     const float low = a.renorm && m < 0.f ? m : 0.f;
     w = won < 0.f ? expf(won - low) / (1.f + expf(won)) : expf(-low) / (1.f + expf(-won));
+    if (won <= ZERO_SIGMOID) w = 0.f;
   }
   if (mine < 0) w = 0.f;
   if (a.renorm) {

@@ -53,8 +53,8 @@ enum { SFFN_SCORE_SOFTMAX = 0, SFFN_SCORE_SIGMOID = 1 };
  *     best c_e (group_top 1) or the sum of its two best scores c_e (group_top 2; without a
  *     bias the two best s_e); only the top_groups most valuable groups stay
  *   idx: the k largest c_e of what stays, in descending order; weights: their s_e (without
- *     the bias), divided by their sum when renormalize is 1 (all 0 where that sum is 0),
- *     times scale.
+ *     the bias), divided by their sum when renormalize is 1 (all 0 where that sum is 0, as it
+ *     is for sigmoids of logits below -709.78, which are 0 in 64 bits), times scale.
  * Scores are compared in 64 bits; ties go to the lower index. An expert whose logit is minus
  * infinity or NaN, or whose c_e is, is never chosen, takes no part in the softmax or in its
  * group's worth; slots for which no expert is left hold idx -1 and weight 0.

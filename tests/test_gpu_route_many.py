@@ -4,7 +4,7 @@ import pytest
 import torch
 
 from gpu_util import say
-from test_gpu_experts import P  # noqa: F401
+from test_gpu_experts import P, check_route  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -29,3 +29,12 @@ def test_more_tokens_than_one_launch_holds(P, T, biased):  # noqa: F811
         # |l| is below 8: the exponent's argument and the exponential 10 u, the sum and quotient 2 u
         d = (w[part:part + (1 << 24), 0].double() / s.gather(1, want.long().unsqueeze(1))[:, 0] - 1).abs()
         assert float(d.max()) <= 12 * 2.0 ** -24
+
+
+@pytest.mark.parametrize("T", [9, 2051])
+def test_sigmoids_that_are_zero(P, T):  # noqa: F811
+    """Renormalised weights of scores that are zero in 64 bits are zero, however many tokens."""
+    say("route zero sigmoids", T)
+    rows = torch.tensor([[-800.0, -900.0, -1e30], [-700.0, -709.0, -750.0], [-709.78, -709.783, -710.0],
+                         [-100.0, -101.0, -800.0], [0.0, -90.0, -800.0]], device="cuda")
+    check_route(P, rows.repeat((T + 4) // 5, 1)[:T].contiguous(), 3, score="sigmoid")
