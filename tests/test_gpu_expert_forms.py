@@ -53,7 +53,8 @@ def experts_of(ffn, x, idx, weights):
 
 
 def experts_in_a_window(P, ffn, T, E, k, d, xt, yt, dropped, seed):  # noqa: F811
-    """The call on random tables, its output a window of a larger tensor at an odd column."""
+    """The call on random tables, in one chunk, its output a window of a larger tensor at an odd
+    column."""
     gen = torch.Generator(device="cuda")
     gen.manual_seed(seed)
     idx = torch.randint(0, E, (T, k), generator=gen, device="cuda", dtype=torch.int32)
@@ -61,7 +62,7 @@ def experts_in_a_window(P, ffn, T, E, k, d, xt, yt, dropped, seed):  # noqa: F81
     w = torch.rand((T, k), generator=gen, device="cuda")
     x = torch.randn((T, d), generator=gen, device="cuda").to(DT[xt])
     out = torch.full((T + 2, d + 9), -7.0, dtype=DT[yt], device="cuda")
-    ffn(x, idx, w, y=out[1:-1, 3:3 + d])
+    ffn(x, idx, w, y=out[1:-1, 3:3 + d], work=ffn.work(T, k))
     want, mag = experts_of(ffn, x, idx, w)
     check(out[1:-1, 3:3 + d], want, (k + 4) * U * mag, DT[yt])
     out[1:-1, 3:3 + d] = -7.0
