@@ -359,7 +359,7 @@ __global__ __launch_bounds__(TPB) void k_route(RouteArgs a) {
   }
   if (lane < a.k) {
     a.idx[(size_t)t * a.k + lane] = mine;
-    a.weights[(size_t)t * a.k + lane] = w;
+    a.weights[(size_t)t * a.k + lane] = mine < 0 ? 0.f : w;  // also where scale is not finite
   }
 }
 
@@ -457,7 +457,7 @@ __global__ __launch_bounds__(TPB) void k_route_pair(RouteArgs a) {
   }
   if (l32 < a.k && t < a.T) {
     a.idx[(size_t)t * a.k + l32] = mine;
-    a.weights[(size_t)t * a.k + l32] = w * a.scale;
+    a.weights[(size_t)t * a.k + l32] = mine < 0 ? 0.f : w * a.scale;
   }
 }
 

@@ -38,3 +38,17 @@ def test_sigmoids_that_are_zero(P, T):  # noqa: F811
     rows = torch.tensor([[-800.0, -900.0, -1e30], [-700.0, -709.0, -750.0], [-709.78, -709.783, -710.0],
                          [-100.0, -101.0, -800.0], [0.0, -90.0, -800.0]], device="cuda")
     check_route(P, rows.repeat((T + 4) // 5, 1)[:T].contiguous(), 3, score="sigmoid")
+
+
+@pytest.mark.parametrize("T", [3, 2049])
+@pytest.mark.parametrize("scale", [float("inf"), float("-inf"), float("nan"), 0.0])
+@pytest.mark.parametrize("biased", [False, True])
+def test_slots_without_an_expert_have_weight_zero(P, T, scale, biased):  # noqa: F811
+    """Whatever the weights are multiplied by."""
+    say("route empty slots", T, scale, biased)
+    l = torch.full((T, 5), -float("inf"), device="cuda")
+    l[1:, 2] = 1.0
+    for renorm in (True, False):
+        idx, w = P.route(l, 3, bias=torch.zeros(5, device="cuda") if biased else None, scale=scale, renormalize=renorm)
+        assert bool((idx[0] == -1).all()) and bool((idx[1:] == torch.tensor([2, -1, -1], device="cuda")).all())
+        assert bool((w[idx < 0] == 0).all())
