@@ -342,7 +342,7 @@ __global__ __launch_bounds__(TPB) void k_route(RouteArgs a) {
   if (a.renorm) {
     sum = wave_total(w);
     // scores that 32 bits do not hold beside each other: their quotients may still count
-    if (sum < 0x1p-20f && -wave_max(mine >= 0 ? -w : NINF) < 0x1p-100f) sure = false;
+    if (sum < 1.f && -wave_max(mine >= 0 ? -w : NINF) < 0x1p-100f) sure = false;
   }
   if (sure) {
     if (a.renorm) w = sum > 0.f ? w / sum : 0.f;

@@ -52,3 +52,14 @@ def test_slots_without_an_expert_have_weight_zero(P, T, scale, biased):  # noqa:
         idx, w = P.route(l, 3, bias=torch.zeros(5, device="cuda") if biased else None, scale=scale, renormalize=renorm)
         assert bool((idx[0] == -1).all()) and bool((idx[1:] == torch.tensor([2, -1, -1], device="cuda")).all())
         assert bool((w[idx < 0] == 0).all())
+
+
+@pytest.mark.parametrize("T", [5, 2050])
+def test_small_weights_beside_a_small_sum(P, T):  # noqa: F811
+    """A score below the normal numbers is a normal one once it is divided by the sum."""
+    say("route small weights", T)
+    rows = torch.tensor([[-11.5, -89.0, -95.0], [-3.0, -88.9, -89.5], [-13.0, -100.0, -102.0], [-0.5, -89.5, -90.0],
+                         [-30.0, -95.0, -110.0]], device="cuda")
+    l = rows.repeat(T // 5, 1)
+    check_route(P, l, 3, score="sigmoid")
+    check_route(P, l, 3, score="sigmoid", bias=torch.tensor([0.5, 0.25, 0.0], device="cuda"))
