@@ -40,3 +40,21 @@ def test_gate_scales_that_are_not_finite(P, T):  # noqa: F811
     y = check_experts(P, ffn, x, idx, w, torch.float32)
     one = (idx[:, 0] == 1)
     assert bool(torch.isfinite(y[one]).all())
+
+
+def test_scale_of_a_row_is_a_product(P):  # noqa: F811
+    """The scale is the largest magnitude times the 32-bit float nearest to 1 / 127, as the header
+    says: not their quotient, which is one last place off for some rows. Largest magnitudes all
+    over the range, in the row and by itself."""
+    g = rng(62)
+    a = (2.0 ** g.uniform(-99, 127, 4000)).astype(np.float32)
+    want = (a.astype(np.float64) * float(np.float32(1 / 127))).astype(np.float32)  # 48 bits, rounded once
+    quotient = (a.astype(np.float64) / 127).astype(np.float32)
+    differ = want != quotient
+    assert 40 < int(differ.sum()) < 1000  # about one in twenty
+    rows = np.stack([a, -0.75 * a, 0.3 * a], 1)
+    for x in (rows, rows[:, ::-1], -rows, a[:, None]):
+        q, s = P.quantize_rows(dev(np.ascontiguousarray(x)))
+        assert np.array_equal(s.cpu().numpy(), want)
+        near = np.rint(x.astype(np.float64) / want[:, None].astype(np.float64))
+        assert np.array_equal(q.cpu().numpy(), near)
