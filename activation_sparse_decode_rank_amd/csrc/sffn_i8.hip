@@ -101,7 +101,7 @@ __device__ __forceinline__ int quantize4(const float4_t& v, float s, float r) {
 
 // A workgroup of W waves takes a row. NV groups of four values per thread stay in registers
 // between the maximum and the rounding, so the row is read once (NV = 0: longer rows, twice).
-// Bound by that read: 8192 rows of 11008 fp32 in 100 us, 4.5 TB/s with the bytes written; a few
+// Bound by that read: 8192 rows of 11008 fp32 in 104 us, 4.3 TB/s with the bytes written; a few
 // rows take the 4 us of a launch, two round trips and the barrier.
 template <typename T, int W, int NV>
 __global__ __launch_bounds__(W * 64) void k_quantize(QuantArgs a) {
@@ -971,10 +971,12 @@ __global__ __launch_bounds__(TD_W * 64) void k_token_down(ProductArgs a, const f
 // every wave is done with the stage's LDS and the next stage has landed; the second step's
 // products run while the freed stage is refilled and the next stage's first operands are read.
 // Reads and loads are issued between the products, not before them.
-// Bound by the matrix cores and what surrounds a tile's products: 4096 x 4096 x 11008 in 173 us
-// (2.13 POP/s); of a 256 x 256 tile's 57 us about 10 are its first loads and its stores. 256 rows of w and of x need 64 KB a stage, a 128 x 64 part for each of 8 waves
-// 24 KB of LDS reads against 32 products' 1024 cycles; 256 x 128 tiles take 7% longer, 128 x 128
-// 20%, 32 x 32 products 5%, four waves 45%.
+// Bound by the loop, in which the matrix cores are busy 47% of the time, and by what surrounds a
+// tile's products: 4096 x 4096 x 11008 in 177 us (2.09 POP/s; under the profiler 182 at least, 194
+// in the mean); of a 256 x 256 tile's 57 us about 10 are its first loads and its stores. 256 rows
+// of w and of x need 64 KB a stage, a 128 x 64 part for each of 8 waves 24 KB of LDS reads against
+// 32 products' 1024 cycles; 256 x 128 tiles take 7% longer, 128 x 128 20%, 32 x 32 products 5%,
+// four waves 45%.
 // this lane's 16 bytes at src to place 16 * lane of the 1 KB block at dst (LDS)
 __device__ __forceinline__ void load_block(const int8_t* src, int8_t* dst) {
   __builtin_amdgcn_global_load_lds(reinterpret_cast<const u32x4*>(src),
@@ -994,7 +996,7 @@ template <int MODE, int CH, int TK, int WC, int WT, int NS>
 __global__ __launch_bounds__(WC * WT * 64) void k_product(ProductArgs a) {
   constexpr bool G = MODE == MODE_ACT_GATED;
   // rows of w in an order that gives a lane 8 neighbouring channels in two tiles: 16-bit outputs
-  // leave in 64-byte pieces of a row, not 32 (182 -> 173 us at 4096 x 4096 x 11008)
+  // leave in 64-byte pieces of a row, not 32 (5% less time at 4096 x 4096 x 11008)
   constexpr bool PAIRS = MODE == MODE_LINEAR;
   constexpr int W = WC * WT;
   constexpr int NT = G ? CH / 2 : CH;                    // channels (neurons) per tile
@@ -1179,11 +1181,11 @@ void few_launch(const ProductArgs& a, int64_t tiles, size_t lds, hipStream_t s) 
   k_product_few<MODE, NR, X, W, SK>
       <<<dim3((unsigned)std::min<int64_t>(groups, at_once)), dim3(W * 64), lds, s>>>(a);
 }
-// Waves of a tile. One where rows are short (up to 32 blocks) and the tiles give every compute
-// unit ten: a wave alone waits for nobody (16 tokens' up products through 8 experts, d 4096,
-// d_ffn 11008: 125 us; four waves 156, eight 170). Else four (16 tokens through the whole layer
-// 203 us, with eight for the down products 213), or eight where the workgroups hold x in 8 bits
-// themselves and fewer of them do it (1 token x 4096 x 11008: 11.5 us, 12.0 with four).
+// Waves of a tile. One where rows are short (up to 32 blocks) and the tiles give every compute unit
+// ten: a wave alone waits for nobody (16 tokens' up products through 8 experts, d 4096, d_ffn
+// 11008: 131 us; four waves take 25% more, eight 36%). Else four (16 tokens through the whole layer
+// 195 to 205 us, 5% more with eight for the down products), or eight where the workgroups hold x in
+// 8 bits themselves and fewer of them do it (1 token x 4096 x 11008: 11.5 us, 12.0 with four).
 template <int MODE, int NR, typename X>
 void few_launch(const ProductArgs& a, int64_t row_tiles, size_t lds, hipStream_t s) {
   constexpr int NT = MODE == MODE_ACT_GATED ? 8 : 16;

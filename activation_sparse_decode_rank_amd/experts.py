@@ -7,6 +7,11 @@ supplies device memory and streams; every step runs in the library.
     ffn = ExpertFFN.from_float(w_act=gate, w_up=up, w_down=down)
     idx, weights = route(logits, k=2)              # logits [T, E] of the model's own router
     y = ffn(x, idx, weights)
+
+The experts are ReLU FFNs, plain or gated; there are no gradients. Tensors given for outputs must
+not overlap the inputs (the experts' y may lie over x). A call with `stream` goes to that stream
+and takes its outputs from that stream's memory: use them elsewhere only in order after it, and
+keep the inputs until it is done, or record_stream them.
 """
 from __future__ import annotations
 
@@ -313,7 +318,8 @@ def experts(x: torch.Tensor, idx: torch.Tensor, weights: torch.Tensor, w_act: to
     w_act int8 [E, d_ffn, d], or [E, d_ffn, 2, d] (gate row, up row) for the gated form, with
     act_scale fp32 [E, d_ffn(, 2)]; w_down int8 [E, d, d_ffn] with down_scale fp32 [E, d];
     b_act fp32 [E, d_ffn]: bias inside the ReLU. out_dtype: default x's type. work: scratch
-    from experts_work (allocated here when None); calls that share one must be ordered."""
+    from experts_work (allocated here when None, for chunks of up to 32768 slots: 2.4 GB at d 4096,
+    d_ffn 11008); calls that share one must be ordered."""
     D = _experts_desc(w_act, act_scale, w_down, down_scale, b_act)
     return _experts_call(D, w_act.device, x, idx, weights, out_dtype, y, work, stream)
 

@@ -55,9 +55,12 @@ enum { SFFN_SCORE_SOFTMAX = 0, SFFN_SCORE_SIGMOID = 1 };
  *   idx: the k largest c_e of what stays, in descending order; weights: their s_e (without
  *     the bias), divided by their sum when renormalize is 1 (all 0 where that sum is 0, as it
  *     is for sigmoids of logits below -709.78, which are 0 in 64 bits), times scale.
- * Scores are compared in 64 bits; ties go to the lower index. An expert whose logit is minus
- * infinity or NaN, or whose c_e is, is never chosen, takes no part in the softmax or in its
- * group's worth; slots for which no expert is left hold idx -1 and weight 0.
+ * Scores are compared in 64 bits; ties go to the lower index. Weights are computed in 32 bits
+ * (in 64 where the choice needed them): off by a few 2^-24 of their value where the logits lie
+ * close together, and by less than 2^-15 of it, or 2^-126 scale, wherever they lie. An expert
+ * whose logit is minus infinity or NaN takes no part in the softmax. Neither it nor one whose
+ * c_e is minus infinity or NaN (by its bias) is ever chosen or counts in its group's worth;
+ * slots for which no expert is left hold idx -1 and weight 0.
  * logits: device [T] rows of E values (dtype SFFN_F32, SFFN_F16 or SFFN_BF16), ld elements
  * apart (ld >= E); bias: device [E] fp32 or NULL; idx: device int32 [T][k]; weights: device
  * fp32 [T][k]. T >= 0 (0: nothing happens), 1 <= k <= min(E, SFFN_MAX_TOPK), E <=

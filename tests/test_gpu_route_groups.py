@@ -67,3 +67,12 @@ def test_pairs_at_the_lowest_value(P, score):  # noqa: F811
     for group_top in (1, 2):
         for top_groups in (1, 2, 3):
             check_route(P, l, 6, score=score, bias=bias, groups=4, top_groups=top_groups, group_top=group_top)
+
+
+def test_an_expert_switched_off_by_its_bias_stays_in_the_softmax(P):  # noqa: F811
+    """Its score counts in the sum of the others' scores; a logit of minus infinity does not."""
+    l = dev(np.array([[1.0, 2.0, 3.0, 0.5], [1.0, 2.0, -INF, 0.5]], np.float32))
+    bias = dev(np.array([0, 0, -INF, np.nan], np.float32))
+    idx, w = check_route(P, l, 4, bias=bias, renormalize=False)
+    assert idx.tolist() == [[1, 0, -1, -1], [1, 0, -1, -1]]
+    assert float(w[0].sum()) < 0.4 < 0.8 < float(w[1].sum())

@@ -63,3 +63,13 @@ def test_small_weights_beside_a_small_sum(P, T):  # noqa: F811
     l = rows.repeat(T // 5, 1)
     check_route(P, l, 3, score="sigmoid")
     check_route(P, l, 3, score="sigmoid", bias=torch.tensor([0.5, 0.25, 0.0], device="cuda"))
+
+
+@pytest.mark.parametrize("T", [4, 2052])
+def test_subnormal_logits_are_told_apart(P, T):  # noqa: F811
+    """Logits below the normal numbers, and zeros of either sign, which are equal."""
+    say("route subnormal", T)
+    rows = torch.tensor([[0.0, 1e-40, -1e-40, 3e-45], [-0.0, 0.0, -1e-45, 1e-45], [-1e-42, -2e-42, 0.0, -0.0],
+                         [1e-38, 1.1e-38, 1.2e-38, 0.0]], device="cuda")
+    check_route(P, rows.repeat(T // 4, 1), 4)
+    check_route(P, rows.repeat(T // 4, 1), 3, score="sigmoid", groups=2, top_groups=1)
