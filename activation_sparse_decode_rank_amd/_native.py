@@ -1,5 +1,5 @@
-"""ctypes binding of libsparse_ffn.so: the C-ABI entry points of include/sparse_ffn.h
-and include/sparse_ffn_experts.h under the same names. Arguments are plain integers (device addresses, sizes, a stream handle);
+"""ctypes binding of libsparse_ffn.so: the C-ABI entry points of include/sparse_ffn.h,
+include/sparse_ffn_experts.h and include/sparse_ffn_mx4.h under the same names. Arguments are plain integers (device addresses, sizes, a stream handle);
 this module only marshals them and turns a non-zero status into SparseFFNError. There is no
 fallback: if the HIP library is not built, importing this module raises."""
 from __future__ import annotations
@@ -18,7 +18,8 @@ LIB_PATH = os.path.join(_HERE, "libsparse_ffn.so")
 
 SFFN_OK, SFFN_ERR_INVALID, SFFN_ERR_UNSUPPORTED, SFFN_ERR_HIP, SFFN_ERR_TOO_LARGE = 0, -1, -2, -3, -4
 SFFN_STATIC_SCRATCH_BYTES = 16 << 20
-SFFN_F32, SFFN_F16, SFFN_BF16, SFFN_I8 = 0, 1, 2, 3
+SFFN_F32, SFFN_F16, SFFN_BF16, SFFN_I8, SFFN_MX4 = 0, 1, 2, 3, 4
+SFFN_MX4_MAX_K = 1 << 20
 SFFN_SCORE_SOFTMAX, SFFN_SCORE_SIGMOID = 0, 1
 SFFN_MAX_EXPERTS, SFFN_MAX_TOPK, SFFN_I8_MAX_K = 1024, 64, 131071
 SFFN_LAYOUT_SPLIT, SFFN_LAYOUT_BUNDLE = 0, 1
@@ -63,6 +64,7 @@ def _load():
             "`python -m activation_sparse_decode_rank_amd.build`); there is no fallback path")
     lib = C.CDLL(LIB_PATH)
     P, I32, I64, SZ, F32 = C.c_void_p, C.c_int32, C.c_int64, C.c_size_t, C.c_float
+    F64 = C.c_double
     sig = {
         "sparse_ffn_workspace_bytes": (SZ, [C.POINTER(SffnDesc)]),
         "sparse_ffn_create": (C.c_int, [C.POINTER(SffnDesc), C.POINTER(P)]),
@@ -96,6 +98,14 @@ def _load():
         "sparse_ffn_experts_work_bytes": (SZ, [C.POINTER(SffnExpertsDesc), I32, I32]),
         "sparse_ffn_experts": (C.c_int, [C.POINTER(SffnExpertsDesc), P, I32, I64, I32, P, P, I32, P,
                                          I32, I64, P, SZ, P]),
+        # include/sparse_ffn_mx4.h
+        "sparse_ffn_rms_norm": (C.c_int, [P, I32, I64, P, I64, I32, I32, P, I32, F64, P, I64, P, I32,
+                                          I64, P, I64, P]),
+        "sparse_ffn_quantize_mx4": (C.c_int, [P, I32, I64, I32, I32, P, I64, P, I64, P]),
+        "sparse_ffn_dequantize_mx4": (C.c_int, [P, I64, P, I64, I32, I32, P, I32, I64, P]),
+        "sparse_ffn_mx4_matmul_work_bytes": (SZ, [I32, I32, I32, I32]),
+        "sparse_ffn_mx4_matmul": (C.c_int, [P, I32, P, I64, I64, I32, I32, P, I64, P, I64, P, I32, P,
+                                            I32, I64, P, SZ, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -117,6 +127,9 @@ EXPORTED = ("sparse_ffn_workspace_bytes", "sparse_ffn_create", "sparse_ffn_destr
 EXPORTED_EXPERTS = ("sparse_ffn_route", "sparse_ffn_quantize_rows",
                     "sparse_ffn_i8_matmul_work_bytes", "sparse_ffn_i8_matmul",
                     "sparse_ffn_experts_work_bytes", "sparse_ffn_experts")
+# the entry points of include/sparse_ffn_mx4.h
+EXPORTED_MX4 = ("sparse_ffn_rms_norm", "sparse_ffn_quantize_mx4", "sparse_ffn_dequantize_mx4",
+                "sparse_ffn_mx4_matmul_work_bytes", "sparse_ffn_mx4_matmul")
 
 
 def lib():
@@ -271,3 +284,35 @@ def sparse_ffn_experts(desc: SffnExpertsDesc, x, x_dtype, ldx, T, idx, weights, 
     _fits(T | k, "sparse_ffn_experts")
     _ck(_lib.sparse_ffn_experts(C.byref(desc), x, x_dtype, ldx, T, idx, weights, k, y, y_dtype, ldy,
                                 work, work_bytes, stream), "sparse_ffn_experts")
+
+
+def sparse_ffn_rms_norm(x, dtype, ldx, residual, ldr, rows, cols, w, w_dtype, eps, total, ldsum, y,
+                        y_dtype, ldy, scale, lds, stream) -> None:
+    _fits(rows | cols, "sparse_ffn_rms_norm")
+    _ck(_lib.sparse_ffn_rms_norm(x, dtype, ldx, residual, ldr, rows, cols, w, w_dtype, eps, total, ldsum,
+                                 y, y_dtype, ldy, scale, lds, stream), "sparse_ffn_rms_norm")
+
+
+def sparse_ffn_quantize_mx4(x, dtype, ldx, rows, cols, q, ldq, scale, lds, stream) -> None:
+    _fits(rows | cols, "sparse_ffn_quantize_mx4")
+    _ck(_lib.sparse_ffn_quantize_mx4(x, dtype, ldx, rows, cols, q, ldq, scale, lds, stream),
+        "sparse_ffn_quantize_mx4")
+
+
+def sparse_ffn_dequantize_mx4(q, ldq, scale, lds, rows, cols, y, dtype, ldy, stream) -> None:
+    _fits(rows | cols, "sparse_ffn_dequantize_mx4")
+    _ck(_lib.sparse_ffn_dequantize_mx4(q, ldq, scale, lds, rows, cols, y, dtype, ldy, stream),
+        "sparse_ffn_dequantize_mx4")
+
+
+def sparse_ffn_mx4_matmul_work_bytes(x_dtype, M, N, K) -> int:
+    if (M | N | K) >> 31:
+        return C.c_size_t(-1).value
+    return int(_lib.sparse_ffn_mx4_matmul_work_bytes(x_dtype, M, N, K))
+
+
+def sparse_ffn_mx4_matmul(x, x_dtype, x_scale, ldx, ldxs, M, K, w, ldw, w_scale, ldws, bias, N, y,
+                          y_dtype, ldy, work, work_bytes, stream) -> None:
+    _fits(M | N | K, "sparse_ffn_mx4_matmul")
+    _ck(_lib.sparse_ffn_mx4_matmul(x, x_dtype, x_scale, ldx, ldxs, M, K, w, ldw, w_scale, ldws, bias, N,
+                                   y, y_dtype, ldy, work, work_bytes, stream), "sparse_ffn_mx4_matmul")
