@@ -4,19 +4,14 @@
 // of two such rows is the exact whole-number sum of q_j w_j (at most 131071 products of two
 // 8-bit values fit 32 bits), times the two rows' scales.
 #include <algorithm>
-#include <atomic>
 
 #include "sffn_device.h"
 #include "sffn_i8.h"
+#include "sffn_pipeline.h"
 #include "sffn_rows.h"
 
 namespace sffn {
 namespace {
-
-typedef int int4_t __attribute__((ext_vector_type(4)));
-
-// s_waitcnt operand (gfx9 encoding): LDS accesses only (lgkmcnt 0, vmcnt and expcnt at most)
-constexpr int I8_WAIT_LGKM0 = 0xC07F;
 
 // A workgroup of W waves takes a row. NV groups of four values per thread stay in registers
 // between the maximum and the rounding, so the row is read once (NV = 0: longer rows, twice).
@@ -317,29 +312,6 @@ __device__ __forceinline__ int row_of_out(const ProductArgs& a, int r) {
 template <int MODE>
 __device__ __forceinline__ int row_of_x(const ProductArgs& a, int r) {
   return MODE == MODE_ACT || MODE == MODE_ACT_GATED ? a.src[r] / a.k : r;
-}
-
-// LDS accesses before it are done, in every wave of the workgroup, before any after it; loads
-// from memory stay in flight.
-__device__ __forceinline__ void lds_barrier() {
-  asm volatile("" ::: "memory");
-  __builtin_amdgcn_s_waitcnt(I8_WAIT_LGKM0);
-  __builtin_amdgcn_s_barrier();
-  asm volatile("" ::: "memory");
-}
-
-// The stream of weights reads whole 128-byte lines: one load takes 8 rows x 128 bytes, lane
-// (r16 = lane % 16, g = lane / 16) the 16-byte chunk g + 4 (r16 / 8) of row r16 % 8, and a second
-// one the 8 rows after them. The matrix cores want chunk g (then 4 + g) of row r16 in that
-// lane: the two loads' values change places between the halves of each 16 lanes. Loads of 16
-// rows x 64 bytes need no change but halve the lines: 6.1 against 6.9 TB/s for a plain stream.
-constexpr int DPP_ROW_ROR8 = 0x128;
-__device__ __forceinline__ void to_steps(const int4_t& a, const int4_t& b, int4_t& s0, int4_t& s1) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    s0[i] = __builtin_amdgcn_update_dpp(a[i], b[i], DPP_ROW_ROR8, 0xF, 0xC, false);
-    s1[i] = __builtin_amdgcn_update_dpp(b[i], a[i], DPP_ROW_ROR8, 0xF, 0x3, false);
-  }
 }
 
 // Few rows: the weights are streamed from memory once, straight into the matrix cores'
@@ -861,21 +833,6 @@ __global__ __launch_bounds__(TD_W * 64) void k_token_down(ProductArgs a, const f
 // of w and of x need 64 KB a stage, a 128 x 64 part for each of 8 waves 24 KB of LDS reads against
 // 32 products' 1024 cycles; 256 x 128 tiles take 7% longer, 128 x 128 20%, 32 x 32 products 5%,
 // four waves 45%.
-// this lane's 16 bytes at src to place 16 * lane of the 1 KB block at dst (LDS)
-__device__ __forceinline__ void load_block(const int8_t* src, int8_t* dst) {
-  __builtin_amdgcn_global_load_lds(reinterpret_cast<const u32x4*>(src),
-                                   (__attribute__((address_space(3))) void*)dst, 16, 0, 0);
-}
-
-// until at most N of this wave's loads are in flight
-template <int N>
-__device__ __forceinline__ void wait_loads() {
-  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
-}
-
-// instruction kinds of __builtin_amdgcn_sched_group_barrier
-constexpr int SG_MFMA = 0x8, SG_LOAD = 0x20, SG_LDS_READ = 0x100;
-
 template <int MODE, int CH, int TK, int WC, int WT, int NS>
 __global__ __launch_bounds__(WC * WT * 64) void k_product(ProductArgs a) {
   constexpr bool G = MODE == MODE_ACT_GATED;
@@ -1038,24 +995,6 @@ void tile_launch(const ProductArgs& a, int64_t row_tiles, hipStream_t s) {
   const int64_t tiles = row_tiles * ((a.n + NT - 1) / NT);
   k_product<MODE, CH, TK, WC, WT, NS>
       <<<dim3((unsigned)((tiles + 7) / 8 * 8)), dim3(WC * WT * 64), 0, s>>>(a);
-}
-
-// Workgroups of a kernel that the current device holds at once. The last answer is kept: device,
-// dynamic LDS (below 2^24) and number in one word.
-template <auto Kernel>
-int resident(int threads, size_t lds) {
-  static std::atomic<uint64_t> kept{0};
-  int dev = 0, cus = 0, per = 0;
-  if (hipGetDevice(&dev) != hipSuccess) return 512;
-  const uint64_t key = ((uint64_t)(dev + 1) << 48) | ((uint64_t)lds << 24);
-  const uint64_t last = kept.load(std::memory_order_relaxed);
-  if ((last & ~(uint64_t)0xFFFFFF) == key) return (int)(last & 0xFFFFFF);
-  if (hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess ||
-      hipOccupancyMaxActiveBlocksPerMultiprocessor(&per, Kernel, threads, lds) != hipSuccess)
-    return 512;
-  const int n = std::min(std::max(1, cus * per), 0xFFFFFF);
-  kept.store(key | (uint64_t)n, std::memory_order_relaxed);
-  return n;
 }
 
 template <int MODE, int NR, typename X, int W, int SK>

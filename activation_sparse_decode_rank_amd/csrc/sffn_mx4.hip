@@ -6,11 +6,12 @@
 
 #include "sffn_mx4.h"
 #include "sffn_mx4_rows.h"
+#include "sffn_pipeline.h"
 
 namespace sffn {
 namespace {
 
-typedef int int4_t __attribute__((ext_vector_type(4)));
+typedef int int2_t __attribute__((ext_vector_type(2)));
 typedef int int8_vec __attribute__((ext_vector_type(8)));
 
 constexpr int FMT_FP4 = 4;  // the instruction's operand format
@@ -21,6 +22,17 @@ __device__ __forceinline__ float4_t mfma16(const int4_t& w, const int4_t& x, con
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
       int8_vec{w[0], w[1], w[2], w[3], 0, 0, 0, 0}, int8_vec{x[0], x[1], x[2], x[3], 0, 0, 0, 0}, acc,
       FMT_FP4, FMT_FP4, SW, sw, SX, sx);
+}
+
+typedef float float16_t __attribute__((ext_vector_type(16)));
+
+// acc += the products of 32 rows of w and 32 rows of x, two blocks long. Lane (r32 = lane % 32,
+// h = lane / 32) holds block h of row r32 of either operand; S: the byte of sw and sx.
+template <int S>
+__device__ __forceinline__ float16_t mfma32(const int4_t& w, const int4_t& x, const float16_t& acc, int sw, int sx) {
+  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+      int8_vec{w[0], w[1], w[2], w[3], 0, 0, 0, 0}, int8_vec{x[0], x[1], x[2], x[3], 0, 0, 0, 0}, acc,
+      FMT_FP4, FMT_FP4, S, sw, S, sx);
 }
 
 // Four neighbouring sums of a row as outputs
@@ -37,58 +49,564 @@ __device__ __forceinline__ void emit4(const Mx4ProductArgs& a, int64_t r, int c,
   else store4<__bf16>(a.out, o, v, a.n - c);
 }
 
-// 64 channels x 64 rows of x a workgroup, 16 channels a wave, operands straight from memory.
-__global__ __launch_bounds__(TPB) void k_mx4_product(Mx4ProductArgs a) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+// Few rows: the weights are streamed from memory once, straight into the matrix cores' registers. W
+// waves take a tile of 16 rows of w and up to 16 rows of x, one block of 256 bytes of the length (16
+// blocks of numbers, whose scales are 16 bytes) after the other in turn. Three buffers of a block
+// take turns: one is refilled, with the block three ahead, also across the end of a tile, as soon
+// as its products are issued. The waves' sums of a tile meet in LDS and are added in the waves'
+// order. Each workgroup first holds the rows of x in 4-bit blocks in its own LDS while its first
+// weights are on their way (X = uint8_t: copies those of x that are so held): that costs less than
+// a launch before this one, and x is then read from there for every tile.
+constexpr int G_BLK = host::kMx4Group;  // blocks of numbers (16 bytes of codes) a block of the stream
+
+template <typename X, int W>
+__global__ __launch_bounds__(W * 64, 4) void k_mx4_few(Mx4ProductArgs a) {
+  constexpr bool HELD = std::is_same<X, uint8_t>::value;
+  __shared__ __attribute__((aligned(16))) float4_t s_sum[2 * W * 64];  // [tile parity][wave][lane]
+  extern __shared__ __attribute__((aligned(16))) uint8_t s_x[];        // codes, then scales
+  const int nnt = (a.n + 15) / 16;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r16 = lane & 15, g = lane >> 4;
-  const int nnt = (a.n + 63) / 64;
-  const int n0 = (blockIdx.x % nnt) * 64 + wave * 16;
-  const int r0 = (int)(blockIdx.x / nnt) * 64;
-  const int wr = min(n0 + r16, a.n - 1);
-  const uint8_t* w = a.w + (size_t)wr * a.ldw;
-  const uint8_t* ws = a.ws + (size_t)wr * a.ldws;
-  const uint8_t *x[4], *xs[4];
+  const int nbk = (a.nb + G_BLK - 1) / G_BLK;
+  // Lane g of four (16 lanes apart) loads word g of a row's 16 scales; the instruction wants bytes
+  // g, 4 + g, 8 + g and 12 + g in it: the bytes change places like a 4 x 4 matrix's, between lanes
+  // 32 apart, then 16 apart.
+  const unsigned far = g < 2 ? 0x05040100u : 0x07060302u, near = g & 1 ? 0x07030501u : 0x06020400u;
+  auto to_scales = [&](unsigned v) {
+    const auto p = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    const unsigned q = __builtin_amdgcn_perm(p[1], p[0], far);
+    const auto r = __builtin_amdgcn_permlane16_swap(q, q, false, false);
+    return __builtin_amdgcn_perm(r[1], r[0], near);
+  };
+  // the stream: next block (tile, block of it) to load
+  const int lc = g + 4 * (r16 >> 3);  // chunk of 128 bytes that this lane loads
+  int ft = blockIdx.x, fb = wave;
+  const uint8_t *wbase = nullptr, *sbase = nullptr;  // first rows of that tile, one for all lanes
+  unsigned wrow[2], srow;  // this lane's two rows of codes, and its row of scales, from there
+  auto aim = [&]() {
+    const int n0 = ft * 16;
+    wbase = a.w + (size_t)n0 * a.ldw;
+    sbase = a.ws + (size_t)n0 * a.ldws;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int r = min(r0 + 16 * j + r16, a.rows - 1);
-    x[j] = a.x + (size_t)r * a.ldx;
-    xs[j] = a.xs + (size_t)r * a.ldxs;
-  }
-  float4_t acc[4];
+    for (int q = 0; q < 2; ++q) wrow[q] = (unsigned)min((r16 & 7) + 8 * q, a.n - 1 - n0) * (unsigned)a.ldw;
+    srow = (unsigned)min(r16, a.n - 1 - n0) * (unsigned)a.ldws + 4 * g;
+  };
+  struct Block {
+    int4_t w[4];
+    unsigned s;
+  };
+  auto fetch = [&](Block& B) {
+    if (ft >= nnt) return;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) acc[j] = float4_t{0.f, 0.f, 0.f, 0.f};
-  for (int b0 = 0; b0 < a.nb; b0 += 4) {
-    const int b = b0 + g;
-    int4_t f = {0, 0, 0, 0}, v[4];
-    int s = 127, vs[4];
-    if (b < a.nb) {
-      f = *reinterpret_cast<const int4_t*>(w + 16 * b);
-      s = ws[b];
+    for (int s = 0; s < 4; s += 2) {
+      // past w's row x is zero, so any chunk will do
+      const unsigned c = (unsigned)min(fb * G_BLK + s * 4 + lc, a.nb - 1) * 16;
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+        B.w[s + q] = __builtin_nontemporal_load(reinterpret_cast<const int4_t*>(wbase + (size_t)(wrow[q] + c)));
     }
+    B.s = *reinterpret_cast<const unsigned*>(sbase + (size_t)(srow + (unsigned)fb * 16));
+    fb += W;
+    if (fb >= nbk) {
+      fb = wave;
+      ft += gridDim.x;
+      if (ft < nnt) aim();
+    }
+  };
+  int t = blockIdx.x;
+  const bool works = wave < nbk;  // a wave past the blocks of a row only meets the others
+  Block ring[3];
+  if (works && t < nnt) {
+    aim();
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      v[j] = int4_t{0, 0, 0, 0};
-      vs[j] = 127;
-      if (b < a.nb) {
-        v[j] = *reinterpret_cast<const int4_t*>(x[j] + 16 * b);
-        vs[j] = xs[j][b];
+    for (int i = 0; i < 3; ++i) fetch(ring[i]);
+  }
+  // x's rows: codes [rows][nbk * 256], scales [rows][nbk] of four words, word g the bytes of blocks
+  // g, 4 + g, 8 + g and 12 + g
+  uint8_t* sc = s_x + (size_t)a.rows * nbk * 256;
+  auto scale_at = [&](int r, int b) { return (size_t)(r * nbk + (b >> 4)) * 16 + (b & 3) * 4 + (b >> 2 & 3); };
+  for (int r = 0; r < a.rows; ++r) {
+    uint8_t* q = s_x + (size_t)r * nbk * 256;
+    if constexpr (HELD) {
+      for (int b = tid; b < nbk * G_BLK; b += W * 64) {
+        int4_t v = {0, 0, 0, 0};
+        if (b < a.nb) v = *reinterpret_cast<const int4_t*>(a.x + (size_t)r * a.ldx + 16 * b);
+        *reinterpret_cast<int4_t*>(q + 16 * b) = v;
+        sc[scale_at(r, b)] = b < a.nb ? a.xs[(size_t)r * a.ldxs + b] : 127;
+      }
+    } else {
+      const X* x = reinterpret_cast<const X*>(a.x) + (size_t)r * a.ldx;
+      for (int i = tid; i < nbk * G_BLK * 4; i += W * 64) {
+        unsigned E;
+        reinterpret_cast<unsigned*>(q)[i] = mx4_encode(load8(x, i, a.cols), E);
+        if ((i & 3) == 0) sc[scale_at(r, i >> 2)] = (uint8_t)E;
       }
     }
-#pragma unroll
-    for (int j = 0; j < 4; ++j) acc[j] = mfma16<0, 0>(f, v[j], acc[j], s, vs[j]);
   }
+  lds_barrier();
+  const int xr = min(r16, a.rows - 1);
+  const uint8_t* fx = s_x + (size_t)xr * nbk * 256 + g * 16;
+  const uint8_t* fs = sc + (size_t)xr * nbk * 16 + g * 4;
+  float4_t acc = {0.f, 0.f, 0.f, 0.f};
+  int b = wave, par = 0;
+  auto end_tile = [&]() {
+    float4_t* sum = s_sum + par * W * 64 + lane;
+    sum[wave * 64] = acc;
+    // The sums of the tile two before this one were read before their reader's arrival here, and
+    // the other parity's are free to be written after it.
+    lds_barrier();
+    if (wave == 0) {
+      float4_t v = sum[0];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int r = r0 + 16 * j + r16;
-    if (r < a.rows) emit4(a, r, n0 + 4 * g, acc[j]);
+      for (int q = 1; q < W; ++q) {
+        const float4_t u = sum[q * 64];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] += u[e];
+      }
+      if (r16 < a.rows) emit4(a, r16, t * 16 + 4 * g, v);
+    }
+    acc = float4_t{0.f, 0.f, 0.f, 0.f};
+    par ^= 1;
+    b = wave;
+    t += gridDim.x;
+  };
+  if (!works) {
+    while (t < nnt) end_tile();
+    return;
   }
+  auto block = [&](Block& B) {
+    unsigned sw = to_scales(B.s);
+    const int sx = *reinterpret_cast<const int*>(fs + b * 16);
+    if ((b + 1) * G_BLK > a.nb) {  // past the row's end the scales may be anything: 1 stands there
+      const int left = (a.nb - b * G_BLK - g + 3) >> 2;  // steps of this lane
+      const unsigned keep = left >= 4 ? ~0u : (1u << (8 * max(left, 0))) - 1;
+      sw = (sw & keep) | (0x7f7f7f7fu & ~keep);
+    }
+    auto pair = [&](auto s0) {
+      constexpr int s = decltype(s0)::value;
+      int4_t w[2];
+      to_steps(B.w[s], B.w[s + 1], w[0], w[1]);
+      const uint8_t* x = fx + b * 256 + s * 64;
+      acc = mfma16<s, s>(w[0], *reinterpret_cast<const int4_t*>(x), acc, (int)sw, sx);
+      acc = mfma16<s + 1, s + 1>(w[1], *reinterpret_cast<const int4_t*>(x + 64), acc, (int)sw, sx);
+    };
+    pair(std::integral_constant<int, 0>{});
+    pair(std::integral_constant<int, 2>{});
+    fetch(B);
+    b += W;
+    if (b >= nbk) end_tile();
+  };
+  while (t < nnt) {
+    block(ring[0]);
+    if (t >= nnt) break;
+    block(ring[1]);
+    if (t >= nnt) break;
+    block(ring[2]);
+  }
+}
+
+// Many rows: a workgroup of WC x WT waves takes CH rows of w (channels) and TK rows of x over the
+// whole length, in stages of 128 bytes (256 values), a whole line of every row. Both operands go
+// from memory straight into LDS, two stages deep; row r of 32 holds its 16-byte chunk c at place
+// c ^ (r / 2 % 8), so that the lanes that LDS serves together touch different banks. A stage is
+// four steps of two blocks; a step's operands are read while the products of the step before it
+// run. Before the last step's products every wave is done with the stage's LDS and the next stage
+// has landed: they run while the freed stage is refilled and the next stage's first operands are
+// read. The scales, 16 bytes of a row for two stages, lie beside the stages; a lane's eight of them
+// (blocks h, 2 + h, .., 14 + h) become two words by two permutations, and the matrix instruction
+// takes the byte of its step.
+// A wave's rows of w are dealt so that a lane's 16 sums are neighbouring channels.
+template <int CH, int TK, int WC, int WT>
+__global__ __launch_bounds__(WC * WT * 64) void k_mx4_tiles(Mx4ProductArgs a) {
+  constexpr int W = WC * WT, NS = 2;
+  constexpr int NI = CH / 32 / WC, NJ = TK / 32 / WT;  // 32 x 32 tiles of a wave
+  constexpr int ROWS = CH + TK, STAGE = ROWS * 128;
+  constexpr int UW = CH / 8, DPS = ROWS / 8 / W;       // 1 KB loads of w a stage; of one wave
+  constexpr int SG = ROWS / 64, SPW = (SG + W - 1) / W;  // 1 KB loads of scales for two stages
+  static_assert(ROWS / 8 % W == 0 && W % 2 == 0 && CH % 64 == 0 && TK % 64 == 0, "whole loads");
+  __shared__ __attribute__((aligned(16))) int8_t sbuf[NS * STAGE];
+  __shared__ __attribute__((aligned(16))) int8_t s_scale[2 * ROWS * 16];
+  const int nnt = (a.n + CH - 1) / CH, nmt = (a.rows + TK - 1) / TK;
+  // Tiles in runs of 4 row tiles, channels outer; workgroups 8 apart run on one XCD, and each XCD
+  // takes a run of neighbours.
+  const int total = nmt * nnt, per = (total + 7) / 8;
+  const int id = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
+  if ((int)(blockIdx.x >> 3) >= per || id >= total) return;
+  const int run = id / (4 * nnt), in = id % (4 * nnt);
+  const int rm = min(4, nmt - run * 4);
+  const int r0 = (run * 4 + in % rm) * TK, n0 = in / rm * CH;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wc = wave % WC, wt = wave / WC;
+  const int r32 = lane & 31, h = lane >> 5;
+  // the channel behind row R of the tile
+  auto channel = [](int R) { return (R & ~31) + 16 * ((R >> 2) & 1) + 4 * ((R >> 3) & 3) + (R & 3); };
+  const uint8_t* wbase = a.w + (size_t)n0 * a.ldw;
+  const uint8_t* xbase = a.x + (size_t)r0 * a.ldx;
+  // this lane's rows, in bytes from there (below 2^32: 256 rows, 2^24 apart at most)
+  unsigned row[DPS];
+#pragma unroll
+  for (int v = 0; v < DPS; ++v) {
+    const int u = wave + W * v, R = 8 * u + (lane >> 3);
+    row[v] = u < UW ? (unsigned)min(channel(R), a.n - 1 - n0) * (unsigned)a.ldw
+                    : (unsigned)min(R - CH, a.rows - 1 - r0) * (unsigned)a.ldx;
+  }
+  // the chunk of a line that this lane loads (its row of 32 is 8 (u % 4) + lane / 8)
+  const int lc = (lane & 7) ^ ((wave & 1) * 4 + (lane >> 4));
+  const uint8_t* sc[SPW];
+#pragma unroll
+  for (int v = 0; v < SPW; ++v) {
+    const int R = ((wave + W * v) % SG) * 64 + lane;
+    sc[v] = R < CH ? a.ws + (size_t)min(n0 + channel(R), a.n - 1) * a.ldws
+                   : a.xs + (size_t)min(r0 + R - CH, a.rows - 1) * a.ldxs;
+  }
+  const int nst = (a.nb + 7) / 8;
+  auto issue = [&](int st, int buf) {
+    const int kc = st * 8 + lc;
+    const unsigned k = (unsigned)min(kc, a.nb - 1) * 16;  // past the row's end any chunk will do
+#pragma unroll
+    for (int v = 0; v < DPS; ++v) {
+      const int u = wave + W * v;
+      load_block(reinterpret_cast<const int8_t*>((u < UW ? wbase : xbase) + (size_t)(row[v] + k)),
+                 sbuf + buf * STAGE + u * 1024);
+    }
+  };
+  auto issue_scales = [&](int grp) {
+#pragma unroll
+    for (int v = 0; v < SPW; ++v)
+      load_block(reinterpret_cast<const int8_t*>(sc[v] + (size_t)grp * 16),
+                 s_scale + (grp & 1) * ROWS * 16 + ((wave + W * v) % SG) * 1024);
+  };
+  float16_t acc[NI][NJ];
+#pragma unroll
+  for (int i = 0; i < NI; ++i)
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
+  struct Frags {
+    int4_t w[NI], x[NJ];
+  };
+  struct Scales {
+    int w[2][NI], x[2][NJ];
+  } S;
+  auto read_frags = [&](Frags& F, int buf, int step) {
+    const int8_t* base = sbuf + buf * STAGE + r32 * 128 + (((2 * step + h) ^ (r32 >> 1)) & 7) * 16;
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+      F.x[j] = *reinterpret_cast<const int4_t*>(base + (CH / 32 + wt * NJ + j) * 4096);
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+      F.w[i] = *reinterpret_cast<const int4_t*>(base + (wc * NI + i) * 4096);
+  };
+  const unsigned pick = h ? 0x07050301u : 0x06040200u;  // odd or even bytes of eight
+  // Scales of group grp (16 blocks). Past the row's end, in the last group, the bytes may be
+  // anything: 1 stands there.
+  auto read_scales = [&](int grp) {
+    const int8_t* base = s_scale + (grp & 1) * ROWS * 16 + r32 * 16;
+    unsigned keep[2];
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const int left = (a.nb - grp * 16 - 8 * q - h + 1) >> 1;  // blocks of this lane
+      keep[q] = left >= 4 ? ~0u : (1u << (8 * max(left, 0))) - 1;
+    }
+    auto get = [&](int R, int& s0, int& s1) {
+      const int4_t v = *reinterpret_cast<const int4_t*>(base + R * 16);
+      s0 = (int)((__builtin_amdgcn_perm((unsigned)v[1], (unsigned)v[0], pick) & keep[0]) | (0x7f7f7f7fu & ~keep[0]));
+      s1 = (int)((__builtin_amdgcn_perm((unsigned)v[3], (unsigned)v[2], pick) & keep[1]) | (0x7f7f7f7fu & ~keep[1]));
+    };
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) get(CH + (wt * NJ + j) * 32, S.x[0][j], S.x[1][j]);
+#pragma unroll
+    for (int i = 0; i < NI; ++i) get((wc * NI + i) * 32, S.w[0][i], S.w[1][i]);
+  };
+  auto products = [&](const Frags& F, auto step) {  // step of the group, 0 .. 7
+    constexpr int Q = decltype(step)::value / 4, B = decltype(step)::value % 4;
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) acc[i][j] = mfma32<B>(F.w[i], F.x[j], acc[i][j], S.w[Q][i], S.x[Q][j]);
+  };
+  constexpr int READS = NI + NJ, PER = NI * NJ / READS > 0 ? NI * NJ / READS : 1;
+  constexpr int LOADS = (DPS + READS - 1) / READS;
+  auto barrier = [&]() {
+    __builtin_amdgcn_s_waitcnt(I8_WAIT_LGKM0);  // this wave's reads are done
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+  };
+  // reads between the products, not before them
+  auto mix = [&]() {
+#pragma unroll
+    for (int q = 0; q < READS; ++q) {
+      __builtin_amdgcn_sched_group_barrier(SG_LDS_READ, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(SG_MFMA, PER, 0);
+    }
+  };
+  Frags F0, F1;
+  issue_scales(0);
+#pragma unroll
+  for (int st = 0; st < NS; ++st) issue(min(st, nst - 1), st);
+  wait_loads<0>();
+  barrier();
+  read_scales(0);
+  read_frags(F0, 0, 0);
+  int buf = 0;
+  // Stage st, the PH-th of its group. Past the last stage the refill loads the last stage again (in
+  // bounds, never read), so every stage has the same loads in flight and no branch.
+  auto stage = [&](int st, auto phase) {
+    constexpr int PH = decltype(phase)::value;
+    read_frags(F1, buf, 1);
+    products(F0, std::integral_constant<int, 4 * PH>{});
+    mix();
+    read_frags(F0, buf, 2);
+    products(F1, std::integral_constant<int, 4 * PH + 1>{});
+    mix();
+    read_frags(F1, buf, 3);
+    products(F0, std::integral_constant<int, 4 * PH + 2>{});
+    mix();
+    wait_loads<0>();
+    barrier();
+    if (PH == 0) issue_scales(min(st + NS, nst - 1) / 2);
+    issue(min(st + NS, nst - 1), buf);
+    buf ^= 1;
+    read_frags(F0, buf, 0);
+    products(F1, std::integral_constant<int, 4 * PH + 3>{});
+#pragma unroll
+    for (int q = 0; q < READS; ++q) {
+      __builtin_amdgcn_sched_group_barrier(SG_LDS_READ, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(SG_LOAD, LOADS, 0);
+      __builtin_amdgcn_sched_group_barrier(SG_MFMA, PER, 0);
+    }
+    if (PH == 1) read_scales((st + 1) / 2);
+  };
+  const int full = a.nb / 8;
+  int st = 0;
+  for (; st + 2 <= full; st += 2) {
+    stage(st, std::integral_constant<int, 0>{});
+    stage(st + 1, std::integral_constant<int, 1>{});
+  }
+  if (st < full) stage(st, std::integral_constant<int, 0>{});
+  if (full < nst) {
+    // the row ends inside the last stage: the codes of x past its end become zeros
+    if (full & 1) {
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) S.x[0][j] = S.x[1][j];
+#pragma unroll
+      for (int i = 0; i < NI; ++i) S.w[0][i] = S.w[1][i];
+    }
+    auto step = [&](auto s) {
+      constexpr int Q = decltype(s)::value;
+      if (Q > 0) read_frags(F0, buf, Q);
+      if (full * 8 + 2 * Q + h >= a.nb) {
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) F0.x[j] = int4_t{0, 0, 0, 0};
+      }
+      products(F0, s);
+    };
+    step(std::integral_constant<int, 0>{});
+    step(std::integral_constant<int, 1>{});
+    step(std::integral_constant<int, 2>{});
+    step(std::integral_constant<int, 3>{});
+  }
+  wait_loads<0>();  // no load may land in LDS after the loop
+  // lane holds row r32 of tile j and channels 16 h .. +15 of tile i
+#pragma unroll
+  for (int i = 0; i < NI; ++i) {
+    const int c = n0 + (wc * NI + i) * 32 + 16 * h;
+    if (c >= a.n) continue;
+    const int left = a.n - c;
+    float4_t b[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) b[q][e] = a.bias && 4 * q + e < left ? a.bias[c + 4 * q + e] : 0.f;
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      const int r = r0 + (wt * NJ + j) * 32 + r32;
+      if (r >= a.rows) continue;
+      const size_t o = (size_t)r * a.ldo + c;
+      float4_t v[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[q][e] = acc[i][j][4 * q + e] + b[q][e];
+#pragma unroll
+      for (int q = 0; q < 4; q += 2) {
+        if (a.out_type == T_F32) store8<float>(a.out, o + 4 * q, v[q], v[q + 1], left - 4 * q);
+        else if (a.out_type == T_F16) store8<_Float16>(a.out, o + 4 * q, v[q], v[q + 1], left - 4 * q);
+        else store8<__bf16>(a.out, o + 4 * q, v[q], v[q + 1], left - 4 * q);
+      }
+    }
+  }
+}
+
+// Some rows, and few tiles: eight waves share a tile of CH rows of w and TK rows of x and split the
+// length, in stages of 256 bytes (16 blocks, two lines of every row, NS stages deep): wave q takes
+// blocks 2 q and 2 q + 1 of each stage. A tile's chain of dependent products is an eighth as long,
+// which is what bounds a tile that a compute unit has to itself. A 16-byte chunk c of row r of 32
+// lies at place c ^ (r % 16) of the row's 16. At the end the waves' sums meet in LDS, and each wave
+// adds a share of them in the waves' order.
+template <int CH, int TK, int NS>
+__global__ __launch_bounds__(512) void k_mx4_split(Mx4ProductArgs a) {
+  constexpr int W = 8;
+  constexpr int NI = CH / 32, NJ = TK / 32;
+  constexpr int ROWS = CH + TK, STAGE = ROWS * 256;
+  constexpr int UW = CH / 4, UN = ROWS / 4, DPS = UN / W;  // 1 KB loads (4 rows) of w, of both; of one wave
+  constexpr int PIECES = NI * NJ * 4;
+  static_assert(UN % W == 0 && ROWS <= 256, "whole loads");
+  constexpr int BUF = NS * STAGE > W * PIECES * 1024 ? NS * STAGE : W * PIECES * 1024;
+  __shared__ __attribute__((aligned(16))) int8_t sbuf[BUF];
+  __shared__ __attribute__((aligned(16))) int8_t s_scale[NS * 256 * 16];
+  const int nnt = (a.n + CH - 1) / CH;
+  const int n0 = (int)(blockIdx.x % nnt) * CH, r0 = (int)(blockIdx.x / nnt) * TK;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int r32 = lane & 31, h = lane >> 5;
+  auto channel = [](int R) { return (R & ~31) + 16 * ((R >> 2) & 1) + 4 * ((R >> 3) & 3) + (R & 3); };
+  const uint8_t* wbase = a.w + (size_t)n0 * a.ldw;
+  const uint8_t* xbase = a.x + (size_t)r0 * a.ldx;
+  unsigned row[DPS];
+  int lc[DPS];  // the chunk that this lane loads
+#pragma unroll
+  for (int v = 0; v < DPS; ++v) {
+    const int u = wave + W * v, R = 4 * u + (lane >> 4);
+    row[v] = u < UW ? (unsigned)min(channel(R), a.n - 1 - n0) * (unsigned)a.ldw
+                    : (unsigned)min(R - CH, a.rows - 1 - r0) * (unsigned)a.ldx;
+    lc[v] = (lane & 15) ^ (R & 15);
+  }
+  // waves 0 to 3 load the scales of 64 rows each
+  const int sr = min(wave * 64 + lane, ROWS - 1);
+  const uint8_t* sc = sr < CH ? a.ws + (size_t)min(n0 + channel(sr), a.n - 1) * a.ldws
+                              : a.xs + (size_t)min(r0 + sr - CH, a.rows - 1) * a.ldxs;
+  const int nst = (a.nb + 15) / 16;
+  auto issue = [&](int st, int buf) {
+    if (wave < 4)
+      load_block(reinterpret_cast<const int8_t*>(sc + (size_t)st * 16), s_scale + buf * 4096 + wave * 1024);
+#pragma unroll
+    for (int v = 0; v < DPS; ++v) {
+      const int u = wave + W * v;
+      // past the row's end any chunk will do
+      const unsigned k = (unsigned)min(st * 16 + lc[v], a.nb - 1) * 16;
+      load_block(reinterpret_cast<const int8_t*>((u < UW ? wbase : xbase) + (size_t)(row[v] + k)),
+                 sbuf + buf * STAGE + u * 1024);
+    }
+  };
+  float16_t acc[NI][NJ];
+#pragma unroll
+  for (int i = 0; i < NI; ++i)
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
+#pragma unroll
+  for (int st = 0; st < NS - 1; ++st) issue(min(st, nst - 1), st);
+  const int c = 2 * wave + h;
+  const int8_t* at = sbuf + r32 * 256 + ((c ^ r32) & 15) * 16;
+  const int8_t* sat = s_scale + r32 * 16 + c;
+  int buf = 0;
+  for (int st = 0; st < nst; ++st) {
+    // the NS - 2 stages after this one stay in flight
+    if (wave < 4) wait_loads<(NS - 2) * (DPS + 1)>();
+    else wait_loads<(NS - 2) * DPS>();
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    int4_t fw[NI], fx[NJ];
+    int sw[NI], sx[NJ];
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      fx[j] = *reinterpret_cast<const int4_t*>(at + buf * STAGE + (NI + j) * 8192);
+      sx[j] = *reinterpret_cast<const uint8_t*>(sat + buf * 4096 + (NI + j) * 512);
+    }
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      fw[i] = *reinterpret_cast<const int4_t*>(at + buf * STAGE + i * 8192);
+      sw[i] = *reinterpret_cast<const uint8_t*>(sat + buf * 4096 + i * 512);
+    }
+    // the buffer of the stage before this one is free: every wave read it before the barrier
+    issue(min(st + NS - 1, nst - 1), buf == 0 ? NS - 1 : buf - 1);
+    if (st * 16 + c >= a.nb) {  // past the row's end: codes of zero and scales of 1
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) {
+        fx[j] = int4_t{0, 0, 0, 0};
+        sx[j] = 127;
+      }
+#pragma unroll
+      for (int i = 0; i < NI; ++i) sw[i] = 127;
+    }
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) acc[i][j] = mfma32<0>(fw[i], fx[j], acc[i][j], sw[i], sx[j]);
+    buf = buf + 1 == NS ? 0 : buf + 1;
+    __builtin_amdgcn_s_waitcnt(I8_WAIT_LGKM0);  // this wave's reads are done before the next barrier
+  }
+  wait_loads<0>();  // no load may land in LDS after the loop
+  lds_barrier();
+  float4_t* sums = reinterpret_cast<float4_t*>(sbuf) + lane;  // [wave][piece][lane]
+#pragma unroll
+  for (int i = 0; i < NI; ++i)
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        sums[(wave * PIECES + (i * NJ + j) * 4 + q) * 64] =
+            float4_t{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+  lds_barrier();
+  for (int p = wave; p < PIECES; p += W) {
+    float4_t v = sums[p * 64];
+#pragma unroll
+    for (int k = 1; k < W; ++k) {
+      const float4_t u = sums[(k * PIECES + p) * 64];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] += u[e];
+    }
+    const int i = p / (4 * NJ), j = p / 4 % NJ, q = p & 3;
+    const int r = r0 + j * 32 + r32;
+    if (r < a.rows) emit4(a, r, n0 + i * 32 + 16 * h + 4 * q, v);
+  }
+}
+
+template <int CH, int TK, int NS>
+void split_launch(const Mx4ProductArgs& a, hipStream_t s) {
+  const int64_t tiles = (((int64_t)a.rows + TK - 1) / TK) * (((int64_t)a.n + CH - 1) / CH);
+  k_mx4_split<CH, TK, NS><<<dim3((unsigned)tiles), dim3(512), 0, s>>>(a);
+}
+
+template <int CH, int TK, int WC, int WT>
+void tile_launch(const Mx4ProductArgs& a, hipStream_t s) {
+  const int64_t tiles = (((int64_t)a.rows + TK - 1) / TK) * (((int64_t)a.n + CH - 1) / CH);
+  k_mx4_tiles<CH, TK, WC, WT>
+      <<<dim3((unsigned)((tiles + 7) / 8 * 8)), dim3(WC * WT * 64), 0, s>>>(a);
+}
+
+// Eight waves a tile: 1 row x 12288 x 49152 in 50 us (6.4 TB/s of weights and scales; four waves 52,
+// sixteen 81), 1 x 4096 x 11008 in 6.6 (four waves 7.1, sixteen 9.7).
+template <typename X>
+void few_launch(const Mx4ProductArgs& a, hipStream_t s) {
+  constexpr int W = 8;
+  const size_t lds = host::mx4_few_lds((size_t)a.rows, a.cols);
+  const int at_once = resident<k_mx4_few<X, W>>(W * 64, lds);
+  k_mx4_few<X, W><<<dim3((unsigned)std::min((a.n + 15) / 16, at_once)), dim3(W * 64), lds, s>>>(a);
 }
 
 }  // namespace
 
 hipError_t launch_mx4_product(const Mx4ProductArgs& a, hipStream_t s) {
-  const int64_t tiles = ((int64_t)a.n + 63) / 64 * (((int64_t)a.rows + 63) / 64);
-  k_mx4_product<<<dim3((unsigned)tiles), dim3(TPB), 0, s>>>(a);
+  switch (host::mx4_form((size_t)a.rows, (size_t)a.n, a.nb)) {
+    case host::kMx4Few: few_launch<uint8_t>(a, s); break;
+    case host::kMx4Split32: split_launch<32, 32, 3>(a, s); break;
+    case host::kMx4Split64: split_launch<64, 64, 3>(a, s); break;
+    case host::kMx4Tile64: tile_launch<64, 64, 2, 2>(a, s); break;
+    case host::kMx4Tile64x128: tile_launch<64, 128, 2, 2>(a, s); break;
+    case host::kMx4Tile128: tile_launch<128, 128, 2, 2>(a, s); break;
+    default: tile_launch<256, 256, 4, 2>(a, s); break;
+  }
+  return hipGetLastError();
+}
+
+hipError_t launch_mx4_few(const Mx4ProductArgs& a, int x_type, hipStream_t s) {
+  if (x_type == T_F32) few_launch<float>(a, s);
+  else if (x_type == T_F16) few_launch<_Float16>(a, s);
+  else few_launch<__bf16>(a, s);
   return hipGetLastError();
 }
 

@@ -175,8 +175,8 @@ def check_product(got, x, w, bias, dtype):
     """x, w: 64-bit values of the rows in blocks."""
     want, mag = ref.matmul(x, w, bias)
     got = f64(got)
-    bad = np.isnan(want)
-    assert np.array_equal(np.isnan(got), bad)
+    bad = np.isnan(mag)  # a NaN block reaches these
+    assert np.isnan(got[bad]).all()
     with np.errstate(invalid="ignore"):
         err = (4 * ((x.shape[1] + 127) // 128) + 16) * U * mag + 2.0 ** -126
         fi = torch.finfo(dtype)
