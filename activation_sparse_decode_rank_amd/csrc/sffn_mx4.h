@@ -17,9 +17,12 @@ struct NormArgs {
   void* scale;      // I8: fp32 [rows]; MX4: bytes
   int64_t ldx, ldr, ldsum, ldy, lds;
   int rows, cols, w_type;
-  double eps;
+  double eps, per_col;  // per_col: 1 / cols
 };
 hipError_t launch_norm(const NormArgs& a, int x_type, int y_type, hipStream_t s);
+hipError_t launch_norm_f32(const NormArgs& a, int y_type, hipStream_t s);
+hipError_t launch_norm_f16(const NormArgs& a, int y_type, hipStream_t s);
+hipError_t launch_norm_bf16(const NormArgs& a, int y_type, hipStream_t s);
 
 // rows of x into blocks; blocks from the row's end up to `blocks` are written as zeros
 struct Mx4QuantArgs {

@@ -65,6 +65,7 @@ int sparse_ffn_rms_norm(const void* x, int32_t dtype, int64_t ldx, const void* r
   a.cols = cols;
   a.w_type = w_dtype;
   a.eps = eps;
+  a.per_col = 1.0 / cols;
   return status(sffn::launch_norm(a, dtype, y_dtype, static_cast<hipStream_t>(stream)));
 }
 

@@ -23,14 +23,15 @@ __device__ __forceinline__ int quantize(float x, float s, float r) {
   return qi;
 }
 
-// scale of a row from the bits of its largest magnitude; r = 1 / scale (0: a row of zeros)
+// scale of a row from the bits of its largest magnitude; r: 1 / scale but for its last places, which
+// decide nothing (0: a row of zeros)
 __device__ __forceinline__ float row_scale(unsigned bits, float& r) {
   const float a = __builtin_bit_cast(float, bits);
   r = 0.f;
   if (bits >= 0x7f800000u) return __builtin_nanf("");
   if (a < SMALLEST_ROW) return 0.f;
   const float s = a * (1.f / 127.f);
-  r = 1.f / s;
+  r = __builtin_amdgcn_rcpf(s);
   return s;
 }
 
@@ -68,25 +69,27 @@ __device__ __forceinline__ float4_t load4(const T* x, int i, int cols) {
 }
 
 // Four values of a row, packed. Almost always every remainder is clearly inside half a step and
-// q stands; the neighbours are looked at only where one is not.
+// q stands; the neighbours are looked at only where one is not. x r + 1.5 * 2^23 is rounded to a
+// whole number, and holds q in its lowest byte: four operations a value, and three permutations.
 __device__ __forceinline__ int quantize4(const float4_t& v, float s, float r) {
 #pragma clang fp contract(off)
+  constexpr float MAGIC = 12582912.f;
   const float lim = 0.4999f * s;
-  int q[4];
-  bool near = false;
+  unsigned q[4];
+  float far = 0.f;
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    const float f = rintf(v[e] * r);
-    near |= fabsf(__builtin_fmaf(-f, s, v[e])) > lim;
-    q[e] = (int)f;
+    const float f = __builtin_fmaf(v[e], r, MAGIC);
+    q[e] = __builtin_bit_cast(unsigned, f);
+    far = fmaxf(far, fabsf(__builtin_fmaf(-(f - MAGIC), s, v[e])));
   }
-  if (near) {
+  if (far > lim) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) q[e] = quantize(v[e], s, r);
+    for (int e = 0; e < 4; ++e) q[e] = (unsigned)quantize(v[e], s, r);
   }
-  const unsigned lo = (q[0] & 0xff) | ((q[1] & 0xff) << 8);
-  const unsigned hi = (q[2] & 0xff) | ((q[3] & 0xff) << 8);
-  return (int)(lo | (hi << 16));
+  const unsigned lo = __builtin_amdgcn_perm(q[1], q[0], 0x0c0c0400u);
+  const unsigned hi = __builtin_amdgcn_perm(q[3], q[2], 0x0c0c0400u);
+  return (int)__builtin_amdgcn_perm(hi, lo, 0x05040100u);
 }
 
 // Four neighbouring values of a row as T, the first `left` of them
