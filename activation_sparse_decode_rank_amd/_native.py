@@ -136,6 +136,11 @@ def lib():
     return _lib
 
 
+def address(name: str) -> int:
+    """Address of an entry point, for the extension module _calls."""
+    return C.cast(getattr(_lib, name), C.c_void_p).value
+
+
 def _ck(status: int, what: str):
     if status != SFFN_OK:
         raise SparseFFNError(status, what)

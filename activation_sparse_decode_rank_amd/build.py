@@ -1,4 +1,5 @@
-"""Build libsparse_ffn.so (HIP, gfx950 only) in-tree with hipcc.
+"""Build libsparse_ffn.so (HIP, gfx950 only) in-tree with hipcc, and _calls.so, the extension module
+that takes regular calls of mx4.py past ctypes, with the host compiler.
 
 Usage: python activation_sparse_decode_rank_amd/build.py   (or __graft_entry__.build()).
 Run it as a script: importing the package loads the library this builds.
@@ -7,10 +8,12 @@ directory, where the Python binding loads it.
 """
 from __future__ import annotations
 
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -18,6 +21,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libsparse_ffn.so")
+CALLS = os.path.join(HERE, "_calls.so")
 SOURCES = ["sffn_api.hip", "sffn_dispatch.hip", "sffn_stage1.hip", "sffn_decode_b1.hip", "sffn_batch.hip",
            "sffn_mid_bt_h4.hip", "sffn_mid_bt_h8.hip", "sffn_mid_bt_f4.hip", "sffn_mid_bt_f8.hip",
            "sffn_tiles.hip", "sffn_offline.hip", "sffn_measure.hip", "sffn_prefill.hip",
@@ -25,6 +29,7 @@ SOURCES = ["sffn_api.hip", "sffn_dispatch.hip", "sffn_stage1.hip", "sffn_decode_
            "sffn_experts_api.hip", "sffn_norm.hip", "sffn_norm_f32.hip", "sffn_norm_f16.hip",
            "sffn_norm_bf16.hip", "sffn_mx4.hip", "sffn_mx4_api.hip"]
 HIPCC = shutil.which("hipcc") or "/opt/rocm/bin/hipcc"
+CXX = shutil.which("g++") or "g++"
 
 FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-Wall",
@@ -46,10 +51,27 @@ def _compile(src: str) -> str:
     return obj
 
 
+def _compile_calls() -> None:
+    """_calls.so against torch's headers; its libraries are the ones that torch has loaded."""
+    torch = importlib.util.find_spec("torch").submodule_search_locations[0]
+    inc = [os.path.join(ROOT, "include"), os.path.join(torch, "include"),
+           os.path.join(torch, "include", "torch", "csrc", "api", "include"), sysconfig.get_paths()["include"]]
+    tmp = CALLS + ".tmp"
+    cmd = [CXX, "-O2", "-std=c++17", "-fPIC", "-shared", *(f"-I{i}" for i in inc),
+           os.path.join(CSRC, "sffn_calls.cpp"), "-L" + os.path.join(torch, "lib"), "-ltorch_python",
+           "-ltorch_cpu", "-lc10", "-o", tmp]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"sffn_calls.cpp failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, CALLS)
+
+
 def build(verbose: bool = True) -> str:
     os.makedirs(BUILD, exist_ok=True)
     with ThreadPoolExecutor(max_workers=min(len(SOURCES), os.cpu_count() or 4)) as ex:
+        calls = ex.submit(_compile_calls)
         objs = list(ex.map(_compile, SOURCES))
+        calls.result()
     tmp = LIB + ".tmp"
     cmd = [HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
@@ -57,7 +79,7 @@ def build(verbose: bool = True) -> str:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
     if verbose:
-        print(f"built {LIB}")
+        print(f"built {LIB} and {CALLS}")
     return LIB
 
 

@@ -14,6 +14,11 @@ There are no gradients. Rows in 4-bit blocks are two uint8 tensors: codes [..., 
 given for outputs must not overlap the inputs unless it is said. A call with `stream` goes to that
 stream and takes its outputs from that stream's memory: use them elsewhere only in order after it,
 and keep the inputs until it is done, or record_stream them.
+
+Calls on the current device and stream whose tensors lie as the library reads them go through the
+extension module _calls (csrc/sffn_calls.cpp), which does in one step what the functions here do: a
+third to a half of the host's time. Where it returns None the function goes on here, with copies,
+another stream or device, given outputs, or the error.
 """
 from __future__ import annotations
 
@@ -21,9 +26,23 @@ from typing import Optional, Tuple, Union
 
 import torch
 
+from . import _calls
 from . import _native as N
 from .experts import _F32, _I8, _TYPES, _U8, _on, _out, _out_dtype, _type, _vector, _work
-from .experts import _rows as _some_rows
+from .experts import _current, _rows as _some_rows
+
+_calls.bind(*(N.address(f) for f in ("sparse_ffn_rms_norm", "sparse_ffn_quantize_mx4",
+                                     "sparse_ffn_dequantize_mx4", "sparse_ffn_mx4_matmul_work_bytes",
+                                     "sparse_ffn_mx4_matmul")))
+_device = torch._C._cuda_getDevice
+_OUT = {None: -1, **_TYPES, "i8": N.SFFN_I8, "mx4": N.SFFN_MX4}
+
+
+def _done(got, what: str):
+    """What _calls returned: outputs, or a status."""
+    if type(got) is int:
+        raise N.SparseFFNError(got, what)
+    return got
 
 
 def _rows(t: torch.Tensor, name: str) -> Tuple[int, int]:
@@ -93,10 +112,15 @@ def rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, *,
     them; "mx4": returns codes and scales, as quantize_mx4 gives them for the float32 y and
     mx4_matmul takes them. With a residual (x's shape and type) v comes last, in residual_out where
     that is given: it may be the residual itself, or x."""
+    kind = _OUT.get(out)
+    i = x.device.index
+    if kind is not None and stream is None and i is not None and i == _device():
+        got = _calls.norm(x, weight, residual, eps, kind, residual_out, i, _current(i))
+        if got is not None:
+            return _done(got, "sparse_ffn_rms_norm")
     dt = _type(x, "x")
     if out is None:
-        out = x.dtype
-    kind = _OUT.get(out)
+        out, kind = x.dtype, dt
     if kind is None:
         raise ValueError("out must be float32, float16, bfloat16, 'i8' or 'mx4'")
     if (residual is None) and residual_out is not None:
@@ -150,13 +174,15 @@ def rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, *,
     return (y, residual_out) if scale is None else (y, scale, residual_out)
 
 
-_OUT = {**_TYPES, "i8": N.SFFN_I8, "mx4": N.SFFN_MX4}
-
-
 def quantize_mx4(x: torch.Tensor, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
     """The rows of x ([..., K]) in 4-bit blocks of 32: codes (uint8 [..., 16 B], two a byte) and
     scales (uint8 [..., B]), B = ceil(K / 32) (sparse_ffn_quantize_mx4). The scales' rows begin at
     multiples of 16 bytes, as the products want them."""
+    i = x.device.index
+    if stream is None and i is not None and i == _device():
+        got = _calls.quantize(x, i, _current(i))
+        if got is not None:
+            return _done(got, "sparse_ffn_quantize_mx4")
     dt = _type(x, "x")
     with _on(x, stream) as on:
         flat = _flat(x, stream)
@@ -173,6 +199,11 @@ def dequantize_mx4(q: torch.Tensor, scale: torch.Tensor, *, cols: Optional[int] 
     """The values that rows in 4-bit blocks stand for (sparse_ffn_dequantize_mx4): [..., cols] of
     dtype, cols at most 32 for each block (the default)."""
     dt = _TYPES.get(dtype)
+    i = q.device.index
+    if dt is not None and stream is None and i is not None and i == _device():
+        got = _calls.dequantize(q, scale, -1 if cols is None else cols, dt, i, _current(i))
+        if got is not None:
+            return _done(got, "sparse_ffn_dequantize_mx4")
     if dt is None:
         raise ValueError("dtype must be float32, float16 or bfloat16")
     if q.dim() < 1 or scale.dim() != q.dim() or q.shape[:-1] != scale.shape[:-1]:
@@ -196,6 +227,8 @@ def dequantize_mx4(q: torch.Tensor, scale: torch.Tensor, *, cols: Optional[int] 
 
 def _merged(t: torch.Tensor) -> torch.Tensor:
     """t [..., B] as a matrix of rows that all lie the same distance apart, without a copy."""
+    if 0 in t.shape:
+        return t.new_empty((0, t.shape[-1]))
     ld, rows = None, 1
     for i in range(t.dim() - 2, -1, -1):
         n = t.shape[i]
@@ -206,8 +239,6 @@ def _merged(t: torch.Tensor) -> torch.Tensor:
         elif t.stride(i) != ld * rows:
             raise ValueError("the rows of the scales must lie the same distance apart")
         rows *= n
-    if 0 in t.shape[:-1]:
-        rows = 0
     return t.as_strided((rows, t.shape[-1]), (t.shape[-1] if ld is None else ld, t.stride(-1)))
 
 
@@ -220,6 +251,12 @@ def mx4_matmul(x: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor, *,
     holds in 4-bit blocks first, or codes [M, 16 B] with x_scale [M, B]. out_dtype: float32,
     float16 or bfloat16 (default: x's type; float32 for codes). work: uint8 scratch (allocated here
     when None); calls that share one must be ordered."""
+    kind = _OUT.get(out_dtype)
+    i = x.device.index
+    if kind is not None and stream is None and y is None and work is None and i is not None and i == _device():
+        got = _calls.matmul(x, w, w_scale, x_scale, bias, kind, i, _current(i))
+        if got is not None:
+            return _done(got, "sparse_ffn_mx4_matmul")
     mx4 = x.dtype == _U8
     if mx4 != (x_scale is not None):
         raise ValueError("x_scale belongs to rows in 4-bit blocks, and they need it")

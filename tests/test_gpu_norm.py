@@ -293,3 +293,53 @@ def test_a_layer_of_them(P, T, bits):
     out, r2 = P.rms_norm(y, n1, residual=r, residual_out=r)
     assert r2.data_ptr() == r.data_ptr() and torch.equal(r2, y + (x + res))
     check(out, ref.norm(f64(r2), f64(n1)), torch.bfloat16)
+
+
+@pytest.mark.parametrize("shape", [(1, 40), (5, 64), (3, 4, 100), (77,), (0, 33), (2, 0, 33), (6, 1)])
+def test_both_ways_to_the_library(P, shape, monkeypatch):
+    """The extension module's calls and the functions' own give the same bits, shapes and strides; a
+    regular call takes the first way."""
+    import sys
+    say("both ways", shape)
+    M = sys.modules["activation_sparse_decode_rank_amd.mx4"]
+    g = rng(10, *shape)
+    x, r = dev(g.standard_normal(shape), torch.float16), dev(g.standard_normal(shape), torch.float16)
+    w = dev(g.standard_normal(shape[-1]))
+    n = int(np.prod(shape[:-1], dtype=np.int64))
+
+    class Off:
+        def __getattr__(self, name):
+            return lambda *a: None
+
+    def calls():
+        out = []
+        for kind in (None, torch.float32, "i8", "mx4"):
+            for res in (None, r):
+                got = P.rms_norm(x, w, residual=res, out=kind)
+                out += list(got) if isinstance(got, tuple) else [got]
+        out += list(P.rms_norm(x, residual=r, residual_out=torch.empty_like(x)))
+        q, s = P.quantize_mx4(x)
+        out += [q, s, P.dequantize_mx4(q, s, cols=shape[-1]), P.dequantize_mx4(q, s, dtype=torch.bfloat16)]
+        if n:
+            x2 = x.reshape(n, shape[-1])
+            q2, s2 = P.quantize_mx4(x2)
+            b = dev(np.arange(n))
+            out += [P.mx4_matmul(x2, q2, s2), P.mx4_matmul(q2, q2, s2, x_scale=s2, bias=b),
+                    P.mx4_matmul(x2, q2, s2, out_dtype=torch.bfloat16)]
+        return out
+
+    fast = calls()
+    monkeypatch.setattr(M, "_calls", Off())
+    slow = calls()
+    assert len(fast) == len(slow)
+    for a, b in zip(fast, slow):
+        assert a.shape == b.shape and a.dtype == b.dtype and torch.equal(a, b)
+        assert a.numel() == 0 or a.stride() == b.stride()
+    monkeypatch.undo()
+    if n and len(shape) == 2:
+        def no(*a):
+            raise AssertionError("the ctypes way was taken")
+        for f in ("sparse_ffn_rms_norm", "sparse_ffn_quantize_mx4", "sparse_ffn_dequantize_mx4",
+                  "sparse_ffn_mx4_matmul"):
+            monkeypatch.setattr(M.N, f, no)
+        calls()

@@ -209,3 +209,22 @@ def test_reference_holds_blocks_as_defined():
     code, E = ref.blocks(x)
     assert E.tolist() == [[255, 255]] and not code.any()
     assert ref.blocks(np.full((1, 32), 2.0 ** -149))[1].tolist() == [[0]]
+
+
+def test_calls_leave_what_is_not_regular():
+    """The extension module takes device tensors only, and says so by None before it does anything."""
+    import torch
+    from activation_sparse_decode_rank_amd import _calls
+    x = torch.zeros((2, 64))
+    q, s = torch.zeros((4, 32), dtype=torch.uint8), torch.zeros((4, 2), dtype=torch.uint8)
+    assert _calls.norm(x, None, None, 1e-6, -1, None, 0, 0) is None
+    assert _calls.norm([1.0], None, None, 1e-6, -1, None, 0, 0) is None
+    assert _calls.quantize(x, 0, 0) is None and _calls.quantize("x", 0, 0) is None
+    assert _calls.dequantize(q, s, -1, 0, 0, 0) is None
+    assert _calls.matmul(x, q, s, None, None, -1, 0, 0) is None
+    for call in (lambda: _calls.norm(x, None, None, "a", -1, None, 0, 0), lambda: _calls.bind(1),
+                 lambda: _calls.quantize(x, "0", 0)):
+        with pytest.raises(TypeError):
+            call()
+    with pytest.raises(ValueError):
+        _calls.bind(0, 0, 0, 0, 0)
