@@ -565,6 +565,114 @@ __global__ __launch_bounds__(512) void k_mx4_split(Mx4ProductArgs a) {
   }
 }
 
+// The same with tiles of 16 rows of w and 16 NJ rows of x, for products whose larger tiles would leave
+// compute units idle: what one of them can have in flight bounds it. Stages of 512 bytes (32 blocks)
+// of a row: wave q takes blocks 4 q to 4 q + 3 of each. Chunk c of row r lies at place c ^ (r % 16) of
+// the row's 32.
+template <int NJ>
+__global__ __launch_bounds__(512) void k_mx4_split16(Mx4ProductArgs a) {
+  constexpr int W = 8, NS = 3, TK = 16 * NJ;
+  constexpr int ROWS = 16 + TK, STAGE = ROWS * 512;
+  constexpr int UW = 8, DPS = ROWS / 2 / W;  // 1 KB loads (2 rows) of w; of one wave
+  constexpr int SROWS = (ROWS + 63) / 64 * 64, SLOADS = SROWS / 64 * 2;  // rows of scales; loads of them
+  static_assert(ROWS % 16 == 0 && SLOADS <= W, "whole loads");
+  __shared__ __attribute__((aligned(16))) int8_t sbuf[NS * STAGE];
+  __shared__ __attribute__((aligned(16))) int8_t s_scale[NS * SROWS * 32];  // [half of a stage][row][16]
+  const int nnt = (a.n + 15) / 16;
+  const int n0 = (int)(blockIdx.x % nnt) * 16, r0 = (int)(blockIdx.x / nnt) * TK;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int r16 = lane & 15, g = lane >> 4;
+  const uint8_t* wbase = a.w + (size_t)n0 * a.ldw;
+  const uint8_t* xbase = a.x + (size_t)r0 * a.ldx;
+  unsigned row[DPS];
+  int lc[DPS];  // the chunk that this lane loads
+#pragma unroll
+  for (int v = 0; v < DPS; ++v) {
+    const int u = wave + W * v, R = 2 * u + (lane >> 5);
+    row[v] = u < UW ? (unsigned)min(R, a.n - 1 - n0) * (unsigned)a.ldw
+                    : (unsigned)min(R - 16, a.rows - 1 - r0) * (unsigned)a.ldx;
+    lc[v] = (lane & 31) ^ (R & 15);
+  }
+  // waves below SLOADS load the scales of 64 rows of one half of a stage
+  const int sr = min((wave >> 1) * 64 + lane, ROWS - 1);
+  const uint8_t* sc = sr < 16 ? a.ws + (size_t)min(n0 + sr, a.n - 1) * a.ldws
+                              : a.xs + (size_t)min(r0 + sr - 16, a.rows - 1) * a.ldxs;
+  const int nst = (a.nb + 31) / 32, groups = (a.nb + 15) / 16;
+  auto issue = [&](int st, int buf) {
+    if (wave < SLOADS)
+      load_block(reinterpret_cast<const int8_t*>(sc + (size_t)min(2 * st + (wave & 1), groups - 1) * 16),
+                 s_scale + (buf * 2 + (wave & 1)) * SROWS * 16 + (wave >> 1) * 1024);
+#pragma unroll
+    for (int v = 0; v < DPS; ++v) {
+      const int u = wave + W * v;
+      // past the row's end any chunk will do
+      const unsigned k = (unsigned)min(st * 32 + lc[v], a.nb - 1) * 16;
+      load_block(reinterpret_cast<const int8_t*>((u < UW ? wbase : xbase) + (size_t)(row[v] + k)),
+                 sbuf + buf * STAGE + u * 1024);
+    }
+  };
+  float4_t acc[NJ];
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) acc[j] = float4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int st = 0; st < NS - 1; ++st) issue(min(st, nst - 1), st);
+  const int c = 4 * wave + g;
+  const int8_t* at = sbuf + r16 * 512 + (c ^ r16) * 16;
+  const int8_t* sat = s_scale + (wave >> 2) * SROWS * 16 + r16 * 16 + (c & 15);
+  int buf = 0;
+  for (int st = 0; st < nst; ++st) {
+    // the stage after this one stays in flight
+    if (wave < SLOADS) wait_loads<(NS - 2) * (DPS + 1)>();
+    else wait_loads<(NS - 2) * DPS>();
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    int4_t fw = *reinterpret_cast<const int4_t*>(at + buf * STAGE), fx[NJ];
+    int sw = *reinterpret_cast<const uint8_t*>(sat + buf * SROWS * 32), sx[NJ];
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      fx[j] = *reinterpret_cast<const int4_t*>(at + buf * STAGE + (1 + j) * 8192);
+      sx[j] = *reinterpret_cast<const uint8_t*>(sat + buf * SROWS * 32 + (1 + j) * 256);
+    }
+    // the buffer of the stage before this one is free: every wave read it before the barrier
+    issue(min(st + NS - 1, nst - 1), buf == 0 ? NS - 1 : buf - 1);
+    if (st * 32 + c >= a.nb) {  // past the row's end: codes of zero and scales of 1
+      sw = 127;
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) {
+        fx[j] = int4_t{0, 0, 0, 0};
+        sx[j] = 127;
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) acc[j] = mfma16<0, 0>(fw, fx[j], acc[j], sw, sx[j]);
+    buf = buf + 1 == NS ? 0 : buf + 1;
+    __builtin_amdgcn_s_waitcnt(I8_WAIT_LGKM0);  // this wave's reads are done before the next barrier
+  }
+  wait_loads<0>();  // no load may land in LDS after the loop
+  lds_barrier();
+  float4_t* sums = reinterpret_cast<float4_t*>(sbuf) + lane;  // [wave][16 rows of x][lane]
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) sums[(wave * NJ + j) * 64] = acc[j];
+  lds_barrier();
+  if (wave < NJ) {
+    float4_t v = sums[wave * 64];
+#pragma unroll
+    for (int k = 1; k < W; ++k) {
+      const float4_t u = sums[(k * NJ + wave) * 64];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] += u[e];
+    }
+    const int r = r0 + wave * 16 + r16;
+    if (r < a.rows) emit4(a, r, n0 + 4 * g, v);
+  }
+}
+
+template <int NJ>
+void split16_launch(const Mx4ProductArgs& a, hipStream_t s) {
+  const int64_t tiles = (((int64_t)a.rows + 16 * NJ - 1) / (16 * NJ)) * (((int64_t)a.n + 15) / 16);
+  k_mx4_split16<NJ><<<dim3((unsigned)tiles), dim3(512), 0, s>>>(a);
+}
+
 template <int CH, int TK, int NS>
 void split_launch(const Mx4ProductArgs& a, hipStream_t s) {
   const int64_t tiles = (((int64_t)a.rows + TK - 1) / TK) * (((int64_t)a.n + CH - 1) / CH);
@@ -593,6 +701,8 @@ void few_launch(const Mx4ProductArgs& a, hipStream_t s) {
 hipError_t launch_mx4_product(const Mx4ProductArgs& a, hipStream_t s) {
   switch (host::mx4_form((size_t)a.rows, (size_t)a.n, a.nb)) {
     case host::kMx4Few: few_launch<uint8_t>(a, s); break;
+    case host::kMx4Split16: split16_launch<1>(a, s); break;
+    case host::kMx4Split16x32: split16_launch<2>(a, s); break;
     case host::kMx4Split32: split_launch<32, 32, 3>(a, s); break;
     case host::kMx4Split64: split_launch<64, 64, 3>(a, s); break;
     case host::kMx4Tile64: tile_launch<64, 64, 2, 2>(a, s); break;

@@ -26,14 +26,19 @@ inline bool mx4_few(size_t M, int K) {
 // The kernel that M rows and N channels of nb blocks take: the one with the least time by a fit of
 // measured ones, in microseconds: a + (b + (f - b) l) k for tiles that fill a share l of the device's
 // room for them at once, k thousands of values long, and a + f k for each full room before them.
-enum Mx4Form { kMx4Few, kMx4Split32, kMx4Split64, kMx4Tile64, kMx4Tile64x128, kMx4Tile128, kMx4Tile256 };
+enum Mx4Form {
+  kMx4Few, kMx4Split16, kMx4Split16x32, kMx4Split32, kMx4Split64, kMx4Tile64, kMx4Tile64x128, kMx4Tile128,
+  kMx4Tile256
+};
 inline int mx4_form(size_t M, size_t N, int nb) {
   struct Fit {
     int form;
     size_t ch, tk, room;
     double a, b, f;
   };
-  static const Fit fits[] = {{kMx4Split32, 32, 32, 512, 2.6, 0.48, 0.97},
+  static const Fit fits[] = {{kMx4Split16, 16, 16, 512, 2.2, 0.36, 0.57},
+                             {kMx4Split16x32, 16, 32, 512, 2.4, 0.38, 0.76},
+                             {kMx4Split32, 32, 32, 512, 2.6, 0.48, 0.97},
                              {kMx4Split64, 64, 64, 256, 3.7, 0.69, 1.18},
                              {kMx4Tile64, 64, 64, 1024, 3.0, 1.9, 5.4},
                              {kMx4Tile64x128, 64, 128, 512, 6.0, 1.9, 3.5},
