@@ -698,19 +698,32 @@ void few_launch(const Mx4ProductArgs& a, hipStream_t s) {
 
 }  // namespace
 
-hipError_t launch_mx4_product(const Mx4ProductArgs& a, hipStream_t s) {
-  switch (host::mx4_form((size_t)a.rows, (size_t)a.n, a.nb)) {
-    case host::kMx4Few: few_launch<uint8_t>(a, s); break;
-    case host::kMx4Split16: split16_launch<1>(a, s); break;
-    case host::kMx4Split16x32: split16_launch<2>(a, s); break;
-    case host::kMx4Split32: split_launch<32, 32, 3>(a, s); break;
-    case host::kMx4Split64: split_launch<64, 64, 3>(a, s); break;
-    case host::kMx4Tile64: tile_launch<64, 64, 2, 2>(a, s); break;
-    case host::kMx4Tile64x128: tile_launch<64, 128, 2, 2>(a, s); break;
-    case host::kMx4Tile128: tile_launch<128, 128, 2, 2>(a, s); break;
-    default: tile_launch<256, 256, 4, 2>(a, s); break;
-  }
-  return hipGetLastError();
+hipError_t launch_mx4_product(Mx4ProductArgs a, hipStream_t s) {
+  auto go = [&](int form) {
+    switch (form) {
+      case host::kMx4Few: few_launch<uint8_t>(a, s); break;
+      case host::kMx4Split16: split16_launch<1>(a, s); break;
+      case host::kMx4Split16x32: split16_launch<2>(a, s); break;
+      case host::kMx4Split32: split_launch<32, 32, 3>(a, s); break;
+      case host::kMx4Split64: split_launch<64, 64, 3>(a, s); break;
+      case host::kMx4Tile64: tile_launch<64, 64, 2, 2>(a, s); break;
+      case host::kMx4Tile64x128: tile_launch<64, 128, 2, 2>(a, s); break;
+      case host::kMx4Tile128: tile_launch<128, 128, 2, 2>(a, s); break;
+      default: tile_launch<256, 256, 4, 2>(a, s); break;
+    }
+    return hipGetLastError();
+  };
+  const host::Mx4Plan p = host::mx4_plan((size_t)a.rows, (size_t)a.n, a.nb);
+  const int n = a.n;
+  a.n = (int)p.n1;
+  const hipError_t e = go(p.form);
+  if (e != hipSuccess || a.n == n) return e;
+  a.w += (size_t)a.n * a.ldw;
+  a.ws += (size_t)a.n * a.ldws;
+  if (a.bias) a.bias += a.n;
+  a.out = static_cast<char*>(a.out) + (size_t)a.n * (a.out_type == T_F32 ? 4 : 2);
+  a.n = n - a.n;
+  return go(p.rest);
 }
 
 hipError_t launch_mx4_few(const Mx4ProductArgs& a, int x_type, hipStream_t s) {

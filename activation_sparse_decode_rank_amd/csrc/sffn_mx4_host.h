@@ -30,35 +30,53 @@ enum Mx4Form {
   kMx4Few, kMx4Split16, kMx4Split16x32, kMx4Split32, kMx4Split64, kMx4Tile64, kMx4Tile64x128, kMx4Tile128,
   kMx4Tile256
 };
-inline int mx4_form(size_t M, size_t N, int nb) {
-  struct Fit {
-    int form;
-    size_t ch, tk, room;
-    double a, b, f;
-  };
-  static const Fit fits[] = {{kMx4Split16, 16, 16, 512, 2.2, 0.36, 0.57},
-                             {kMx4Split16x32, 16, 32, 512, 2.4, 0.38, 0.76},
-                             {kMx4Split32, 32, 32, 512, 2.6, 0.48, 0.97},
-                             {kMx4Split64, 64, 64, 256, 3.7, 0.69, 1.18},
-                             {kMx4Tile64, 64, 64, 1024, 3.0, 1.9, 5.4},
-                             {kMx4Tile64x128, 64, 128, 512, 6.0, 1.9, 3.5},
-                             {kMx4Tile128, 128, 128, 512, 7.0, 2.65, 5.1},
-                             {kMx4Tile256, 256, 256, 256, 9.0, 4.6, 8.6}};
-  if (mx4_few(M, nb * 32)) return kMx4Few;
-  const double k = nb / 32.0;
-  int best = kMx4Tile256;
-  double least = 1e300;
-  for (const Fit& t : fits) {
-    const size_t tiles = ((M + t.tk - 1) / t.tk) * ((N + t.ch - 1) / t.ch);
-    const size_t full = (tiles - 1) / t.room;
-    const double l = (double)(tiles - full * t.room) / (double)t.room;
-    const double us = (double)full * (t.a + t.f * k) + t.a + (t.b + (t.f - t.b) * l) * k;
-    if (us < least) {
-      least = us;
-      best = t.form;
-    }
+struct Mx4Fit {
+  int form;
+  size_t ch, tk, room;
+  double a, b, f;
+  size_t tiles(size_t M, size_t N) const { return ((M + tk - 1) / tk) * ((N + ch - 1) / ch); }
+  double us(size_t M, size_t N, double k) const {
+    const size_t t = tiles(M, N), full = (t - 1) / room;
+    const double l = (double)(t - full * room) / (double)room;
+    return (double)full * (a + f * k) + a + (b + (f - b) * l) * k;
   }
-  return best;
+};
+inline const Mx4Fit& mx4_best(size_t M, size_t N, double k) {
+  static const Mx4Fit fits[] = {{kMx4Split16, 16, 16, 512, 2.2, 0.36, 0.57},
+                                {kMx4Split16x32, 16, 32, 512, 2.4, 0.38, 0.76},
+                                {kMx4Split32, 32, 32, 512, 2.6, 0.48, 0.97},
+                                {kMx4Split64, 64, 64, 256, 3.7, 0.69, 1.18},
+                                {kMx4Tile64, 64, 64, 1024, 3.0, 1.9, 5.4},
+                                {kMx4Tile64x128, 64, 128, 512, 6.0, 1.9, 3.5},
+                                {kMx4Tile128, 128, 128, 512, 7.0, 2.65, 5.1},
+                                {kMx4Tile256, 256, 256, 256, 9.0, 4.6, 8.6}};
+  const Mx4Fit* best = nullptr;
+  for (const Mx4Fit& t : fits)
+    if (!best || t.us(M, N, k) < best->us(M, N, k)) best = &t;
+  return *best;
+}
+// Where the largest tiles leave their last room half empty, the channels of that room may do better
+// with smaller ones, in a launch of their own: the first n1 channels take `form`, the others `rest`.
+// 512 x 12288 x 49152 takes 208 us so, 227 in one launch.
+struct Mx4Plan {
+  int form, rest;
+  size_t n1;  // N: one launch
+};
+inline Mx4Plan mx4_plan(size_t M, size_t N, int nb) {
+  if (mx4_few(M, nb * 32)) return {kMx4Few, kMx4Few, N};
+  const double k = nb / 32.0;
+  const Mx4Fit& one = mx4_best(M, N, k);
+  Mx4Plan p{one.form, one.form, N};
+  const size_t down = (M + one.tk - 1) / one.tk, full = one.tiles(M, N) / one.room;
+  if (one.form != kMx4Tile256 || full == 0) return p;
+  const size_t n1 = full * one.room / down * one.ch;
+  if (n1 == 0 || n1 >= N) return p;
+  const Mx4Fit& rest = mx4_best(M, N - n1, k);
+  if (rest.form != kMx4Tile256 && one.us(M, n1, k) + rest.us(M, N - n1, k) < 0.95 * one.us(M, N, k)) {
+    p.rest = rest.form;
+    p.n1 = n1;
+  }
+  return p;
 }
 
 struct Mx4Carve {
