@@ -34,7 +34,8 @@ int sparse_ffn_rms_norm(const void* x, int32_t dtype, int64_t ldx, const void* r
   if (!float_type(dtype) || (!float_type(y_dtype) && !i8 && !mx4) || rows < 0 || cols < 1 ||
       ldx < cols)
     return SFFN_ERR_INVALID;
-  if ((w && !float_type(w_dtype)) || !(eps >= 0.0) || eps > 1.7976931348623157e308)
+  if ((w && !float_type(w_dtype)) || !(eps >= 0.0) || eps > 1.7976931348623157e308 ||
+      (eps > 0.0 && eps < 2.2250738585072014e-308))
     return SFFN_ERR_INVALID;
   if ((residual != nullptr) != (sum != nullptr) || (sum && (ldr < cols || ldsum < cols)))
     return SFFN_ERR_INVALID;
@@ -132,7 +133,7 @@ int sparse_ffn_mx4_matmul(const void* x, int32_t x_dtype, const uint8_t* x_scale
     return SFFN_ERR_UNSUPPORTED;
   // tiles round rows and channels up in 32 bits; a launch holds less than 2^32 threads
   if (M > sffn::host::kI8MaxCount || N > sffn::host::kI8MaxCount ||
-      (((int64_t)M + 63) / 64) * (((int64_t)N + 63) / 64) >= (int64_t)1 << 24)
+      !sffn::host::mx4_launches((size_t)(M > 0 ? M : 1), (size_t)N))
     return SFFN_ERR_UNSUPPORTED;
   if (M == 0) return SFFN_OK;
   if (!x || (mx4 != (x_scale != nullptr)) || !w || !w_scale || !y) return SFFN_ERR_INVALID;

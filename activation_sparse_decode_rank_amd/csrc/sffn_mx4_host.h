@@ -32,8 +32,10 @@ enum Mx4Form {
 };
 struct Mx4Fit {
   int form;
-  size_t ch, tk, room;
+  size_t ch, tk, room, threads;
   double a, b, f;
+  // a launch holds less than 2^32 threads
+  bool launches(size_t M, size_t N) const { return (tiles(M, N) + 8) * threads < (size_t)1 << 32; }
   size_t tiles(size_t M, size_t N) const { return ((M + tk - 1) / tk) * ((N + ch - 1) / ch); }
   double us(size_t M, size_t N, double k) const {
     const size_t t = tiles(M, N), full = (t - 1) / room;
@@ -41,18 +43,20 @@ struct Mx4Fit {
     return (double)full * (a + f * k) + a + (b + (f - b) * l) * k;
   }
 };
+constexpr Mx4Fit kMx4Fits[] = {{kMx4Split16, 16, 16, 512, 512, 2.2, 0.36, 0.57},
+                              {kMx4Split16x32, 16, 32, 512, 512, 2.4, 0.38, 0.76},
+                              {kMx4Split32, 32, 32, 512, 512, 2.6, 0.48, 0.97},
+                              {kMx4Split64, 64, 64, 256, 512, 3.7, 0.69, 1.18},
+                              {kMx4Tile64, 64, 64, 1024, 256, 3.0, 1.9, 5.4},
+                              {kMx4Tile64x128, 64, 128, 512, 256, 6.0, 1.9, 3.5},
+                              {kMx4Tile128, 128, 128, 512, 256, 7.0, 2.65, 5.1},
+                              {kMx4Tile256, 256, 256, 256, 512, 9.0, 4.6, 8.6}};
+// Whether M rows and N channels fit a launch: the largest tiles' do
+inline bool mx4_launches(size_t M, size_t N) { return kMx4Fits[7].launches(M, N); }
 inline const Mx4Fit& mx4_best(size_t M, size_t N, double k) {
-  static const Mx4Fit fits[] = {{kMx4Split16, 16, 16, 512, 2.2, 0.36, 0.57},
-                                {kMx4Split16x32, 16, 32, 512, 2.4, 0.38, 0.76},
-                                {kMx4Split32, 32, 32, 512, 2.6, 0.48, 0.97},
-                                {kMx4Split64, 64, 64, 256, 3.7, 0.69, 1.18},
-                                {kMx4Tile64, 64, 64, 1024, 3.0, 1.9, 5.4},
-                                {kMx4Tile64x128, 64, 128, 512, 6.0, 1.9, 3.5},
-                                {kMx4Tile128, 128, 128, 512, 7.0, 2.65, 5.1},
-                                {kMx4Tile256, 256, 256, 256, 9.0, 4.6, 8.6}};
-  const Mx4Fit* best = nullptr;
-  for (const Mx4Fit& t : fits)
-    if (!best || t.us(M, N, k) < best->us(M, N, k)) best = &t;
+  const Mx4Fit* best = &kMx4Fits[7];
+  for (const Mx4Fit& t : kMx4Fits)
+    if (t.launches(M, N) && t.us(M, N, k) < best->us(M, N, k)) best = &t;
   return *best;
 }
 // Where the largest tiles leave their last room half empty, the channels of that room may do better

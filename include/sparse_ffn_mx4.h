@@ -55,7 +55,7 @@ enum { SFFN_MX4 = 4 };
  * x: device, `rows` rows of `cols` values of dtype (SFFN_F32, SFFN_F16, SFFN_BF16), ldx elements
  * apart; residual and sum: device, rows of the same type, ldr and ldsum elements apart, both or
  * neither (NULL). w: device, cols values of w_dtype (SFFN_F32, SFFN_F16, SFFN_BF16), or NULL (1).
- * eps: finite, not negative. y: device, rows ldy elements (SFFN_I8, SFFN_MX4: bytes) apart; what
+ * eps: 0, or a positive normal number. y: device, rows ldy elements (SFFN_I8, SFFN_MX4: bytes) apart; what
  * lies between the rows is left as it was, but that 8-bit rows are filled with zeros to a multiple
  * of 16. scale: SFFN_I8: device fp32 [rows] (lds is not read); SFFN_MX4: device, rows of scales lds
  * bytes apart; otherwise NULL. sum may lie over residual or over x, row on row; a float y of x's
@@ -91,8 +91,8 @@ int sparse_ffn_dequantize_mx4(const uint8_t* q, int64_t ldq, const uint8_t* scal
  * SFFN_BF16), ldy elements apart; what lies between the rows is left as it was. work: device
  * scratch, 256-byte aligned, of at least sparse_ffn_mx4_matmul_work_bytes() (0 bytes: may be
  * NULL). M >= 0, 1 <= K <= SFFN_MX4_MAX_K. SFFN_ERR_UNSUPPORTED: K above that, M or N above
- * 2^31 - 1024, or more tiles of output than one launch holds (possible from 2^36 outputs on). The
- * size query returns (size_t)-1 for an argument it cannot size. */
+ * 2^31 - 1024, or 2^23 - 8 tiles of 256 x 256 outputs or more, which no launch holds. The size
+ * query returns (size_t)-1 for an argument it cannot size. */
 size_t sparse_ffn_mx4_matmul_work_bytes(int32_t x_dtype, int32_t M, int32_t N, int32_t K);
 int sparse_ffn_mx4_matmul(const void* x, int32_t x_dtype, const uint8_t* x_scale, int64_t ldx,
                           int64_t ldxs, int32_t M, int32_t K, const uint8_t* w, int64_t ldw,

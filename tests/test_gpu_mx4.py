@@ -17,6 +17,7 @@ import pytest
 import torch
 
 import mx4_ref as ref
+import mx4_sizes
 from gpu_util import say, to_np
 
 pytestmark = pytest.mark.gpu
@@ -383,3 +384,59 @@ def test_same_bits_every_time(P):
         first = P.mx4_matmul(xt, wq, ws)
         for _ in range(5):
             assert torch.equal(P.mx4_matmul(xt, wq, ws), first)
+
+
+@pytest.mark.parametrize("form,rest,M,K,N", mx4_sizes.FORMS)
+def test_product_forms(P, form, rest, M, K, N):
+    """Each kernel that sizes choose, and products in two launches, on float rows and on rows in blocks,
+    against 64-bit products on the device."""
+    say("product forms", form, rest, M, K, N)
+    gen = torch.Generator("cuda").manual_seed(M + K + N)
+    x = torch.randn((M, K), generator=gen, device="cuda").half()
+    w = torch.randn((N, K), generator=gen, device="cuda")
+    b = torch.randn(N, generator=gen, device="cuda")
+    x[M // 2], w[N - 2] = 0, 0
+    xq, xs = P.quantize_mx4(x)
+    wq, ws = P.quantize_mx4(w)
+    xv, wv = P.dequantize_mx4(xq, xs, cols=K).double(), P.dequantize_mx4(wq, ws, cols=K).double()
+    room = torch.full((M, N + 3), 9.0, device="cuda")
+    y = P.mx4_matmul(x, wq, ws, bias=b, y=room[:, 1:N + 1])
+    step = 4096
+    for n in range(0, N, step):
+        wt = wv[n:n + step].t().contiguous()
+        want = torch.matmul(xv, wt) + b[n:n + step].double()
+        mag = torch.matmul(xv.abs(), wt.abs()) + b[n:n + step].double().abs()
+        lim = (4 * ((K + 127) // 128) + 16) * U * mag + U * want.abs() + 2.0 ** -126
+        off = int((~((y[:, n:n + step].double() - want).abs() <= lim)).sum())
+        assert off == 0, f"{off} values off from channel {n} on"
+    assert (room[:, 0] == 9).all() and (room[:, N + 1:] == 9).all()
+    assert torch.equal(P.mx4_matmul(xq, wq, ws, x_scale=xs, bias=b, out_dtype=torch.float32), y)
+    half = P.mx4_matmul(x, wq, ws, bias=b, out_dtype=torch.bfloat16)
+    assert torch.equal(half, y.to(torch.bfloat16))
+
+
+def test_many_rows(P):
+    """Rows whose codes, values and outputs pass 2^32 bytes, and more of them than a kernel of small tiles
+    can be launched for."""
+    say("many rows")
+    M, K, N = (1 << 26) + 77, 40, 35
+    gen = torch.Generator("cuda").manual_seed(3)
+    x = torch.randn((M, K), generator=gen, device="cuda", dtype=torch.float16)
+    w = torch.randn((N, K), generator=gen, device="cuda")
+    wq, ws = P.quantize_mx4(w)
+    wv = P.dequantize_mx4(wq, ws, cols=K).double().t().contiguous()
+    q, s = P.quantize_mx4(x)
+    y = P.mx4_matmul(x, wq, ws)
+    z = P.mx4_matmul(q, wq, ws, x_scale=s, out_dtype=torch.float16)
+    v = P.dequantize_mx4(q, s, cols=K, dtype=torch.float16)
+    for r in (0, (1 << 25) - 100, (1 << 26) - 300, M - 513):
+        rows = slice(r, r + 513)
+        rq, rs = P.quantize_mx4(x[rows].clone())
+        assert torch.equal(q[rows], rq) and torch.equal(s[rows], rs)
+        rv = P.dequantize_mx4(rq, rs, cols=K)
+        assert torch.equal(v[rows], rv.half())
+        want = torch.matmul(rv.double(), wv)
+        mag = torch.matmul(rv.double().abs(), wv.abs())
+        lim = 20 * U * mag + 2.0 ** -11 * want.abs() + 2.0 ** -24
+        assert bool(((y[rows].double() - want).abs() <= lim).all())
+        assert torch.equal(z[rows], y[rows])

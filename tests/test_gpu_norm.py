@@ -44,7 +44,8 @@ def check(got, want, dtype):
     bad = np.isnan(want)
     assert np.array_equal(np.isnan(got), bad)
     over = np.abs(want) >= fi.max * (1 + fi.eps / 4)
-    d = np.abs(got - want)[~bad & ~over]
+    with np.errstate(invalid="ignore"):
+        d = np.abs(got - want)[~bad & ~over]
     lim = (fi.eps / 2 * (1 + 2.0 ** -20) * np.maximum(np.abs(want), fi.tiny))[~bad & ~over]
     off = int((~(d <= lim)).sum())
     assert off == 0, f"{off} values off, worst {np.max(d / lim):.3g} of the bound"
@@ -117,6 +118,10 @@ def test_far_values(P, d):
     for eps in (1e-6, 0.0, 1e-30):
         check_norm(P, dev(x), dev(w), None, eps)
     check_norm(P, dev(x), None, dev(np.roll(x, 1, axis=0)))
+    for bad in (np.inf, -np.inf, np.nan, 1e38):  # reaches that column, and every number held with it
+        wb = w.copy()
+        wb[d // 3] = bad
+        check_norm(P, dev(x), dev(wb), None)
     h = x[[0, 2, 5, 6, 9, 10, 11]] * np.float32(3)
     for dt in ("f16", "bf16"):
         check_norm(P, dev(h, DT[dt]), dev(w, DT[dt]), dev(h[::-1] * 100, DT[dt]))
@@ -191,6 +196,39 @@ def test_rows_between_outputs(P):
             assert (y[:, 70:80] == 0).all() and (s.view(-1)[16:] == 0x55).all()
         if kind == N.SFFN_MX4:
             assert (s[:, 3:] == 0x55).all()
+
+
+@pytest.mark.parametrize("d", [70, 3000, 20001])
+def test_outputs_over_inputs(P, d):
+    """Through the C call: a float y of x's type over x or over the residual, with the sum elsewhere or
+    over the other one."""
+    say("norm over inputs", d)
+    N = P._native
+    g = rng(11, d)
+    x0, r0 = dev(g.standard_normal((9, d)), torch.bfloat16), dev(g.standard_normal((9, d)), torch.bfloat16)
+    plain = P.rms_norm(x0)
+    y0, v0 = P.rms_norm(x0, residual=r0)
+
+    def call(x, r, v, y):
+        N.sparse_ffn_rms_norm(x.data_ptr(), N.SFFN_BF16, d, None if r is None else r.data_ptr(), d, 9, d, None, 0,
+                              1e-6, None if v is None else v.data_ptr(), d, y.data_ptr(), N.SFFN_BF16, d, None, 0, 0)
+        torch.cuda.synchronize()
+
+    x = x0.clone()
+    call(x, None, None, x)
+    assert torch.equal(x, plain)
+    x, r, v = x0.clone(), r0.clone(), torch.empty_like(x0)
+    call(x, r, v, x)
+    assert torch.equal(x, y0) and torch.equal(v, v0) and torch.equal(r, r0)
+    x, r, v = x0.clone(), r0.clone(), torch.empty_like(x0)
+    call(x, r, v, r)
+    assert torch.equal(r, y0) and torch.equal(v, v0) and torch.equal(x, x0)
+    x, r = x0.clone(), r0.clone()
+    call(x, r, r, x)
+    assert torch.equal(x, y0) and torch.equal(r, v0)
+    x, r = x0.clone(), r0.clone()
+    call(x, r, x, r)
+    assert torch.equal(r, y0) and torch.equal(x, v0)
 
 
 def test_refusals(P):

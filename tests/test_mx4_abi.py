@@ -48,7 +48,7 @@ def norm(N, **over):
 @pytest.mark.parametrize("over", [
     dict(x=None), dict(y=None), dict(scale=None), dict(dtype=3), dict(dtype=4), dict(dtype=-1),
     dict(yd=5), dict(yd=-1), dict(rows=-1), dict(cols=0), dict(ldx=99), dict(ldr=99), dict(ldsum=99),
-    dict(res=None), dict(sum=None), dict(wd=3), dict(eps=-1e-6), dict(eps=math.inf), dict(eps=math.nan),
+    dict(res=None), dict(sum=None), dict(wd=3), dict(eps=-1e-6), dict(eps=math.inf), dict(eps=math.nan), dict(eps=1e-310),
     dict(ldy=48), dict(ldy=72), dict(lds=8), dict(lds=0), dict(lds=24), dict(y=A + 8), dict(scale=A + 4),
     dict(x=A + 1), dict(res=A + 1), dict(sum=A + 1), dict(w=A + 2),
     dict(yd=3, ldy=96), dict(yd=3, ldy=104), dict(yd=3, ldy=112, scale=None),
@@ -122,6 +122,7 @@ def test_unsupported(N):
     assert matmul(N, **dict(PACKED, ldx=far)) == U and matmul(N, **dict(PACKED, ldxs=far)) == U
     assert matmul(N, M=n) == U and matmul(N, N=n, ldy=n) == U
     assert matmul(N, M=1 << 20, N=1 << 20, ldy=1 << 20) == U
+    assert matmul(N, M=(1 << 31) - 1024) == U and matmul(N, M=(1 << 31) - 4096, x=None) == N.SFFN_ERR_INVALID
     assert quantize(N, cols=n, ldx=n, ldq=1 << 31, lds=1 << 27) == U
     assert quantize(N, ldq=far) == U and quantize(N, lds=far) == U
     assert dequantize(N, ldq=far) == U and dequantize(N, lds=far) == U
@@ -228,3 +229,64 @@ def test_calls_leave_what_is_not_regular():
             call()
     with pytest.raises(ValueError):
         _calls.bind(0, 0, 0, 0, 0)
+
+
+def test_product_plan(tmp_path):
+    """Every kernel is taken somewhere, at the sizes that the GPU test runs; a product in two launches
+    covers every channel once, the first ones in whole tiles; launches stay within the device's limits
+    for what the C call lets through."""
+    import mx4_sizes
+    names = {f: i for i, f in enumerate(("Few", "Split16", "Split16x32", "Split32", "Split64", "Tile64",
+                                         "Tile64x128", "Tile128", "Tile256"))}
+    want = "".join(f"  want({m}, {k}, {n}, kMx4{a}, {'kMx4' + b if b else -1});\n"
+                   for a, b, m, k, n in mx4_sizes.FORMS)
+    src = r'''
+#include <cmath>
+#include <cstdio>
+#include <cstdlib>
+#include <random>
+#include "sffn_mx4_host.h"
+using namespace sffn::host;
+#define CHECK(c) do { if (!(c)) { std::printf("failed: %s line %d\n", #c, __LINE__); std::exit(1); } } while (0)
+static int seen[9];
+static void want(size_t M, int K, size_t N, int form, int rest) {
+  const Mx4Plan p = mx4_plan(M, N, mx4_blocks(K));
+  if (p.form != form || (rest < 0 ? p.n1 != N : p.n1 >= N || p.rest != rest)) {
+    std::printf("%zu x %d x %zu: form %d, rest %d from %zu on\n", M, K, N, p.form, p.rest, p.n1);
+    std::exit(1);
+  }
+  seen[form]++;
+}
+int main() {
+''' + want + r'''
+  for (int f = 0; f < 9; ++f) CHECK(seen[f]);
+  std::mt19937 g(11);
+  auto pick = [&](double lo, double hi) { return (size_t)std::lround(std::exp(std::log(lo) + std::log(hi / lo) * (g() / 4294967296.0))); };
+  for (int i = 0; i < 200000; ++i) {
+    const size_t M = pick(1, i % 3 ? 1e4 : 2147482624.), N = pick(1, i % 2 ? 5e4 : 2147482624.);
+    const int K = (int)pick(1, 1 << 20);
+    if (!mx4_launches(M, N)) continue;  // refused
+    const Mx4Plan p = mx4_plan(M, N, mx4_blocks(K));
+    CHECK(p.n1 >= 1 && p.n1 <= N && (p.n1 == N || p.n1 % 256 == 0));
+    auto one = [&](int form, size_t n) {
+      static const size_t ch[] = {16, 16, 16, 32, 64, 64, 64, 128, 256}, tk[] = {4, 16, 32, 32, 64, 64, 128, 128, 256};
+      static const size_t threads[] = {512, 512, 512, 512, 512, 256, 256, 256, 512};
+      CHECK(form != kMx4Few || (M <= 4 && mx4_few_lds(M, K) <= kMx4FewLds));
+      const size_t tiles = (n + ch[form] - 1) / ch[form] * ((M + tk[form] - 1) / tk[form]);
+      if (form != kMx4Few) CHECK((tiles + 8) * threads[form] < (size_t)1 << 32);
+    };
+    one(p.form, p.n1);
+    if (p.n1 < N) one(p.rest, N - p.n1);
+  }
+  std::puts("ok");
+  return 0;
+}
+'''
+    assert len(names) == 9
+    (tmp_path / "plan.cpp").write_text(src)
+    exe = str(tmp_path / "plan")
+    subprocess.run(["g++", "-std=c++17", "-O1", "-Wall", "-I",
+                    os.path.join(ROOT, "activation_sparse_decode_rank_amd", "csrc"),
+                    str(tmp_path / "plan.cpp"), "-o", exe], check=True)
+    r = subprocess.run([exe], capture_output=True, text=True, timeout=120)
+    assert r.returncode == 0 and "ok" in r.stdout, r.stdout
