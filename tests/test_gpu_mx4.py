@@ -411,8 +411,11 @@ def test_product_forms(P, form, rest, M, K, N):
         assert off == 0, f"{off} values off from channel {n} on"
     assert (room[:, 0] == 9).all() and (room[:, N + 1:] == 9).all()
     assert torch.equal(P.mx4_matmul(xq, wq, ws, x_scale=xs, bias=b, out_dtype=torch.float32), y)
-    half = P.mx4_matmul(x, wq, ws, bias=b, out_dtype=torch.bfloat16)
-    assert torch.equal(half, y.to(torch.bfloat16))
+    assert torch.equal(P.mx4_matmul(x, wq, ws, bias=b, out_dtype=torch.bfloat16), y.to(torch.bfloat16))
+    room = torch.full((M, N + 3), 9.0, device="cuda", dtype=torch.float16)
+    P.mx4_matmul(xq, wq, ws, x_scale=xs, bias=b, y=room[:, 1:N + 1])
+    assert torch.equal(room[:, 1:N + 1], y.half())
+    assert (room[:, 0] == 9).all() and (room[:, N + 1:] == 9).all()
 
 
 def test_many_rows(P):
