@@ -208,16 +208,16 @@ PyObject* quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
-// dequantize(q, scale, cols, out, device, stream): two-dimensional rows; cols -1: all
+// dequantize(q, scale, cols, out, device, stream): two-dimensional rows; cols None: all
 PyObject* dequantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
-  int64_t cols, out, dev;
-  if (n != 6 || !whole(a[2], cols) || !whole(a[3], out) || !whole(a[4], dev)) return nullptr;
+  int64_t cols = 0, out, dev;
+  if (n != 6 || (a[2] != Py_None && !whole(a[2], cols)) || !whole(a[3], out) || !whole(a[4], dev)) return nullptr;
   const at::Tensor *q = tensor(a[0], (int)dev), *s = tensor(a[1], (int)dev);
   if (!q || !s || out < 0 || out > SFFN_BF16) Py_RETURN_NONE;
   const Blocks b(*q, *s);
   if (!b.ok) Py_RETURN_NONE;
-  if (cols < 0) cols = 32 * b.B;
+  if (a[2] == Py_None) cols = 32 * b.B;
   if (cols <= 32 * (b.B - 1) || cols > 32 * b.B) Py_RETURN_NONE;
   at::Tensor y = at::empty({b.R, cols}, q->options().dtype(type_for((int)out)));
   const int st = c_dequantize(static_cast<const uint8_t*>(q->data_ptr()), b.ldq,

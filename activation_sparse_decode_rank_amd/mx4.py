@@ -201,7 +201,7 @@ def dequantize_mx4(q: torch.Tensor, scale: torch.Tensor, *, cols: Optional[int] 
     dt = _TYPES.get(dtype)
     i = q.device.index
     if dt is not None and stream is None and i is not None and i == _device():
-        got = _calls.dequantize(q, scale, -1 if cols is None else cols, dt, i, _current(i))
+        got = _calls.dequantize(q, scale, cols, dt, i, _current(i))
         if got is not None:
             return _done(got, "sparse_ffn_dequantize_mx4")
     if dt is None:

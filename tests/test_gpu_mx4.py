@@ -171,6 +171,16 @@ def test_blocks_leave_the_rest(P):
     assert torch.equal(y[:, :70], P.dequantize_mx4(rq, rs, cols=70)) and (y[:, 70:] == 3.0).all()
 
 
+@pytest.mark.parametrize("cols", [0, -1, -33, 97])
+def test_columns_that_no_blocks_hold(P, cols):
+    say("columns", cols)
+    q, s = P.quantize_mx4(dev(rng(5).standard_normal((2, 70))))
+    with pytest.raises(ValueError):
+        P.dequantize_mx4(q, s, cols=cols)
+    with pytest.raises(ValueError):
+        P.dequantize_mx4(q[:1, :16], s[:1, :1], cols=cols)
+
+
 # --------------------------------------------------------------------------------- products
 def check_product(got, x, w, bias, dtype):
     """x, w: 64-bit values of the rows in blocks."""
