@@ -212,8 +212,8 @@ def dequantize_mx4(q: torch.Tensor, scale: torch.Tensor, *, cols: Optional[int] 
         shape = q.shape[:-1]
         q2, s2 = q, scale
         if q.dim() != 2:
-            q2 = q.reshape(-1, q.shape[-1]) if q.dim() > 2 else q.unsqueeze(0)
-            s2 = _merged(scale) if q.dim() > 2 else scale.unsqueeze(0)
+            q2 = _merged(q, "q") if q.dim() > 2 else q.unsqueeze(0)
+            s2 = _merged(scale, "q's scales") if q.dim() > 2 else scale.unsqueeze(0)
         R, B, ldq, lds = _blocks(q2, s2, on.device, "q")
         if cols is None:
             cols = 32 * B
@@ -225,8 +225,8 @@ def dequantize_mx4(q: torch.Tensor, scale: torch.Tensor, *, cols: Optional[int] 
     return y
 
 
-def _merged(t: torch.Tensor) -> torch.Tensor:
-    """t [..., B] as a matrix of rows that all lie the same distance apart, without a copy."""
+def _merged(t: torch.Tensor, name: str) -> torch.Tensor:
+    """t [..., n] as a matrix of rows that all lie the same distance apart, without a copy."""
     if 0 in t.shape:
         return t.new_empty((0, t.shape[-1]))
     ld, rows = None, 1
@@ -237,7 +237,7 @@ def _merged(t: torch.Tensor) -> torch.Tensor:
         if ld is None:
             ld = t.stride(i)
         elif t.stride(i) != ld * rows:
-            raise ValueError("the rows of the scales must lie the same distance apart")
+            raise ValueError(f"the rows of {name} must lie the same distance apart")
         rows *= n
     return t.as_strided((rows, t.shape[-1]), (t.shape[-1] if ld is None else ld, t.stride(-1)))
 

@@ -181,6 +181,24 @@ def test_columns_that_no_blocks_hold(P, cols):
         P.dequantize_mx4(q[:1, :16], s[:1, :1], cols=cols)
 
 
+def test_slices_of_many_rows_on_another_stream(P):
+    """Codes whose rows lie the same distance apart are read where they are, also on a stream that does
+    not wait for this one's work; others are refused, as their scales are."""
+    say("slices on another stream")
+    x = dev(rng(6).standard_normal((4, 6, 70)))
+    q, s = P.quantize_mx4(x)
+    want = P.dequantize_mx4(q, s, cols=70)
+    other = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(20_000_000)
+    y = P.dequantize_mx4(q[:, ::2], s[:, ::2], cols=70, stream=other)
+    z = P.dequantize_mx4(q[1:, 3], s[1:, 3], cols=70, stream=other)
+    torch.cuda.synchronize()
+    assert torch.equal(y, want[:, ::2]) and torch.equal(z, want[1:, 3])
+    with pytest.raises(ValueError):
+        P.dequantize_mx4(q[:, :2], s[:, :2], cols=70)
+
+
 # --------------------------------------------------------------------------------- products
 def check_product(got, x, w, bias, dtype):
     """x, w: 64-bit values of the rows in blocks."""
