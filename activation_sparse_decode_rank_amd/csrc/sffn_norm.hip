@@ -74,8 +74,9 @@ __global__ __launch_bounds__(TPB) void k_dequantize_mx4(Mx4DequantArgs a, int L)
   }
 }
 
-// lanes a row, and the grid: rows down x, pieces of long rows down y. Sets of rows are unrolled only
-// where that leaves every compute unit several workgroups.
+// lanes a row, and the grid: rows down x, pieces of long rows down y, 2^20 workgroups (2^28 threads)
+// at most: the kernels go on from there. Sets of rows are unrolled only where that leaves every
+// compute unit several workgroups.
 struct RowGrid {
   int L;
   dim3 grid;
@@ -85,7 +86,7 @@ struct RowGrid {
     const int64_t y = std::min<int64_t>((groups + L - 1) / L, 64);
     int64_t x = ((int64_t)rows + TPB / L - 1) / (TPB / L);
     if (x * y >= 8192) x = (x + unroll - 1) / unroll;
-    grid = dim3((unsigned)std::min<int64_t>(x, 1 << 20), (unsigned)y);
+    grid = dim3((unsigned)std::min<int64_t>(x, (1 << 20) / y), (unsigned)y);
   }
 };
 

@@ -75,7 +75,8 @@ int sparse_ffn_quantize_mx4(const void* x, int32_t dtype, int64_t ldx, int32_t r
                             uint8_t* q, int64_t ldq, uint8_t* scale, int64_t lds, void* stream);
 
 /* The values that rows in 4-bit blocks stand for, the first `cols` of each: y: device, rows ldy
- * elements apart (SFFN_F32: exact; SFFN_F16, SFFN_BF16: rounded once). */
+ * elements apart (SFFN_F32: exact, but infinite from 2^128 on, which E 253 and 254 reach; SFFN_F16,
+ * SFFN_BF16: those rounded once). */
 int sparse_ffn_dequantize_mx4(const uint8_t* q, int64_t ldq, const uint8_t* scale, int64_t lds,
                               int32_t rows, int32_t cols, void* y, int32_t dtype, int64_t ldy,
                               void* stream);

@@ -181,6 +181,20 @@ def test_columns_that_no_blocks_hold(P, cols):
         P.dequantize_mx4(q[:1, :16], s[:1, :1], cols=cols)
 
 
+def test_blocks_of_many_long_rows(P):
+    """More rows than one launch has workgroups for beside the pieces of long rows."""
+    say("many long rows")
+    R, K = (1 << 14) + 33, 131100
+    x = torch.randn((R, K), device="cuda", generator=torch.Generator("cuda").manual_seed(3))
+    q, s = P.quantize_mx4(x)
+    y = P.dequantize_mx4(q, s, cols=K)
+    for r in (0, 8000, R - 40):
+        rows = slice(r, r + 40)
+        rq, rs = P.quantize_mx4(x[rows])
+        assert torch.equal(q[rows], rq) and torch.equal(s[rows], rs)
+        assert torch.equal(y[rows], P.dequantize_mx4(rq, rs, cols=K))
+
+
 def test_slices_of_many_rows_on_another_stream(P):
     """Codes whose rows lie the same distance apart are read where they are, also on a stream that does
     not wait for this one's work; others are refused, as their scales are."""
