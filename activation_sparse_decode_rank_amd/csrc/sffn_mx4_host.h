@@ -61,7 +61,7 @@ inline const Mx4Fit& mx4_best(size_t M, size_t N, double k) {
 }
 // Where the largest tiles leave their last room half empty, the channels of that room may do better
 // with smaller ones, in a launch of their own: the first n1 channels take `form`, the others `rest`.
-// 512 x 12288 x 49152 takes 208 us so, 227 in one launch.
+// 512 x 12288 x 49152 takes 208 us so (127 and 82 of them), 227 in one launch.
 struct Mx4Plan {
   int form, rest;
   size_t n1;  // N: one launch

@@ -10,7 +10,9 @@ namespace {
 // L lanes a row (a power of two), TPB / L rows a workgroup, and UNROLL such sets of rows at once, whose
 // reads are issued together: 2048 x 12288 blocks into bf16 in 11 us so, 14 with one set; fp32 values
 // are twice the bytes a lane, and gain nothing (11008 x 4096 from blocks 34.6 us, 35.7 with four).
-// Bound by memory: 11008 x 4096 fp32 into blocks 50 us, 4.1 TB/s read and written, and back 6.0.
+// Bound by memory: 11008 x 4096 fp32 into blocks 35.5 us, 5.8 TB/s read and written, and back 32.6 us,
+// 6.3 (in turn 50 and 34: what the second wrote then goes to memory while the first reads). Whole lines
+// a load, values exchanged between lanes afterwards, take as long, and more sets of rows longer.
 template <typename T>
 constexpr int UNROLL = sizeof(T) == 2 ? 4 : 1;
 

@@ -287,8 +287,9 @@ void norm_launch(const NormArgs& a, hipStream_t s) {
 // several workgroups whose reads, barriers and writes overlap: 4096 rows of 4096 bf16 with a residual
 // into 8 bits take 26.7 us with eight waves, 28.2 with four of sixteen values (and into blocks 21.7
 // and 22.4); of 8192, 53.5 with sixteen and 54.3 with eight; one row 3.2 us with eight, 4.0 with four.
-// Bound by memory: 4.4 TB/s read and written into 8 bits (a second barrier, and the remainders), 5.0
-// into blocks; 2048 rows of 12288 into blocks 33 us.
+// Bound by memory: 4.4 TB/s read and written into 8 bits where another operator's writes stand before it
+// (5.1 alone; a second barrier, and the remainders), 5.0 into blocks (5.9); 2048 rows of 12288 into blocks
+// 31 to 33 us.
 template <typename T, int OUT>
 void norm_launch(const NormArgs& a, hipStream_t s) {
   const int64_t groups = ((int64_t)a.cols + 31) / 32 * 4;
