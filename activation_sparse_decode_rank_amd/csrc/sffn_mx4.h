@@ -65,7 +65,7 @@ struct Mx4ProductArgs {
 };
 hipError_t launch_mx4_product(Mx4ProductArgs a, hipStream_t s);
 // The same where a.x holds rows of x_type values (a.cols of them, a.ldx elements apart), which the
-// kernel holds in 4-bit blocks itself (host::mx4_few).
-hipError_t launch_mx4_few(const Mx4ProductArgs& a, int x_type, hipStream_t s);
+// kernel holds in 4-bit blocks itself (host::mx4_own).
+hipError_t launch_mx4_own(const Mx4ProductArgs& a, int x_type, hipStream_t s);
 
 }  // namespace sffn

@@ -49,26 +49,34 @@ __device__ __forceinline__ void emit4(const Mx4ProductArgs& a, int64_t r, int c,
   else store4<__bf16>(a.out, o, v, a.n - c);
 }
 
-// Few rows: the weights are streamed from memory once, straight into the matrix cores' registers. W
-// waves take a tile of 16 rows of w and up to 16 rows of x, one block of 256 bytes of the length (16
-// blocks of numbers, whose scales are 16 bytes) after the other in turn. Three buffers of a block
-// take turns: one is refilled, with the block three ahead, also across the end of a tile, as soon
-// as its products are issued. The waves' sums of a tile meet in LDS and are added in the waves'
-// order. Each workgroup first holds the rows of x in 4-bit blocks in its own LDS while its first
-// weights are on their way (X = uint8_t: copies those of x that are so held): that costs less than
-// a launch before this one, and x is then read from there for every tile.
+// Few rows, or short ones: the weights are streamed from memory, straight into the matrix cores'
+// registers, and x is read from LDS. A tile is 16 rows of w and up to 16 rows of x; a wave takes one
+// block of 256 bytes of its length (16 blocks of numbers, whose scales are 16 bytes) after the other.
+// Each workgroup first holds its rows of x in 4-bit blocks in its own LDS while its first weights are
+// on their way (X = uint8_t: copies those of x that are so held): that costs less than a launch before
+// this one, and x is then read from there for every tile. Chunk c (16 bytes) of row r lies at place
+// c ^ (r % 16) of a block's 16, so that lanes that LDS serves together touch different banks.
+// S = 8, few rows: eight waves share a tile and take every eighth block of it. Three buffers of a block
+// take turns: one is refilled, with the wave's block three ahead, also across the end of a tile, as
+// soon as its products are issued. The waves' sums of a tile meet in LDS and are added in the waves'
+// order. S = 1, rows of one block: a wave has a tile to itself, and its next one is on its way
+// meanwhile; `per` workgroups share the tiles of 16 rows of x.
 constexpr int G_BLK = host::kMx4Group;  // blocks of numbers (16 bytes of codes) a block of the stream
 
-template <typename X, int W>
-__global__ __launch_bounds__(W * 64, 4) void k_mx4_few(Mx4ProductArgs a) {
+template <typename X, int S>
+__global__ __launch_bounds__(512, 4) void k_mx4_few(Mx4ProductArgs a, int per) {
   constexpr bool HELD = std::is_same<X, uint8_t>::value;
-  __shared__ __attribute__((aligned(16))) float4_t s_sum[2 * W * 64];  // [tile parity][wave][lane]
-  extern __shared__ __attribute__((aligned(16))) uint8_t s_x[];        // codes, then scales
+  constexpr int W = 8, G = W / S;  // waves; tiles at once
+  static_assert(S == 1 || S == W, "a tile is one wave's, or all waves'");
+  __shared__ __attribute__((aligned(16))) float4_t s_sum[S > 1 ? 2 * W * 64 : 1];  // [tile parity][wave][lane]
+  extern __shared__ __attribute__((aligned(16))) uint8_t s_x[];                    // codes, then scales
   const int nnt = (a.n + 15) / 16;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r16 = lane & 15, g = lane >> 4;
-  const int nbk = (a.nb + G_BLK - 1) / G_BLK;
+  const int nbk = S > 1 ? (a.nb + G_BLK - 1) / G_BLK : 1;
+  const int r0 = (int)(blockIdx.x / per) * 16, rows = min(16, a.rows - r0);
+  const int first = wave % S, step = per * G;  // first block of a tile; tiles from one to the next
   // Lane g of four (16 lanes apart) loads word g of a row's 16 scales; the instruction wants bytes
   // g, 4 + g, 8 + g and 12 + g in it: the bytes change places like a 4 x 4 matrix's, between lanes
   // 32 apart, then 16 apart.
@@ -81,7 +89,8 @@ __global__ __launch_bounds__(W * 64, 4) void k_mx4_few(Mx4ProductArgs a) {
   };
   // the stream: next block (tile, block of it) to load
   const int lc = g + 4 * (r16 >> 3);  // chunk of 128 bytes that this lane loads
-  int ft = blockIdx.x, fb = wave;
+  int t = (int)(blockIdx.x % per) * G + wave / S;
+  int ft = t, fb = first;
   const uint8_t *wbase = nullptr, *sbase = nullptr;  // first rows of that tile, one for all lanes
   unsigned wrow[2], srow;  // this lane's two rows of codes, and its row of scales, from there
   auto aim = [&]() {
@@ -103,73 +112,130 @@ __global__ __launch_bounds__(W * 64, 4) void k_mx4_few(Mx4ProductArgs a) {
       // past w's row x is zero, so any chunk will do
       const unsigned c = (unsigned)min(fb * G_BLK + s * 4 + lc, a.nb - 1) * 16;
 #pragma unroll
-      for (int q = 0; q < 2; ++q)
-        B.w[s + q] = __builtin_nontemporal_load(reinterpret_cast<const int4_t*>(wbase + (size_t)(wrow[q] + c)));
+      for (int q = 0; q < 2; ++q) {
+        const int4_t* from = reinterpret_cast<const int4_t*>(wbase + (size_t)(wrow[q] + c));
+        B.w[s + q] = S > 1 ? __builtin_nontemporal_load(from) : *from;
+      }
     }
     B.s = *reinterpret_cast<const unsigned*>(sbase + (size_t)(srow + (unsigned)fb * 16));
-    fb += W;
+    fb += S;
     if (fb >= nbk) {
-      fb = wave;
-      ft += gridDim.x;
+      fb = first;
+      ft += step;
       if (ft < nnt) aim();
     }
   };
-  int t = blockIdx.x;
-  const bool works = wave < nbk;  // a wave past the blocks of a row only meets the others
-  Block ring[3];
+  const bool works = first < nbk;  // a wave past the blocks of a row only meets the others
+  constexpr int RING = S > 1 ? 3 : 1;
+  Block ring[RING];
   if (works && t < nnt) {
     aim();
 #pragma unroll
-    for (int i = 0; i < 3; ++i) fetch(ring[i]);
+    for (int i = 0; i < RING; ++i) fetch(ring[i]);
   }
-  // x's rows: codes [rows][nbk * 256], scales [rows][nbk] of four words, word g the bytes of blocks
+  // x's rows: codes [rows][nbk * 256], scales [nbk][rows] of four words, word g the bytes of blocks
   // g, 4 + g, 8 + g and 12 + g
-  uint8_t* sc = s_x + (size_t)a.rows * nbk * 256;
-  auto scale_at = [&](int r, int b) { return (size_t)(r * nbk + (b >> 4)) * 16 + (b & 3) * 4 + (b >> 2 & 3); };
-  for (int r = 0; r < a.rows; ++r) {
-    uint8_t* q = s_x + (size_t)r * nbk * 256;
-    if constexpr (HELD) {
-      for (int b = tid; b < nbk * G_BLK; b += W * 64) {
-        int4_t v = {0, 0, 0, 0};
-        if (b < a.nb) v = *reinterpret_cast<const int4_t*>(a.x + (size_t)r * a.ldx + 16 * b);
-        *reinterpret_cast<int4_t*>(q + 16 * b) = v;
-        sc[scale_at(r, b)] = b < a.nb ? a.xs[(size_t)r * a.ldxs + b] : 127;
+  uint8_t* sc = s_x + (size_t)rows * nbk * 256;
+  constexpr int U = 2;  // pieces on their way at once
+  if constexpr (HELD) {
+    // a thread takes a block of numbers after the other
+    const int n = nbk * G_BLK, dr = W * 64 / n, di = W * 64 % n;
+    int r = tid / n, i = tid % n;
+    while (r < rows) {
+      int4_t v[U];
+      uint8_t e[U];
+      int rr[U], ii[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        rr[u] = r;
+        ii[u] = i;
+        v[u] = int4_t{0, 0, 0, 0};
+        e[u] = 127;
+        if (r < rows && i < a.nb) {
+          v[u] = *reinterpret_cast<const int4_t*>(a.x + (size_t)(r0 + r) * a.ldx + 16 * i);
+          e[u] = a.xs[(size_t)(r0 + r) * a.ldxs + i];
+        }
+        r += dr;
+        i += di;
+        if (i >= n) {
+          i -= n;
+          ++r;
+        }
       }
-    } else {
-      const X* x = reinterpret_cast<const X*>(a.x) + (size_t)r * a.ldx;
-      for (int i = tid; i < nbk * G_BLK * 4; i += W * 64) {
-        unsigned E;
-        reinterpret_cast<unsigned*>(q)[i] = mx4_encode(load8(x, i, a.cols), E);
-        if ((i & 3) == 0) sc[scale_at(r, i >> 2)] = (uint8_t)E;
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (rr[u] < rows) {
+          const int b = ii[u] >> 4, c = ii[u] & 15;
+          *reinterpret_cast<int4_t*>(s_x + (size_t)(rr[u] * nbk + b) * 256 + ((c ^ rr[u]) & 15) * 16) = v[u];
+          sc[(size_t)(b * rows + rr[u]) * 16 + (c & 3) * 4 + (c >> 2)] = e[u];
+        }
+    }
+  } else {
+    // a wave takes a block of the length of a row after the other, a lane eight values of it
+    const X* x = reinterpret_cast<const X*>(a.x) + (size_t)r0 * a.ldx;
+    const int dr = W / nbk, db = W % nbk, c = lane >> 2;
+    int r = wave / nbk, b = wave % nbk;
+    while (r < rows) {
+      vec8<X> f[U];
+      int rr[U], bb[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        rr[u] = r;
+        bb[u] = b;
+        if (r < rows) f[u] = raw8(x + (size_t)r * a.ldx + b * 512, lane, a.cols - b * 512);
+        r += dr;
+        b += db;
+        if (b >= nbk) {
+          b -= nbk;
+          ++r;
+        }
       }
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (rr[u] < rows) {
+          unsigned E;
+          const unsigned q = mx4_encode(floats8(f[u]), E);
+          *reinterpret_cast<unsigned*>(s_x + (size_t)(rr[u] * nbk + bb[u]) * 256 + ((c ^ rr[u]) & 15) * 16 + (lane & 3) * 4) = q;
+          if ((lane & 3) == 0) sc[(size_t)(bb[u] * rows + rr[u]) * 16 + (c & 3) * 4 + (c >> 2)] = (uint8_t)E;
+        }
     }
   }
   lds_barrier();
-  const int xr = min(r16, a.rows - 1);
-  const uint8_t* fx = s_x + (size_t)xr * nbk * 256 + g * 16;
-  const uint8_t* fs = sc + (size_t)xr * nbk * 16 + g * 4;
+  const int xr = min(r16, rows - 1);  // lanes past the rows read some of x, and write nothing
+  const uint8_t *fx = s_x + (size_t)xr * nbk * 256, *fs = sc + (size_t)xr * 16 + g * 4;
+  int place[4];
+#pragma unroll
+  for (int s = 0; s < 4; ++s) place[s] = ((4 * s + g) ^ r16) * 16;
   float4_t acc = {0.f, 0.f, 0.f, 0.f};
-  int b = wave, par = 0;
+  int b = first, par = 0;
   auto end_tile = [&]() {
-    float4_t* sum = s_sum + par * W * 64 + lane;
-    sum[wave * 64] = acc;
-    // The sums of the tile two before this one were read before their reader's arrival here, and
-    // the other parity's are free to be written after it.
-    lds_barrier();
-    if (wave == 0) {
-      float4_t v = sum[0];
+    if constexpr (S > 1) {
+      float4_t* sum = s_sum + par * W * 64 + lane;
+      sum[wave * 64] = acc;
+      // The sums of the tile two before this one were read before their reader's arrival here, and
+      // the other parity's are free to be written after it.
+      lds_barrier();
+      if (wave == 0) {
+        float4_t v = sum[0];
 #pragma unroll
-      for (int q = 1; q < W; ++q) {
-        const float4_t u = sum[q * 64];
+        for (int q = 1; q < W; ++q) {
+          const float4_t u = sum[q * 64];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] += u[e];
+          for (int e = 0; e < 4; ++e) v[e] += u[e];
+        }
+        if (r16 < rows) emit4(a, r0 + r16, t * 16 + 4 * g, v);
       }
-      if (r16 < a.rows) emit4(a, r16, t * 16 + 4 * g, v);
+      par ^= 1;
+    } else {
+      // All lanes' products and their operands come before the lanes that write take a way of their own:
+      // the compiler would move them there, where the others' operands are missing. (The waits are the
+      // matrix instruction's, which reading its result takes.)
+      asm volatile("s_nop 15\n\ts_nop 15" : "+v"(acc));
+      if (r16 < rows) emit4(a, r0 + r16, t * 16 + 4 * g, acc);
     }
     acc = float4_t{0.f, 0.f, 0.f, 0.f};
-    par ^= 1;
-    b = wave;
-    t += gridDim.x;
+    b = first;
+    t += step;
   };
   if (!works) {
     while (t < nnt) end_tile();
@@ -177,7 +243,7 @@ __global__ __launch_bounds__(W * 64, 4) void k_mx4_few(Mx4ProductArgs a) {
   }
   auto block = [&](Block& B) {
     unsigned sw = to_scales(B.s);
-    const int sx = *reinterpret_cast<const int*>(fs + b * 16);
+    const int sx = *reinterpret_cast<const int*>(fs + (size_t)b * rows * 16);
     if ((b + 1) * G_BLK > a.nb) {  // past the row's end the scales may be anything: 1 stands there
       const int left = (a.nb - b * G_BLK - g + 3) >> 2;  // steps of this lane
       const unsigned keep = left >= 4 ? ~0u : (1u << (8 * max(left, 0))) - 1;
@@ -187,22 +253,32 @@ __global__ __launch_bounds__(W * 64, 4) void k_mx4_few(Mx4ProductArgs a) {
       constexpr int s = decltype(s0)::value;
       int4_t w[2];
       to_steps(B.w[s], B.w[s + 1], w[0], w[1]);
-      const uint8_t* x = fx + b * 256 + s * 64;
-      acc = mfma16<s, s>(w[0], *reinterpret_cast<const int4_t*>(x), acc, (int)sw, sx);
-      acc = mfma16<s + 1, s + 1>(w[1], *reinterpret_cast<const int4_t*>(x + 64), acc, (int)sw, sx);
+      const uint8_t* x = fx + (size_t)b * 256;
+      acc = mfma16<s, s>(w[0], *reinterpret_cast<const int4_t*>(x + place[s]), acc, (int)sw, sx);
+      acc = mfma16<s + 1, s + 1>(w[1], *reinterpret_cast<const int4_t*>(x + place[s + 1]), acc, (int)sw, sx);
     };
     pair(std::integral_constant<int, 0>{});
     pair(std::integral_constant<int, 2>{});
-    fetch(B);
-    b += W;
+    if constexpr (S > 1) fetch(B);
+    b += S;
     if (b >= nbk) end_tile();
   };
-  while (t < nnt) {
-    block(ring[0]);
-    if (t >= nnt) break;
-    block(ring[1]);
-    if (t >= nnt) break;
-    block(ring[2]);
+  if constexpr (S > 1) {
+    while (t < nnt) {
+      block(ring[0]);
+      if (t >= nnt) break;
+      block(ring[1]);
+      if (t >= nnt) break;
+      block(ring[2]);
+    }
+  } else {
+    // one copy of the code: what a short product takes is latency, and its instructions' first
+    while (t < nnt) {
+      Block next;
+      fetch(next);
+      block(ring[0]);
+      ring[0] = next;
+    }
   }
 }
 
@@ -737,10 +813,18 @@ void tile_launch(const Mx4ProductArgs& a, hipStream_t s) {
 // sixteen 81), 1 x 4096 x 11008 in 6.6 (four waves 7.1, sixteen 9.7).
 template <typename X>
 void few_launch(const Mx4ProductArgs& a, hipStream_t s) {
-  constexpr int W = 8;
   const size_t lds = host::mx4_few_lds((size_t)a.rows, a.cols);
-  const int at_once = resident<k_mx4_few<X, W>>(W * 64, lds);
-  k_mx4_few<X, W><<<dim3((unsigned)std::min((a.n + 15) / 16, at_once)), dim3(W * 64), lds, s>>>(a);
+  const int at_once = resident<k_mx4_few<X, 8>>(512, lds);
+  const int per = std::min((a.n + 15) / 16, at_once);
+  k_mx4_few<X, 8><<<dim3((unsigned)per), dim3(512), lds, s>>>(a, per);
+}
+// As many workgroups as there are eight tiles for, or a device holds
+template <typename X>
+void short_launch(const Mx4ProductArgs& a, hipStream_t s) {
+  const size_t lds = host::mx4_few_lds((size_t)std::min(a.rows, 16), a.cols);
+  const int at_once = resident<k_mx4_few<X, 1>>(512, lds), down = (a.rows + 15) / 16;
+  const int per = std::max(1, std::min((a.n + 127) / 128, at_once / down));
+  k_mx4_few<X, 1><<<dim3((unsigned)(per * down)), dim3(512), lds, s>>>(a, per);
 }
 
 }  // namespace
@@ -749,6 +833,7 @@ hipError_t launch_mx4_product(Mx4ProductArgs a, hipStream_t s) {
   auto go = [&](int form) {
     switch (form) {
       case host::kMx4Few: few_launch<uint8_t>(a, s); break;
+      case host::kMx4Short: short_launch<uint8_t>(a, s); break;
       case host::kMx4Split16: split16_launch<1>(a, s); break;
       case host::kMx4Split16x32: split16_launch<2>(a, s); break;
       case host::kMx4Split32: split_launch<32, 32, 3>(a, s); break;
@@ -773,11 +858,19 @@ hipError_t launch_mx4_product(Mx4ProductArgs a, hipStream_t s) {
   return go(p.rest);
 }
 
-hipError_t launch_mx4_few(const Mx4ProductArgs& a, int x_type, hipStream_t s) {
-  if (x_type == T_F32) few_launch<float>(a, s);
-  else if (x_type == T_F16) few_launch<_Float16>(a, s);
-  else few_launch<__bf16>(a, s);
+namespace {
+template <typename X>
+hipError_t own_launch(const Mx4ProductArgs& a, hipStream_t s) {
+  if (host::mx4_few((size_t)a.rows, a.cols)) few_launch<X>(a, s);
+  else short_launch<X>(a, s);
   return hipGetLastError();
+}
+}  // namespace
+
+hipError_t launch_mx4_own(const Mx4ProductArgs& a, int x_type, hipStream_t s) {
+  if (x_type == T_F32) return own_launch<float>(a, s);
+  if (x_type == T_F16) return own_launch<_Float16>(a, s);
+  return own_launch<__bf16>(a, s);
 }
 
 }  // namespace sffn

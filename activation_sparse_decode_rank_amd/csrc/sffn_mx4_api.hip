@@ -116,7 +116,7 @@ size_t sparse_ffn_mx4_matmul_work_bytes(int32_t x_dtype, int32_t M, int32_t N, i
   if ((!float_type(x_dtype) && x_dtype != SFFN_MX4) || M < 0 || N < 1 || K < 1 ||
       K > SFFN_MX4_MAX_K)
     return (size_t)-1;
-  if (M == 0 || x_dtype == SFFN_MX4 || sffn::host::mx4_few((size_t)M, K)) return 0;
+  if (M == 0 || x_dtype == SFFN_MX4 || sffn::host::mx4_own((size_t)M, (size_t)N, K)) return 0;
   return sffn::host::mx4_carve((size_t)M, K).bytes;
 }
 
@@ -154,11 +154,11 @@ int sparse_ffn_mx4_matmul(const void* x, int32_t x_dtype, const uint8_t* x_scale
   a.out_type = y_dtype;
   hipStream_t s = static_cast<hipStream_t>(stream);
   a.cols = K;
-  // few rows: held in 4-bit blocks by the product's own workgroups
-  if (!mx4 && sffn::host::mx4_few((size_t)M, K)) {
+  // few or short rows: held in 4-bit blocks by the product's own workgroups
+  if (!mx4 && sffn::host::mx4_own((size_t)M, (size_t)N, K)) {
     a.x = static_cast<const uint8_t*>(x);
     a.ldx = ldx;
-    return status(sffn::launch_mx4_few(a, x_dtype, s));
+    return status(sffn::launch_mx4_own(a, x_dtype, s));
   }
   if (mx4) {
     a.x = static_cast<const uint8_t*>(x);

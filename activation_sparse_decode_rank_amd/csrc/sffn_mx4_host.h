@@ -23,11 +23,27 @@ inline bool mx4_few(size_t M, int K) {
   return M <= (size_t)kMx4FewRows && mx4_few_lds(M, K) <= kMx4FewLds;
 }
 
+// Whether workgroups hold 16 rows of x each in their LDS, and a wave has a tile to itself: for more
+// rows, of at most 512 values (one group), and few tiles. Float rows: 42 x 345 x 3475 (M x K x N) takes
+// 3.8 us so, 6.2 with a launch for x's rows in front, and that launch costs the host 3 to 4 us; 445 x
+// 469 x 552 4.0 and 6.6; 1224 x 375 x 949 (4620 tiles) 7.1 and 8.2, 1007 x 502 x 1332 (5292) 8.2 and
+// 7.7; of two groups, 77 x 950 x 610, 5.9 and 5.3. Rows that are held already take it at the same
+// sizes, so that both give the same bits: 33 x 162 x 3983 3.1 us, 3.9 split over a tile's waves, 13 x
+// 451 x 180 2.9 and 2.8.
+constexpr size_t kMx4ShortTiles = 4096;
+inline bool mx4_short(size_t M, size_t N, int nb) {
+  return nb <= kMx4Group && ((M + 15) / 16) * ((N + 15) / 16) <= kMx4ShortTiles;
+}
+// Whether a product of float rows holds them in 4-bit blocks itself, without scratch
+inline bool mx4_own(size_t M, size_t N, int K) {
+  return mx4_few(M, K) || mx4_short(M, N, mx4_blocks(K));
+}
+
 // The kernel that M rows and N channels of nb blocks take: the one with the least time by a fit of
 // measured ones, in microseconds: a + (b + (f - b) l) k for tiles that fill a share l of the device's
 // room for them at once, k thousands of values long, and a + f k for each full room before them.
 enum Mx4Form {
-  kMx4Few, kMx4Split16, kMx4Split16x32, kMx4Split32, kMx4Split64, kMx4Tile64, kMx4Tile64x128, kMx4Tile128,
+  kMx4Few, kMx4Short, kMx4Split16, kMx4Split16x32, kMx4Split32, kMx4Split64, kMx4Tile64, kMx4Tile64x128, kMx4Tile128,
   kMx4Tile256
 };
 struct Mx4Fit {
@@ -68,6 +84,7 @@ struct Mx4Plan {
 };
 inline Mx4Plan mx4_plan(size_t M, size_t N, int nb) {
   if (mx4_few(M, nb * 32)) return {kMx4Few, kMx4Few, N};
+  if (mx4_short(M, N, nb)) return {kMx4Short, kMx4Short, N};
   const double k = nb / 32.0;
   const Mx4Fit& one = mx4_best(M, N, k);
   Mx4Plan p{one.form, one.form, N};

@@ -10,20 +10,34 @@ struct F8 {
   float v[8];
 };
 
-// Eight values of a row from element 8 i on, and past `cols` zeros
+// Eight values of a row from element 8 i on, as they lie in memory, and past `cols` zeros
 template <typename T>
-__device__ __forceinline__ F8 load8(const T* x, int64_t i, int64_t cols) {
+using vec8 = T __attribute__((ext_vector_type(8)));
+
+template <typename T>
+__device__ __forceinline__ vec8<T> raw8(const T* x, int64_t i, int64_t cols) {
   typedef T vec __attribute__((ext_vector_type(8), aligned(sizeof(T))));
-  F8 f;
+  vec8<T> v;
   if (8 * i + 8 <= cols) {
-    const vec t = *reinterpret_cast<const vec*>(x + 8 * i);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) f.v[e] = (float)t[e];
+    v = *reinterpret_cast<const vec*>(x + 8 * i);
   } else {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) f.v[e] = 8 * i + e < cols ? (float)x[8 * i + e] : 0.f;
+    for (int e = 0; e < 8; ++e) v[e] = 8 * i + e < cols ? x[8 * i + e] : (T)0.f;
   }
+  return v;
+}
+
+template <typename T>
+__device__ __forceinline__ F8 floats8(const vec8<T>& v) {
+  F8 f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) f.v[e] = (float)v[e];
   return f;
+}
+
+template <typename T>
+__device__ __forceinline__ F8 load8(const T* x, int64_t i, int64_t cols) {
+  return floats8(raw8(x, i, cols));
 }
 
 // Eight values of a row to element 8 i on, and none past `cols`

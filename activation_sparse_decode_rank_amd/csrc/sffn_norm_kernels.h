@@ -68,23 +68,6 @@ __device__ __forceinline__ unsigned wg_largest(unsigned v, unsigned* at) {
   }
 }
 
-// Eight neighbouring values of a row as they lie in memory
-template <typename T>
-using vec8 = T __attribute__((ext_vector_type(8)));
-
-template <typename T>
-__device__ __forceinline__ vec8<T> raw8(const T* x, int64_t i, int64_t cols) {
-  typedef T vec __attribute__((ext_vector_type(8), aligned(sizeof(T))));
-  vec8<T> v;
-  if (8 * i + 8 <= cols) {
-    v = *reinterpret_cast<const vec*>(x + 8 * i);
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = 8 * i + e < cols ? x[8 * i + e] : (T)0.f;
-  }
-  return v;
-}
-
 template <typename T>
 __device__ __forceinline__ void put_raw8(T* y, int64_t i, int64_t cols, const vec8<T>& v) {
   typedef T vec __attribute__((ext_vector_type(8), aligned(sizeof(T))));

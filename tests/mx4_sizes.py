@@ -4,6 +4,7 @@ asks the plan (csrc/sffn_mx4_host.h) that they do, the GPU test runs them."""
 # (kernel of the first channels, kernel of the rest or None, M, K, N)
 FORMS = [
     ("Few", None, 3, 1000, 333),
+    ("Short", None, 39, 347, 3471),
     ("Split16", None, 21, 3561, 333),
     ("Split16x32", None, 61, 3561, 3001),
     ("Split32", None, 11, 1001, 8599),

@@ -269,13 +269,55 @@ def test_product_sizes(P, M, K, N):
         assert torch.equal(y, y2)
 
 
-@pytest.mark.parametrize("M", [1, 6, 40, 90, 300])
-def test_product_any_codes(P, M):
+@pytest.mark.parametrize("M,K,N", [(5, 1, 1), (5, 31, 4099), (9, 512, 8), (15, 33, 130), (16, 511, 9),
+                                   (17, 512, 257), (18, 2, 16), (24, 78, 510), (40, 129, 3001),
+                                   (250, 384, 1000), (4000, 65, 33), (1030, 511, 1011), (65000, 7, 2)])
+def test_product_short_rows(P, M, K, N):
+    """Rows of one group, a wave a tile: tiles with a few rows or channels, many of either."""
+    test_product_sizes(P, M, K, N)
+
+
+@pytest.mark.parametrize("M", [5, 21, 300])
+def test_product_short_rows_between(P, M):
+    """Short rows of x, w, their scales and y further apart than they are long, at odd places, NaN and any
+    codes between them; two graphs that share nothing, replayed in turn."""
+    say("product short strides", M)
+    x, w, b = problem(M, 300, 75, 9)
+    wv, wc, wE = held(w)
+    pq, pE = ref.pack(wc, wE)
+    wq = torch.full((75, 400), 0x77, dtype=torch.uint8, device="cuda")
+    ws = torch.full((75, 48), 255, dtype=torch.uint8, device="cuda")
+    wq[:, :160], ws[:, :10] = dev(pq, torch.uint8), dev(pE, torch.uint8)
+    graphs = []
+    for dt in (torch.float32, torch.float16):
+        big = torch.full((M, 777), float("nan"), device="cuda", dtype=dt)
+        big[:, 3:303] = dev(x, dt)
+        xt = big[:, 3:303]
+        room = torch.full((M, 81), 5.0, device="cuda", dtype=torch.bfloat16)
+        y = P.mx4_matmul(xt, wq[:, :160], ws[:, :10], bias=dev(b), y=room[:, 2:77])
+        check_product(y, held(f64(xt))[0], wv, b.astype(np.float32), torch.bfloat16)
+        assert (room[:, :2] == 5).all() and (room[:, 77:] == 5).all()
+        bt, g = dev(b), torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(g):
+            out = P.mx4_matmul(xt, wq[:, :160], ws[:, :10], bias=bt)
+        graphs.append((g, xt, bt, out))
+    for i in range(4):
+        for g, xt, bt, out in graphs:
+            xt.mul_(0.7).add_(0.1)
+            g.replay()
+            want = P.mx4_matmul(xt, wq[:, :160], ws[:, :10], bias=bt)
+            torch.cuda.synchronize()
+            assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("M,B", [(1, 37), (6, 37), (40, 37), (90, 37), (300, 37), (6, 13), (40, 16)])
+def test_product_any_codes(P, M, B):
     """Rows from elsewhere: every code and scales far apart, also so that sums pass 2^127 in one
     block and 2^-126 in the other direction."""
-    say("product codes", M)
+    say("product codes", M, B)
     g = rng(6, M)
-    N, B = 150, 37
+    N = 150
     xq, wq = g.integers(0, 256, (M, 16 * B)), g.integers(0, 256, (N, 16 * B))
     for lo, hi in ((120, 134), (60, 190), (0, 60), (0, 3)):
         xs, ws = g.integers(lo, hi + 1, (M, B)), g.integers(254 - hi, 254 - lo + 1, (N, B))
@@ -285,12 +327,12 @@ def test_product_any_codes(P, M):
         check_product(y, ref.values(xq, xs), ref.values(wq, ws), None, torch.float32)
 
 
-@pytest.mark.parametrize("M", [1, 5, 40, 100, 300])
-def test_product_nan_blocks(P, M):
+@pytest.mark.parametrize("M,K", [(1, 700), (5, 700), (40, 700), (100, 700), (300, 700), (5, 480), (40, 500)])
+def test_product_nan_blocks(P, M, K):
     """A NaN scale or number reaches its row (of x) or channel (of w) and nothing else."""
-    say("product NaN", M)
-    x, w, _ = problem(M, 700, 90, 1)
-    x[M // 2, 699], w[17, 3], w[64, 650] = np.nan, np.inf, np.nan
+    say("product NaN", M, K)
+    x, w, _ = problem(M, K, 90, 1)
+    x[M // 2, K - 1], w[17, 3], w[64, K - 50] = np.nan, np.inf, np.nan
     xt = dev(x)
     (xv, _, _), (wv, wc, wE) = held(f64(xt)), held(w)
     assert np.isnan(xv[M // 2]).any() and np.isnan(wv[17]).any()
@@ -355,8 +397,10 @@ def test_product_refusals(P):
     for call in bad:
         with pytest.raises(ValueError):
             call()
+    x = dev(rng(7).standard_normal((80, 600)))
+    wq, ws = P.quantize_mx4(dev(rng(8).standard_normal((20, 600))))
     with pytest.raises(P.SparseFFNError):
-        P.mx4_matmul(x.repeat(20, 1), wq, ws, work=torch.empty(16, dtype=torch.uint8, device="cuda"))
+        P.mx4_matmul(x, wq, ws, work=torch.empty(16, dtype=torch.uint8, device="cuda"))
 
 
 def test_product_long_rows(P):

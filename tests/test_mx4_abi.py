@@ -97,14 +97,15 @@ def matmul(lib, **over):
 
 
 PACKED = dict(xd=4, xs=A, ldx=64, ldxs=16, K=128)
+LONG = dict(M=50, K=600, ldx=600, ldw=304, ldws=32)  # x's rows are held in scratch
 
 
 @pytest.mark.parametrize("over", [
     dict(x=None), dict(w=None), dict(ws=None), dict(y=None), dict(xd=3), dict(xd=5), dict(yd=3),
     dict(yd=4), dict(M=-1), dict(K=0), dict(N=0), dict(ldx=99), dict(ldy=6), dict(ldw=48),
     dict(ldw=72), dict(ldws=3), dict(ldws=20), dict(w=A + 8), dict(ws=A + 8), dict(x=A + 1),
-    dict(y=A + 2), dict(xs=A), dict(bias=A + 2), dict(M=50, work=None), dict(M=50, work=A + 16),
-    dict(M=50, work_bytes=16),
+    dict(y=A + 2), dict(xs=A), dict(bias=A + 2), dict(LONG, work=None), dict(LONG, work=A + 16),
+    dict(LONG, work_bytes=16),
     dict(PACKED, xs=None), dict(PACKED, K=100), dict(PACKED, ldx=48), dict(PACKED, ldx=72),
     dict(PACKED, ldxs=2), dict(PACKED, ldxs=20), dict(PACKED, x=A + 8), dict(PACKED, xs=A + 8),
 ])
@@ -134,6 +135,9 @@ def test_unsupported(N):
                 (0, 1 << 31, 4, 64)):
         assert wb(*bad) == none, bad
     assert wb(0, 0, 4, 64) == 0
+    # the product's own workgroups hold few rows, and short ones of few tiles; others lie in scratch
+    assert wb(0, 4, 64, 20000) == wb(1, 50, 64, 512) == wb(2, 4096, 256, 1) == wb(4, 50, 64, 600) == 0
+    assert wb(0, 50, 64, 513) > 0 and wb(0, 4097, 256, 64) > 0 and wb(0, 5, 64, 600) > 0
     with pytest.raises(N.SparseFFNError):
         N.sparse_ffn_quantize_mx4(A, 0, 1 << 33, 4, (1 << 32) + 32, A, 1 << 31, A, 1 << 27, None)
 
@@ -236,7 +240,7 @@ def test_product_plan(tmp_path):
     covers every channel once, the first ones in whole tiles; launches stay within the device's limits
     for what the C call lets through."""
     import mx4_sizes
-    names = {f: i for i, f in enumerate(("Few", "Split16", "Split16x32", "Split32", "Split64", "Tile64",
+    names = {f: i for i, f in enumerate(("Few", "Short", "Split16", "Split16x32", "Split32", "Split64", "Tile64",
                                          "Tile64x128", "Tile128", "Tile256"))}
     want = "".join(f"  want({m}, {k}, {n}, kMx4{a}, {'kMx4' + b if b else -1});\n"
                    for a, b, m, k, n in mx4_sizes.FORMS)
@@ -248,7 +252,7 @@ def test_product_plan(tmp_path):
 #include "sffn_mx4_host.h"
 using namespace sffn::host;
 #define CHECK(c) do { if (!(c)) { std::printf("failed: %s line %d\n", #c, __LINE__); std::exit(1); } } while (0)
-static int seen[9];
+static int seen[10];
 static void want(size_t M, int K, size_t N, int form, int rest) {
   const Mx4Plan p = mx4_plan(M, N, mx4_blocks(K));
   if (p.form != form || (rest < 0 ? p.n1 != N : p.n1 >= N || p.rest != rest)) {
@@ -259,7 +263,7 @@ static void want(size_t M, int K, size_t N, int form, int rest) {
 }
 int main() {
 ''' + want + r'''
-  for (int f = 0; f < 9; ++f) CHECK(seen[f]);
+  for (int f = 0; f < 10; ++f) CHECK(seen[f]);
   std::mt19937 g(11);
   auto pick = [&](double lo, double hi) { return (size_t)std::lround(std::exp(std::log(lo) + std::log(hi / lo) * (g() / 4294967296.0))); };
   for (int i = 0; i < 200000; ++i) {
@@ -269,9 +273,10 @@ int main() {
     const Mx4Plan p = mx4_plan(M, N, mx4_blocks(K));
     CHECK(p.n1 >= 1 && p.n1 <= N && (p.n1 == N || p.n1 % 256 == 0));
     auto one = [&](int form, size_t n) {
-      static const size_t ch[] = {16, 16, 16, 32, 64, 64, 64, 128, 256}, tk[] = {4, 16, 32, 32, 64, 64, 128, 128, 256};
-      static const size_t threads[] = {512, 512, 512, 512, 512, 256, 256, 256, 512};
+      static const size_t ch[] = {16, 16, 16, 16, 32, 64, 64, 64, 128, 256}, tk[] = {4, 16, 16, 32, 32, 64, 64, 128, 128, 256};
+      static const size_t threads[] = {512, 512, 512, 512, 512, 512, 256, 256, 256, 512};
       CHECK(form != kMx4Few || (M <= 4 && mx4_few_lds(M, K) <= kMx4FewLds));
+      CHECK((form == kMx4Short) == (M > 4 && mx4_blocks(K) <= 16 && (M + 15) / 16 * ((N + 15) / 16) <= kMx4ShortTiles));
       const size_t tiles = (n + ch[form] - 1) / ch[form] * ((M + tk[form] - 1) / tk[form]);
       if (form != kMx4Few) CHECK((tiles + 8) * threads[form] < (size_t)1 << 32);
     };
@@ -282,7 +287,7 @@ int main() {
   return 0;
 }
 '''
-    assert len(names) == 9
+    assert len(names) == 10
     (tmp_path / "plan.cpp").write_text(src)
     exe = str(tmp_path / "plan")
     subprocess.run(["g++", "-std=c++17", "-O1", "-Wall", "-I",
