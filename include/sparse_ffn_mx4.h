@@ -83,7 +83,9 @@ int sparse_ffn_dequantize_mx4(const uint8_t* q, int64_t ldq, const uint8_t* scal
 
 /* y = x W^T (+ bias) with x and W in 4-bit blocks:
  *   y[t][n] = sum over blocks b of 2^(Ex[t][b] + Ew[n][b] - 254) sum_j x_j w_j  (+ bias[n])
- * The products are exact; the sums are held in 32 bits; rounded once to y_dtype.
+ * The products are exact; the sums are held in 32 bits, in an order that M, N and K decide; rounded
+ * once to y_dtype. Rows that the call holds in 4-bit blocks and the same rows held before give the
+ * same bits.
  * x: device, M rows of K values, ldx elements apart. SFFN_F32, SFFN_F16, SFFN_BF16: each row is
  * held in 4-bit blocks as above first (x_scale NULL, ldxs is not read). SFFN_MX4: codes, ldx bytes
  * apart, with their scales x_scale, ldxs bytes apart; K is then 32 for each block. w: device, codes
