@@ -83,13 +83,13 @@ __device__ __forceinline__ void emit4(const Mx4ProductArgs& a, int64_t r, int c,
 // block of 256 bytes of its length (16 blocks of numbers, whose scales are 16 bytes) after the other.
 // Each workgroup first holds its rows of x in 4-bit blocks in its own LDS while its first weights are
 // on their way (X = uint8_t: copies those of x that are so held): that costs less than a launch before
-// this one, and x is then read from there for every tile. Chunk c (16 bytes) of row r lies at place
-// c ^ (r % 16) of a block's 16, so that lanes that LDS serves together touch different banks.
+// this one, and x is then read from there for every tile.
 // S = 8, few rows: eight waves share a tile and take every eighth block of it. Three buffers of a block
 // take turns: one is refilled, with the wave's block three ahead, also across the end of a tile, as
 // soon as its products are issued. The waves' sums of a tile meet in LDS and are added in the waves'
 // order. S = 1, rows of one block: a wave has a tile to itself, and its next one is on its way
-// meanwhile; `per` workgroups share the tiles of 16 rows of x.
+// meanwhile; `per` workgroups share the tiles of 16 rows of x. Chunk c (16 bytes) of row r lies at place
+// c ^ (r % 16) of the block's 16, so that lanes that LDS serves together touch different banks.
 constexpr int G_BLK = host::kMx4Group;  // blocks of numbers (16 bytes of codes) a block of the stream
 
 template <typename X, int S>
@@ -104,7 +104,7 @@ __global__ __launch_bounds__(512, 4) void k_mx4_few(Mx4ProductArgs a, int per) {
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r16 = lane & 15, g = lane >> 4;
   const int nbk = S > 1 ? (a.nb + G_BLK - 1) / G_BLK : 1;
-  const int r0 = (int)(blockIdx.x / per) * 16, rows = min(16, a.rows - r0);
+  const int down = S > 1 ? 0 : (int)(blockIdx.x / per), r0 = down * 16, rows = min(16, a.rows - r0);
   const int first = wave % S, step = per * G;  // first block of a tile; tiles from one to the next
   // Lane g of four (16 lanes apart) loads word g of a row's 16 scales; the instruction wants bytes
   // g, 4 + g, 8 + g and 12 + g in it: the bytes change places like a 4 x 4 matrix's, between lanes
@@ -118,7 +118,7 @@ __global__ __launch_bounds__(512, 4) void k_mx4_few(Mx4ProductArgs a, int per) {
   };
   // the stream: next block (tile, block of it) to load
   const int lc = g + 4 * (r16 >> 3);  // chunk of 128 bytes that this lane loads
-  int t = (int)(blockIdx.x % per) * G + wave / S;
+  int t = ((int)blockIdx.x - down * per) * G + wave / S;
   int ft = t, fb = first;
   const uint8_t *wbase = nullptr, *sbase = nullptr;  // first rows of that tile, one for all lanes
   unsigned wrow[2], srow;  // this lane's two rows of codes, and its row of scales, from there
@@ -162,44 +162,30 @@ __global__ __launch_bounds__(512, 4) void k_mx4_few(Mx4ProductArgs a, int per) {
 #pragma unroll
     for (int i = 0; i < RING; ++i) fetch(ring[i]);
   }
-  // x's rows: codes [rows][nbk * 256], scales [nbk][rows] of four words, word g the bytes of blocks
+  // x's rows: codes [rows][nbk * 256], scales [rows][nbk] of four words, word g the bytes of blocks
   // g, 4 + g, 8 + g and 12 + g
   uint8_t* sc = s_x + (size_t)rows * nbk * 256;
-  constexpr int U = 2;  // pieces on their way at once
+  auto place = [](int r, int c) { return S > 1 ? c : (c ^ r) & 15; };
   if constexpr (HELD) {
-    // a thread takes a block of numbers after the other
-    const int n = nbk * G_BLK, dr = W * 64 / n, di = W * 64 % n;
-    int r = tid / n, i = tid % n;
-    while (r < rows) {
-      int4_t v[U];
-      uint8_t e[U];
-      int rr[U], ii[U];
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        rr[u] = r;
-        ii[u] = i;
-        v[u] = int4_t{0, 0, 0, 0};
-        e[u] = 127;
-        if (r < rows && i < a.nb) {
-          v[u] = *reinterpret_cast<const int4_t*>(a.x + (size_t)(r0 + r) * a.ldx + 16 * i);
-          e[u] = a.xs[(size_t)(r0 + r) * a.ldxs + i];
-        }
-        r += dr;
-        i += di;
-        if (i >= n) {
-          i -= n;
-          ++r;
-        }
+    auto copy = [&](int r, int i) {
+      int4_t v = {0, 0, 0, 0};
+      uint8_t e = 127;
+      if (i < a.nb) {
+        v = *reinterpret_cast<const int4_t*>(a.x + (size_t)(r0 + r) * a.ldx + 16 * i);
+        e = a.xs[(size_t)(r0 + r) * a.ldxs + i];
       }
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (rr[u] < rows) {
-          const int b = ii[u] >> 4, c = ii[u] & 15;
-          *reinterpret_cast<int4_t*>(s_x + (size_t)(rr[u] * nbk + b) * 256 + ((c ^ rr[u]) & 15) * 16) = v[u];
-          sc[(size_t)(b * rows + rr[u]) * 16 + (c & 3) * 4 + (c >> 2)] = e[u];
-        }
+      const int b = i >> 4, c = i & 15;
+      *reinterpret_cast<int4_t*>(s_x + (size_t)(r * nbk + b) * 256 + place(r, c) * 16) = v;
+      sc[(size_t)(r * nbk + b) * 16 + (c & 3) * 4 + (c >> 2)] = e;
+    };
+    if constexpr (S == 1) {
+      if (tid < rows * G_BLK) copy(tid / G_BLK, tid % G_BLK);
+    } else {
+      for (int r = 0; r < rows; ++r)
+        for (int i = tid; i < nbk * G_BLK; i += W * 64) copy(r, i);
     }
   } else {
+    constexpr int U = 4;  // of them on their way at once: 4 x 4096 x 4096 4.6 us, 5.0 with two
     // a wave takes a block of the length of a row after the other, a lane eight values of it
     const X* x = reinterpret_cast<const X*>(a.x) + (size_t)r0 * a.ldx;
     const int dr = W / nbk, db = W % nbk, c = lane >> 2;
@@ -224,17 +210,17 @@ __global__ __launch_bounds__(512, 4) void k_mx4_few(Mx4ProductArgs a, int per) {
         if (rr[u] < rows) {
           unsigned E;
           const unsigned q = mx4_encode(floats8(f[u]), E);
-          *reinterpret_cast<unsigned*>(s_x + (size_t)(rr[u] * nbk + bb[u]) * 256 + ((c ^ rr[u]) & 15) * 16 + (lane & 3) * 4) = q;
-          if ((lane & 3) == 0) sc[(size_t)(bb[u] * rows + rr[u]) * 16 + (c & 3) * 4 + (c >> 2)] = (uint8_t)E;
+          *reinterpret_cast<unsigned*>(s_x + (size_t)(rr[u] * nbk + bb[u]) * 256 + place(rr[u], c) * 16 + (lane & 3) * 4) = q;
+          if ((lane & 3) == 0) sc[(size_t)(rr[u] * nbk + bb[u]) * 16 + (c & 3) * 4 + (c >> 2)] = (uint8_t)E;
         }
     }
   }
   lds_barrier();
   const int xr = min(r16, rows - 1);  // lanes past the rows read some of x, and write nothing
-  const uint8_t *fx = s_x + (size_t)xr * nbk * 256, *fs = sc + (size_t)xr * 16 + g * 4;
-  int place[4];
+  const uint8_t *fx = s_x + (size_t)xr * nbk * 256, *fs = sc + (size_t)xr * nbk * 16 + g * 4;
+  int at[4];
 #pragma unroll
-  for (int s = 0; s < 4; ++s) place[s] = ((4 * s + g) ^ r16) * 16;
+  for (int s = 0; s < 4; ++s) at[s] = place(r16, 4 * s + g) * 16;
   float4_t acc = {0.f, 0.f, 0.f, 0.f};
   int b = first, par = 0;
   auto end_tile = [&]() {
@@ -275,7 +261,7 @@ __global__ __launch_bounds__(512, 4) void k_mx4_few(Mx4ProductArgs a, int per) {
   }
   auto block = [&](Block& B) {
     unsigned sw = to_scales(B.s);
-    const int sx = *reinterpret_cast<const int*>(fs + (size_t)b * rows * 16);
+    const int sx = *reinterpret_cast<const int*>(fs + b * 16);
     if ((b + 1) * G_BLK > a.nb) {  // past the row's end the scales may be anything: 1 stands there
       const int left = (a.nb - b * G_BLK - g + 3) >> 2;  // steps of this lane
       const unsigned keep = left >= 4 ? ~0u : (1u << (8 * max(left, 0))) - 1;
@@ -285,9 +271,9 @@ __global__ __launch_bounds__(512, 4) void k_mx4_few(Mx4ProductArgs a, int per) {
       constexpr int s = decltype(s0)::value;
       int4_t w[2];
       to_steps(B.w[s], B.w[s + 1], w[0], w[1]);
-      const uint8_t* x = fx + (size_t)b * 256;
-      acc = mfma16<s, s>(w[0], *reinterpret_cast<const int4_t*>(x + place[s]), acc, (int)sw, sx);
-      acc = mfma16<s + 1, s + 1>(w[1], *reinterpret_cast<const int4_t*>(x + place[s + 1]), acc, (int)sw, sx);
+      const uint8_t* x = fx + b * 256;
+      acc = mfma16<s, s>(w[0], *reinterpret_cast<const int4_t*>(x + at[s]), acc, (int)sw, sx);
+      acc = mfma16<s + 1, s + 1>(w[1], *reinterpret_cast<const int4_t*>(x + at[s + 1]), acc, (int)sw, sx);
     };
     pair(std::integral_constant<int, 0>{});
     pair(std::integral_constant<int, 2>{});
