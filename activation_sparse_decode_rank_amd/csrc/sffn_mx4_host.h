@@ -14,7 +14,7 @@ inline int mx4_padded(int K) { return (int)up_to((size_t)mx4_blocks(K), kMx4Grou
 
 // Whether the workgroups of a product hold the M rows of x in their LDS, codes and scales: every one
 // of them does it for all rows, so few of them, and within the LDS that leaves two workgroups a
-// compute unit. Float rows are held in 4-bit blocks on the way. 4 rows x 4096 x 4096 take 4.9 us so,
+// compute unit. Float rows are held in 4-bit blocks on the way. 4 rows x 4096 x 4096 take 4.6 us so,
 // 5.8 split over a tile's waves; 8 rows 6.5 and 5.8 (1 x 12288 x 49152: 49 and 63 us).
 constexpr int kMx4FewRows = 4;
 constexpr size_t kMx4FewLds = 48 * 1024;
