@@ -277,10 +277,10 @@ def test_product_short_rows(P, M, K, N):
     test_product_sizes(P, M, K, N)
 
 
-@pytest.mark.parametrize("M", [5, 21, 300])
+@pytest.mark.parametrize("M", [3, 5, 21, 300])
 def test_product_short_rows_between(P, M):
     """Short rows of x, w, their scales and y further apart than they are long, at odd places, NaN and any
-    codes between them; two graphs that share nothing, replayed in turn."""
+    codes between them; two graphs replayed in turn, on inputs and a bias that change."""
     say("product short strides", M)
     x, w, b = problem(M, 300, 75, 9)
     wv, wc, wE = held(w)
@@ -305,10 +305,12 @@ def test_product_short_rows_between(P, M):
     for i in range(4):
         for g, xt, bt, out in graphs:
             xt.mul_(0.7).add_(0.1)
+            bt.mul_(0.9).add_(0.5)
             g.replay()
             want = P.mx4_matmul(xt, wq[:, :160], ws[:, :10], bias=bt)
             torch.cuda.synchronize()
             assert torch.equal(out, want)
+            check_product(out, held(f64(xt))[0], wv, to_np(bt), xt.dtype)
 
 
 @pytest.mark.parametrize("M,B", [(1, 37), (6, 37), (40, 37), (90, 37), (300, 37), (6, 13), (40, 16)])
