@@ -1,5 +1,6 @@
-"""Build libsparse_ffn.so (HIP, gfx950 only) in-tree with hipcc, and _calls.so, the extension module
-that takes regular calls of mx4.py past ctypes, with the host compiler.
+"""Build libsparse_ffn.so (HIP, gfx950 only) in-tree with hipcc, and _calls, the extension module that
+takes regular calls of mx4.py past ctypes, with the host compiler. That module is for one Python and one
+torch, and the package works without it: where it cannot be built, the build says so and goes on.
 
 Usage: python activation_sparse_decode_rank_amd/build.py   (or __graft_entry__.build()).
 Run it as a script: importing the package loads the library this builds.
@@ -8,8 +9,10 @@ directory, where the Python binding loads it.
 """
 from __future__ import annotations
 
+import glob
 import importlib.util
 import os
+import re
 import shutil
 import subprocess
 import sys
@@ -21,7 +24,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libsparse_ffn.so")
-CALLS = os.path.join(HERE, "_calls.so")
+CALLS = os.path.join(HERE, "_calls" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
 SOURCES = ["sffn_api.hip", "sffn_dispatch.hip", "sffn_stage1.hip", "sffn_decode_b1.hip", "sffn_batch.hip",
            "sffn_mid_bt_h4.hip", "sffn_mid_bt_h8.hip", "sffn_mid_bt_f4.hip", "sffn_mid_bt_f8.hip",
            "sffn_tiles.hip", "sffn_offline.hip", "sffn_measure.hip", "sffn_prefill.hip",
@@ -52,12 +55,18 @@ def _compile(src: str) -> str:
 
 
 def _compile_calls() -> None:
-    """_calls.so against torch's headers; its libraries are the ones that torch has loaded."""
-    torch = importlib.util.find_spec("torch").submodule_search_locations[0]
+    """_calls against torch's headers; its libraries are the ones that torch has loaded. It carries the
+    version of the torch that it is built for."""
+    found = importlib.util.find_spec("torch")
+    if found is None:
+        raise RuntimeError("torch is not installed")
+    torch = found.submodule_search_locations[0]
+    with open(os.path.join(torch, "version.py"), encoding="utf-8") as f:
+        version = re.search(r"^__version__ = ['\"]([\w.+-]+)['\"]", f.read(), re.M)[1]
     inc = [os.path.join(ROOT, "include"), os.path.join(torch, "include"),
            os.path.join(torch, "include", "torch", "csrc", "api", "include"), sysconfig.get_paths()["include"]]
     tmp = CALLS + ".tmp"
-    cmd = [CXX, "-O2", "-std=c++17", "-fPIC", "-shared", *(f"-I{i}" for i in inc),
+    cmd = [CXX, "-O2", "-std=c++17", "-fPIC", "-shared", f'-DSFFN_TORCH="{version}"', *(f"-I{i}" for i in inc),
            os.path.join(CSRC, "sffn_calls.cpp"), "-L" + os.path.join(torch, "lib"), "-ltorch_python",
            "-ltorch_cpu", "-lc10", "-o", tmp]
     r = subprocess.run(cmd, capture_output=True, text=True)
@@ -66,12 +75,26 @@ def _compile_calls() -> None:
     os.replace(tmp, CALLS)
 
 
+def build_calls() -> bool:
+    """Whether _calls was built. One of an earlier build does not stay: it may not fit the library."""
+    try:
+        _compile_calls()
+        built = CALLS
+    except (OSError, RuntimeError, TypeError) as e:  # TypeError: a torch without a version
+        print(f"_calls is left out, so calls of mx4.py go through ctypes: {e}", file=sys.stderr)
+        built = None
+    for old in glob.glob(os.path.join(os.path.dirname(CALLS), "_calls*.so")):
+        if old != built:
+            os.remove(old)
+    return built is not None
+
+
 def build(verbose: bool = True) -> str:
     os.makedirs(BUILD, exist_ok=True)
     with ThreadPoolExecutor(max_workers=min(len(SOURCES), os.cpu_count() or 4)) as ex:
-        calls = ex.submit(_compile_calls)
+        calls = ex.submit(build_calls)
         objs = list(ex.map(_compile, SOURCES))
-        calls.result()
+        calls = calls.result()
     tmp = LIB + ".tmp"
     cmd = [HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
@@ -79,7 +102,7 @@ def build(verbose: bool = True) -> str:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
     if verbose:
-        print(f"built {LIB} and {CALLS}")
+        print(f"built {LIB}" + (f" and {CALLS}" if calls else ""))
     return LIB
 
 

@@ -307,4 +307,9 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_calls", nullptr, -1, methods, nul
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__calls() { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit__calls() {
+  PyObject* m = PyModule_Create(&module);
+  // mx4.py takes the module with that torch only: at::Tensor is another torch's to lay out
+  if (m && PyModule_AddStringConstant(m, "built_for", SFFN_TORCH) != 0) Py_CLEAR(m);
+  return m;
+}

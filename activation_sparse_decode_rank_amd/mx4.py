@@ -18,22 +18,46 @@ and keep the inputs until it is done, or record_stream them.
 Calls on the current device and stream whose tensors lie as the library reads them go through the
 extension module _calls (csrc/sffn_calls.cpp), which does in one step what the functions here do: a
 third to a half of the host's time. Where it returns None the function goes on here, with copies,
-another stream or device, given outputs, or the error.
+another stream or device, given outputs, or the error; so does every call where there is no such module
+that was built for this Python and torch.
 """
 from __future__ import annotations
 
+import warnings
 from typing import Optional, Tuple, Union
 
 import torch
 
-from . import _calls
 from . import _native as N
 from .experts import _F32, _I8, _TYPES, _U8, _on, _out, _out_dtype, _type, _vector, _work
 from .experts import _current, _rows as _some_rows
 
-_calls.bind(*(N.address(f) for f in ("sparse_ffn_rms_norm", "sparse_ffn_quantize_mx4",
-                                     "sparse_ffn_dequantize_mx4", "sparse_ffn_mx4_matmul_work_bytes",
-                                     "sparse_ffn_mx4_matmul")))
+
+class _Without:
+    """In the place of _calls: leaves every call to the functions here."""
+
+    norm = quantize = dequantize = matmul = staticmethod(lambda *a: None)
+
+
+def _short_way():
+    try:
+        from . import _calls
+    except ImportError as e:
+        why = str(e)
+    else:
+        built_for = getattr(_calls, "built_for", None)
+        if built_for == str(torch.__version__):
+            _calls.bind(*(N.address(f) for f in ("sparse_ffn_rms_norm", "sparse_ffn_quantize_mx4",
+                                                 "sparse_ffn_dequantize_mx4", "sparse_ffn_mx4_matmul_work_bytes",
+                                                 "sparse_ffn_mx4_matmul")))
+            return _calls
+        why = f"built for torch {built_for}, not {torch.__version__}"
+    warnings.warn(f"the extension module _calls is not used ({why}): calls of mx4.py take longer on the host. "
+                  "activation_sparse_decode_rank_amd/build.py builds it", RuntimeWarning)
+    return _Without
+
+
+_calls = _short_way()
 _device = torch._C._cuda_getDevice
 _OUT = {None: -1, **_TYPES, "i8": N.SFFN_I8, "mx4": N.SFFN_MX4}
 
