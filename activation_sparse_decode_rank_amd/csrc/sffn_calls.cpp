@@ -38,10 +38,10 @@ at::ScalarType type_for(int code) {
 }
 
 // The tensor behind a Python object, on device `dev`; null if it is not that
-const at::Tensor* tensor(PyObject* o, int dev) {
+const at::Tensor* tensor(PyObject* o, int64_t dev) {
   if (!THPVariable_Check(o)) return nullptr;
   const at::Tensor& t = THPVariable_Unpack(o);
-  return t.layout() == at::kStrided && t.is_cuda() && t.get_device() == dev ? &t : nullptr;
+  return t.layout() == at::kStrided && t.is_cuda() && (int64_t)t.get_device() == dev ? &t : nullptr;
 }
 
 // Rows [R, K] of a tensor whose last dimension is K, ld elements apart, without a copy
@@ -90,7 +90,19 @@ bool whole(PyObject* o, int64_t& v) {
   v = PyLong_AsLongLong(o);
   return !(v == -1 && PyErr_Occurred());
 }
-void* stream_of(PyObject* o) { return PyLong_AsVoidPtr(o); }
+bool address(PyObject* o, void*& p) {
+  p = nullptr;
+  if (!PyLong_Check(o)) {
+    PyErr_SetString(PyExc_TypeError, "a stream is a whole number");
+    return false;
+  }
+  p = PyLong_AsVoidPtr(o);
+  return p || !PyErr_Occurred();
+}
+bool count(Py_ssize_t n, Py_ssize_t want) {
+  if (n != want) PyErr_Format(PyExc_TypeError, "%zd arguments are needed, not %zd", want, n);
+  return n == want;
+}
 
 PyObject* answer(int status, std::initializer_list<at::Tensor> out) {
   if (status != SFFN_OK) return PyLong_FromLong(status);
@@ -98,7 +110,14 @@ PyObject* answer(int status, std::initializer_list<at::Tensor> out) {
   PyObject* t = PyTuple_New((Py_ssize_t)out.size());
   if (!t) return nullptr;
   Py_ssize_t i = 0;
-  for (const at::Tensor& o : out) PyTuple_SET_ITEM(t, i++, THPVariable_Wrap(o));
+  for (const at::Tensor& o : out) {
+    PyObject* p = THPVariable_Wrap(o);
+    if (!p) {
+      Py_DECREF(t);
+      return nullptr;
+    }
+    PyTuple_SET_ITEM(t, i++, p);
+  }
   return t;
 }
 
@@ -126,10 +145,11 @@ struct NewBlocks {
 PyObject* norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   int64_t out, dev;
-  if (n != 8 || !whole(a[4], out) || !whole(a[6], dev)) return nullptr;
+  void* stream;
+  if (!count(n, 8) || !whole(a[4], out) || !whole(a[6], dev) || !address(a[7], stream)) return nullptr;
   const double eps = PyFloat_AsDouble(a[3]);
   if (eps == -1.0 && PyErr_Occurred()) return nullptr;
-  const at::Tensor* x = tensor(a[0], (int)dev);
+  const at::Tensor* x = tensor(a[0], dev);
   if (!x) Py_RETURN_NONE;
   const int xt = type_of(*x);
   const Rows r(*x);
@@ -138,21 +158,21 @@ PyObject* norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const void* w = nullptr;
   int wt = 0;
   if (a[1] != Py_None) {
-    const at::Tensor* t = tensor(a[1], (int)dev);
+    const at::Tensor* t = tensor(a[1], dev);
     if (!t || t->dim() != 1 || t->size(0) != r.K || !t->is_contiguous() || (wt = type_of(*t)) < 0) Py_RETURN_NONE;
     w = t->data_ptr();
   }
   const at::Tensor *res = nullptr, *into = nullptr;
   int64_t ldr = r.K, ldsum = r.K;
   if (a[2] != Py_None) {
-    res = tensor(a[2], (int)dev);
+    res = tensor(a[2], dev);
     if (!res || res->scalar_type() != x->scalar_type() || res->sizes() != x->sizes()) Py_RETURN_NONE;
     const Rows q(*res);
     if (!q.ok) Py_RETURN_NONE;
     ldr = q.ld;
   }
   if (a[5] != Py_None) {
-    into = tensor(a[5], (int)dev);
+    into = tensor(a[5], dev);
     if (!res || !into || into->scalar_type() != x->scalar_type() || into->sizes() != x->sizes()) Py_RETURN_NONE;
     const Rows q(*into);
     if (!q.ok) Py_RETURN_NONE;
@@ -163,7 +183,6 @@ PyObject* norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
   else if (res) sum = at::empty(x->sizes(), x->options());
   void* sp = res ? sum.data_ptr() : nullptr;
   const void* rp = res ? res->data_ptr() : nullptr;
-  void* stream = stream_of(a[7]);
   const int R = (int)r.R, K = (int)r.K;
   if (out == SFFN_MX4) {
     NewBlocks b(*x, r.K);
@@ -195,15 +214,16 @@ PyObject* norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyObject* quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   int64_t dev;
-  if (n != 3 || !whole(a[1], dev)) return nullptr;
-  const at::Tensor* x = tensor(a[0], (int)dev);
+  void* stream;
+  if (!count(n, 3) || !whole(a[1], dev) || !address(a[2], stream)) return nullptr;
+  const at::Tensor* x = tensor(a[0], dev);
   if (!x) Py_RETURN_NONE;
   const int xt = type_of(*x);
   const Rows r(*x);
   if (xt < 0 || !r.ok) Py_RETURN_NONE;
   NewBlocks b(*x, r.K);
   const int st = c_quantize(x->data_ptr(), xt, r.ld, (int)r.R, (int)r.K, static_cast<uint8_t*>(b.q.data_ptr()), b.ldq,
-                            static_cast<uint8_t*>(b.room.data_ptr()), b.lds, stream_of(a[2]));
+                            static_cast<uint8_t*>(b.room.data_ptr()), b.lds, stream);
   return answer(st, {b.q, b.s});
   END_HANDLE_TH_ERRORS
 }
@@ -212,8 +232,14 @@ PyObject* quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyObject* dequantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   int64_t cols = 0, out, dev;
-  if (n != 6 || (a[2] != Py_None && !whole(a[2], cols)) || !whole(a[3], out) || !whole(a[4], dev)) return nullptr;
-  const at::Tensor *q = tensor(a[0], (int)dev), *s = tensor(a[1], (int)dev);
+  void* stream;
+  if (!count(n, 6) || !whole(a[3], out) || !whole(a[4], dev) || !address(a[5], stream)) return nullptr;
+  if (a[2] != Py_None && !whole(a[2], cols)) {
+    if (!PyErr_ExceptionMatches(PyExc_OverflowError)) return nullptr;
+    PyErr_Clear();  // more than any blocks hold
+    Py_RETURN_NONE;
+  }
+  const at::Tensor *q = tensor(a[0], dev), *s = tensor(a[1], dev);
   if (!q || !s || out < 0 || out > SFFN_BF16) Py_RETURN_NONE;
   const Blocks b(*q, *s);
   if (!b.ok) Py_RETURN_NONE;
@@ -222,7 +248,7 @@ PyObject* dequantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
   at::Tensor y = at::empty({b.R, cols}, q->options().dtype(type_for((int)out)));
   const int st = c_dequantize(static_cast<const uint8_t*>(q->data_ptr()), b.ldq,
                               static_cast<const uint8_t*>(s->data_ptr()), b.lds, (int)b.R, (int)cols, y.data_ptr(),
-                              (int)out, cols, stream_of(a[5]));
+                              (int)out, cols, stream);
   return answer(st, {y});
   END_HANDLE_TH_ERRORS
 }
@@ -231,8 +257,9 @@ PyObject* dequantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyObject* matmul(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   int64_t out, dev;
-  if (n != 8 || !whole(a[5], out) || !whole(a[6], dev)) return nullptr;
-  const at::Tensor *x = tensor(a[0], (int)dev), *w = tensor(a[1], (int)dev), *ws = tensor(a[2], (int)dev);
+  void* stream;
+  if (!count(n, 8) || !whole(a[5], out) || !whole(a[6], dev) || !address(a[7], stream)) return nullptr;
+  const at::Tensor *x = tensor(a[0], dev), *w = tensor(a[1], dev), *ws = tensor(a[2], dev);
   if (!x || !w || !ws || x->dim() != 2) Py_RETURN_NONE;
   const Blocks bw(*w, *ws);
   if (!bw.ok) Py_RETURN_NONE;
@@ -240,7 +267,7 @@ PyObject* matmul(PyObject*, PyObject* const* a, Py_ssize_t n) {
   int64_t M, K, ldx, ldxs = 0;
   const uint8_t* xs = nullptr;
   if (a[3] != Py_None) {
-    const at::Tensor* s = tensor(a[3], (int)dev);
+    const at::Tensor* s = tensor(a[3], dev);
     if (!s) Py_RETURN_NONE;
     const Blocks b(*x, *s);
     if (!b.ok || b.B != bw.B) Py_RETURN_NONE;
@@ -263,7 +290,7 @@ PyObject* matmul(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (out > SFFN_BF16) Py_RETURN_NONE;
   const float* bias = nullptr;
   if (a[4] != Py_None) {
-    const at::Tensor* t = tensor(a[4], (int)dev);
+    const at::Tensor* t = tensor(a[4], dev);
     if (!t || t->scalar_type() != at::kFloat || t->dim() != 1 || t->size(0) != bw.R || !t->is_contiguous())
       Py_RETURN_NONE;
     bias = static_cast<const float*>(t->data_ptr());
@@ -276,17 +303,14 @@ PyObject* matmul(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int st = c_matmul(x->data_ptr(), xt, xs, ldx, ldxs, (int)M, (int)K,
                           static_cast<const uint8_t*>(w->data_ptr()), bw.ldq,
                           static_cast<const uint8_t*>(ws->data_ptr()), bw.lds, bias, (int)bw.R, y.data_ptr(), (int)out,
-                          bw.R, need ? work.data_ptr() : nullptr, need, stream_of(a[7]));
+                          bw.R, need ? work.data_ptr() : nullptr, need, stream);
   return answer(st, {y});
   END_HANDLE_TH_ERRORS
 }
 
 // bind(norm, quantize, dequantize, matmul_work_bytes, matmul): the C entry points' addresses
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  if (n != 5) {
-    PyErr_SetString(PyExc_TypeError, "bind takes five addresses");
-    return nullptr;
-  }
+  if (!count(n, 5)) return nullptr;
   void* p[5];
   for (int i = 0; i < 5; ++i) {
     p[i] = PyLong_AsVoidPtr(a[i]);

@@ -92,3 +92,23 @@ def test_the_build_goes_on_without_the_module(tmp_path, monkeypatch, capsys, mis
     assert m.build_calls() is False
     assert "_calls" in capsys.readouterr().err
     assert sorted(os.listdir(tmp_path)) == ["libsparse_ffn.so"]
+
+
+def test_the_module_refuses_what_is_no_argument():
+    """A wrong number of arguments is a TypeError, as from any function, and a stream that is no address is
+    refused before anything is looked at."""
+    import torch
+    from activation_sparse_decode_rank_amd import _calls
+    for name in ("norm", "quantize", "dequantize", "matmul"):
+        for args in ((), (1,), (None,) * 20):
+            with pytest.raises(TypeError):
+                getattr(_calls, name)(*args)
+    x = torch.zeros((2, 64))
+    for stream, error in ((1 << 80, OverflowError), ("0", TypeError), (None, TypeError)):
+        for call in (lambda: _calls.norm(x, None, None, 1e-6, -1, None, 0, stream),
+                     lambda: _calls.quantize(x, 0, stream), lambda: _calls.dequantize(x, x, None, 0, 0, stream),
+                     lambda: _calls.matmul(x, x, x, None, None, -1, 0, stream)):
+            with pytest.raises(error):
+                call()
+    for cols in (1 << 64, -1 << 70):  # left to the function, which says what the blocks hold
+        assert _calls.dequantize(x, x, cols, 0, 0, 0) is None
