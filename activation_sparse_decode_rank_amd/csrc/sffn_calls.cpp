@@ -104,6 +104,17 @@ bool count(Py_ssize_t n, Py_ssize_t want) {
   return n == want;
 }
 
+// f's status, without the interpreter's lock: allocating may wait for the device, and so may a launch
+// behind many others. (The caller holds the tensors meanwhile.)
+template <typename F>
+int unlocked(F f) {
+  struct Free {
+    PyThreadState* held = PyEval_SaveThread();
+    ~Free() { PyEval_RestoreThread(held); }  // before an exception reaches the handlers, too
+  } free;
+  return f();
+}
+
 PyObject* answer(int status, std::initializer_list<at::Tensor> out) {
   if (status != SFFN_OK) return PyLong_FromLong(status);
   if (out.size() == 1) return THPVariable_Wrap(*out.begin());
@@ -123,9 +134,9 @@ PyObject* answer(int status, std::initializer_list<at::Tensor> out) {
 
 // codes and scales of [..., K], and the scales' row distance
 struct NewBlocks {
-  at::Tensor q, s;
-  int64_t ldq, lds;
-  NewBlocks(const at::Tensor& like, int64_t K) {
+  at::Tensor q, s, room;  // room: the scales with what lies behind their rows
+  int64_t ldq = 0, lds = 0;
+  void make(const at::Tensor& like, int64_t K) {
     const int64_t B = (K + 31) / 32;
     ldq = 16 * B;
     lds = (B + 15) / 16 * 16;
@@ -138,7 +149,6 @@ struct NewBlocks {
     room = s;
     if (lds != B) s = room.narrow(-1, 0, B);
   }
-  at::Tensor room;
 };
 
 // norm(x, weight, residual, eps, out, residual_out, device, stream)
@@ -178,34 +188,38 @@ PyObject* norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (!q.ok) Py_RETURN_NONE;
     ldsum = q.ld;
   }
-  at::Tensor sum;
-  if (into) sum = *into;
-  else if (res) sum = at::empty(x->sizes(), x->options());
-  void* sp = res ? sum.data_ptr() : nullptr;
-  const void* rp = res ? res->data_ptr() : nullptr;
-  const int R = (int)r.R, K = (int)r.K;
-  if (out == SFFN_MX4) {
-    NewBlocks b(*x, r.K);
-    const int st = c_norm(x->data_ptr(), xt, r.ld, rp, ldr, R, K, w, wt, eps, sp, ldsum, b.q.data_ptr(), SFFN_MX4,
-                          b.ldq, b.room.data_ptr(), b.lds, stream);
-    return res ? answer(st, {b.q, b.s, sum}) : answer(st, {b.q, b.s});
-  }
-  if (out == SFFN_I8) {
-    c10::SmallVector<int64_t, 5> shape(x->sizes().begin(), x->sizes().end());
-    const int64_t ldy = (r.K + 15) / 16 * 16;
-    shape.back() = ldy;
-    at::Tensor y = at::empty(shape, x->options().dtype(at::kChar));
-    shape.pop_back();
-    at::Tensor s = at::empty(shape, x->options().dtype(at::kFloat));
-    const int st = c_norm(x->data_ptr(), xt, r.ld, rp, ldr, R, K, w, wt, eps, sp, ldsum, y.data_ptr(), SFFN_I8, ldy,
-                          s.data_ptr(), 0, stream);
-    if (ldy != r.K) y = y.narrow(-1, 0, r.K);
-    return res ? answer(st, {y, s, sum}) : answer(st, {y, s});
-  }
-  if (out > SFFN_BF16) Py_RETURN_NONE;
-  at::Tensor y = at::empty(x->sizes(), x->options().dtype(type_for((int)out)));
-  const int st = c_norm(x->data_ptr(), xt, r.ld, rp, ldr, R, K, w, wt, eps, sp, ldsum, y.data_ptr(), (int)out, r.K,
-                        nullptr, 0, stream);
+  if (out > SFFN_MX4) Py_RETURN_NONE;
+  at::Tensor sum, y, s;
+  NewBlocks b;
+  const int st = unlocked([&]() -> int {
+    if (into) sum = *into;
+    else if (res) sum = at::empty(x->sizes(), x->options());
+    void *yp, *sp = nullptr;
+    int64_t ldy = r.K;
+    if (out == SFFN_MX4) {
+      b.make(*x, r.K);
+      yp = b.q.data_ptr();
+      sp = b.room.data_ptr();
+      ldy = b.ldq;
+    } else if (out == SFFN_I8) {
+      c10::SmallVector<int64_t, 5> shape(x->sizes().begin(), x->sizes().end());
+      ldy = (r.K + 15) / 16 * 16;
+      shape.back() = ldy;
+      y = at::empty(shape, x->options().dtype(at::kChar));
+      shape.pop_back();
+      s = at::empty(shape, x->options().dtype(at::kFloat));
+      yp = y.data_ptr();
+      sp = s.data_ptr();
+      if (ldy != r.K) y = y.narrow(-1, 0, r.K);
+    } else {
+      y = at::empty(x->sizes(), x->options().dtype(type_for((int)out)));
+      yp = y.data_ptr();
+    }
+    return c_norm(x->data_ptr(), xt, r.ld, res ? res->data_ptr() : nullptr, ldr, (int)r.R, (int)r.K, w, wt, eps,
+                  res ? sum.data_ptr() : nullptr, ldsum, yp, (int)out, ldy, sp, b.lds, stream);
+  });
+  if (out == SFFN_MX4) return res ? answer(st, {b.q, b.s, sum}) : answer(st, {b.q, b.s});
+  if (out == SFFN_I8) return res ? answer(st, {y, s, sum}) : answer(st, {y, s});
   return res ? answer(st, {y, sum}) : answer(st, {y});
   END_HANDLE_TH_ERRORS
 }
@@ -221,9 +235,12 @@ PyObject* quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int xt = type_of(*x);
   const Rows r(*x);
   if (xt < 0 || !r.ok) Py_RETURN_NONE;
-  NewBlocks b(*x, r.K);
-  const int st = c_quantize(x->data_ptr(), xt, r.ld, (int)r.R, (int)r.K, static_cast<uint8_t*>(b.q.data_ptr()), b.ldq,
-                            static_cast<uint8_t*>(b.room.data_ptr()), b.lds, stream);
+  NewBlocks b;
+  const int st = unlocked([&]() -> int {
+    b.make(*x, r.K);
+    return c_quantize(x->data_ptr(), xt, r.ld, (int)r.R, (int)r.K, static_cast<uint8_t*>(b.q.data_ptr()), b.ldq,
+                      static_cast<uint8_t*>(b.room.data_ptr()), b.lds, stream);
+  });
   return answer(st, {b.q, b.s});
   END_HANDLE_TH_ERRORS
 }
@@ -245,10 +262,13 @@ PyObject* dequantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (!b.ok) Py_RETURN_NONE;
   if (a[2] == Py_None) cols = 32 * b.B;
   if (cols <= 32 * (b.B - 1) || cols > 32 * b.B) Py_RETURN_NONE;
-  at::Tensor y = at::empty({b.R, cols}, q->options().dtype(type_for((int)out)));
-  const int st = c_dequantize(static_cast<const uint8_t*>(q->data_ptr()), b.ldq,
-                              static_cast<const uint8_t*>(s->data_ptr()), b.lds, (int)b.R, (int)cols, y.data_ptr(),
-                              (int)out, cols, stream);
+  at::Tensor y;
+  const int st = unlocked([&]() -> int {
+    y = at::empty({b.R, cols}, q->options().dtype(type_for((int)out)));
+    return c_dequantize(static_cast<const uint8_t*>(q->data_ptr()), b.ldq,
+                        static_cast<const uint8_t*>(s->data_ptr()), b.lds, (int)b.R, (int)cols, y.data_ptr(),
+                        (int)out, cols, stream);
+  });
   return answer(st, {y});
   END_HANDLE_TH_ERRORS
 }
@@ -297,13 +317,14 @@ PyObject* matmul(PyObject*, PyObject* const* a, Py_ssize_t n) {
   }
   const size_t need = c_work_bytes(xt, (int)M, (int)bw.R, (int)K);
   if (need > ((size_t)1 << 62)) Py_RETURN_NONE;
-  at::Tensor y = at::empty({M, bw.R}, x->options().dtype(type_for((int)out)));
-  at::Tensor work;
-  if (need) work = at::empty({(int64_t)need}, x->options().dtype(at::kByte));
-  const int st = c_matmul(x->data_ptr(), xt, xs, ldx, ldxs, (int)M, (int)K,
-                          static_cast<const uint8_t*>(w->data_ptr()), bw.ldq,
-                          static_cast<const uint8_t*>(ws->data_ptr()), bw.lds, bias, (int)bw.R, y.data_ptr(), (int)out,
-                          bw.R, need ? work.data_ptr() : nullptr, need, stream);
+  at::Tensor y, work;
+  const int st = unlocked([&]() -> int {
+    y = at::empty({M, bw.R}, x->options().dtype(type_for((int)out)));
+    if (need) work = at::empty({(int64_t)need}, x->options().dtype(at::kByte));
+    return c_matmul(x->data_ptr(), xt, xs, ldx, ldxs, (int)M, (int)K, static_cast<const uint8_t*>(w->data_ptr()),
+                    bw.ldq, static_cast<const uint8_t*>(ws->data_ptr()), bw.lds, bias, (int)bw.R, y.data_ptr(),
+                    (int)out, bw.R, need ? work.data_ptr() : nullptr, need, stream);
+  });
   return answer(st, {y});
   END_HANDLE_TH_ERRORS
 }
