@@ -58,7 +58,8 @@ def _short_way():
 
 
 _calls = _short_way()
-_device = torch._C._cuda_getDevice
+# the current device's number, without the checks around it where torch offers that
+_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 _OUT = {None: -1, **_TYPES, "i8": N.SFFN_I8, "mx4": N.SFFN_MX4}
 
 

@@ -112,3 +112,12 @@ def test_the_module_refuses_what_is_no_argument():
                 call()
     for cols in (1 << 64, -1 << 70):  # left to the function, which says what the blocks hold
         assert _calls.dequantize(x, x, cols, 0, 0, 0) is None
+
+
+def test_the_package_works_with_a_torch_without_devices(tmp_path):
+    """A torch that was built without device support has no _cuda_getDevice: importing the package does
+    not look for it, and the calls say that they need device tensors."""
+    package(tmp_path)
+    code = "import torch\nfor name in ('_cuda_getDevice', '_cuda_getCurrentRawStream'):\n    delattr(torch._C, name)\n"
+    r = run(tmp_path, code + USE.format(at=str(tmp_path)))
+    assert r.returncode == 0, r.stderr
