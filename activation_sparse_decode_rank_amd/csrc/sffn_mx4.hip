@@ -78,6 +78,21 @@ __device__ __forceinline__ void emit4(const Mx4ProductArgs& a, int64_t r, int c,
   else store4<__bf16>(a.out, o, v, a.n - c);
 }
 
+// v, taken where all lanes run: matrix instructions have no effect that would keep the compiler from moving
+// them behind a branch that some lanes do not take, where those lanes' operands are missing. It leaves
+// exchanges between lanes where they stand, and what they read: this one gives each lane its own value (and
+// the wait for the matrix instruction's result is the compiler's, as before any instruction).
+constexpr int DPP_SAME_LANE = 0xE4;  // quad_perm 0 1 2 3
+__device__ __forceinline__ float4_t in_all_lanes(float4_t v) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float own = v[e];  // a bit cast of v[e] itself would take v[0] for every e
+    v[e] = __builtin_bit_cast(
+        float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, own), DPP_SAME_LANE, 0xF, 0xF, true));
+  }
+  return v;
+}
+
 // Few rows, or short ones: the weights are streamed from memory, straight into the matrix cores'
 // registers, and x is read from LDS. A tile is 16 rows of w and up to 16 rows of x; a wave takes one
 // block of 256 bytes of its length (16 blocks of numbers, whose scales are 16 bytes) after the other.
@@ -244,11 +259,8 @@ __global__ __launch_bounds__(512, 4) void k_mx4_few(Mx4ProductArgs a, int per) {
       }
       par ^= 1;
     } else {
-      // All lanes' products and their operands come before the lanes that write take a way of their own:
-      // the compiler would move them there, where the others' operands are missing. (The waits are the
-      // matrix instruction's, which reading its result takes.)
       const float4_t bias = bias16(a, t * 16, g);
-      asm volatile("s_nop 15\n\ts_nop 15" : "+v"(acc));
+      acc = in_all_lanes(acc);
       if (r16 < rows) emit4(a, r0 + r16, t * 16 + 4 * g, acc, bias);
     }
     acc = float4_t{0.f, 0.f, 0.f, 0.f};
