@@ -323,12 +323,13 @@ __global__ __launch_bounds__(512, 4) void k_mx4_few(Mx4ProductArgs a, int per) {
 // (blocks h, 2 + h, .., 14 + h) become two words by two permutations, and the matrix instruction
 // takes the byte of its step.
 // A wave's rows of w are dealt so that a lane's 16 sums are neighbouring channels.
-// Rows held in 4-bit blocks already, out in bf16: 4096 x 4096 x 11008 113 us (3.3 PFLOP/s), 4096 x 16384
-// x 8192 292 us (3.8). The products alone, without loads and LDS reads, run at 6.3 PFLOP/s, less than the
-// clock would give, and the loads and LDS reads alone in 0.7 of the whole time; together neither hides the
-// other: the same kernel takes 15 to 24% less on zeros, so power is what they share. Rings of three and
-// four stages (of half lines or smaller tiles), four waves of 128 x 128, waves' priorities and other
-// orders of the reads, loads and products take as long or longer.
+// Rows held in 4-bit blocks already, out in bf16: 4096 x 4096 x 11008 119 us (3.1 PFLOP/s, the last of 2.7
+// rounds of tiles 69% full), 4096 x 16384 x 8192 261 us (4.2). The matrix cores are busy 34 to 38% of the
+// time. The products alone, without loads and LDS reads, keep them busy 64% (6.3 PFLOP/s), and the loads
+// and LDS reads alone take 0.7 of the whole time: neither hides the other, and every stage waits for all
+// its loads and for all waves. Power is a part of it: on zeros the same kernel takes 6 to 19% less. Rings
+// of three and four stages (of half lines or smaller tiles), four waves of 128 x 128, waves' priorities
+// and other orders of the reads, loads and products take as long or longer.
 template <int CH, int TK, int WC, int WT>
 __global__ __launch_bounds__(WC * WT * 64) void k_mx4_tiles(Mx4ProductArgs a) {
   constexpr int W = WC * WT, NS = 2;

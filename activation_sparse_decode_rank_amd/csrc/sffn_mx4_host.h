@@ -14,8 +14,11 @@ inline int mx4_padded(int K) { return (int)up_to((size_t)mx4_blocks(K), kMx4Grou
 
 // Whether the workgroups of a product hold the M rows of x in their LDS, codes and scales: every one
 // of them does it for all rows, so few of them, and within the LDS that leaves two workgroups a
-// compute unit. Float rows are held in 4-bit blocks on the way. 4 rows x 4096 x 4096 take 4.6 us so,
-// 5.8 split over a tile's waves; 8 rows 6.5 and 5.8 (1 x 12288 x 49152: 49 and 63 us).
+// compute unit. Float rows are held in 4-bit blocks on the way. 4 rows x 4096 x 4096 take 5.5 us so,
+// 6.0 with a launch for x's rows and split over a tile's waves; 8 rows 6.7 and 6.1; 4 rows x 11008 x
+// 4096 10.2 both ways, 5 rows 11.7 and 10.3 (1 x 12288 x 49152: 51 and 69). Rows that are held already
+// take it too, so that both give the same bits: 4 x 4096 x 4096 5.1 us, 3.5 split over a tile's waves,
+// 4 x 11008 x 4096 7.6 and 7.7, 4 x 12288 x 49152 48 and 64.
 constexpr int kMx4FewRows = 4;
 constexpr size_t kMx4FewLds = 48 * 1024;
 inline size_t mx4_few_lds(size_t M, int K) { return M * (size_t)mx4_padded(K) * 17; }
@@ -25,11 +28,11 @@ inline bool mx4_few(size_t M, int K) {
 
 // Whether workgroups hold 16 rows of x each in their LDS, and a wave has a tile to itself: for more
 // rows, of at most 512 values (one group), and few tiles. Float rows: 42 x 345 x 3475 (M x K x N) takes
-// 3.8 us so, 6.2 with a launch for x's rows in front, and that launch costs the host 3 to 4 us; 445 x
-// 469 x 552 4.0 and 6.6; 1224 x 375 x 949 (4620 tiles) 7.1 and 8.2, 1007 x 502 x 1332 (5292) 8.2 and
-// 7.7; of two groups, 77 x 950 x 610, 5.9 and 5.3. Rows that are held already take it at the same
-// sizes, so that both give the same bits: 33 x 162 x 3983 3.1 us, 3.9 split over a tile's waves, 13 x
-// 451 x 180 2.9 and 2.8.
+// 4.0 us so, 5.5 with a launch for x's rows in front, and that launch costs the host 3 to 4 us; 445 x
+// 469 x 552 4.0 and 5.7; 1024 x 512 x 1024 (4096 tiles) 5.6 and 6.7, 1224 x 375 x 949 (4620) 7.2 and
+// 7.8, 1007 x 502 x 1332 (5292) 8.4 and 7.5; of two groups, 77 x 950 x 610, 5.9 and 5.3. Rows that are
+// held already take it at the same sizes, so that both give the same bits: 33 x 162 x 3983 3.0 us, 3.2
+// split over a tile's waves, 13 x 451 x 180 2.7 both ways, 1024 x 512 x 1024 4.8 and 4.4.
 constexpr size_t kMx4ShortTiles = 4096;
 inline bool mx4_short(size_t M, size_t N, int nb) {
   return nb <= kMx4Group && ((M + 15) / 16) * ((N + 15) / 16) <= kMx4ShortTiles;
@@ -41,7 +44,9 @@ inline bool mx4_own(size_t M, size_t N, int K) {
 
 // The kernel that M rows and N channels of nb blocks take: the one with the least time by a fit of
 // measured ones, in microseconds: a + (b + (f - b) l) k for tiles that fill a share l of the device's
-// room for them at once, k thousands of values long, and a + f k for each full room before them.
+// room for them at once (what 256 compute units hold), k thousands of values long, and a + f k for each
+// full room before them. Over 330 random sizes of 5 to 4000 rows its choice takes 1.9% more than the
+// fastest of them in the mean, 33% at most (profiles/mx4_plan.txt).
 enum Mx4Form {
   kMx4Few, kMx4Short, kMx4Split16, kMx4Split16x32, kMx4Split32, kMx4Split64, kMx4Tile64, kMx4Tile64x128, kMx4Tile128,
   kMx4Tile256
