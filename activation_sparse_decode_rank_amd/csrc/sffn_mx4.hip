@@ -324,7 +324,7 @@ __global__ __launch_bounds__(512, 4) void k_mx4_few(Mx4ProductArgs a, int per) {
 // takes the byte of its step.
 // A wave's rows of w are dealt so that a lane's 16 sums are neighbouring channels.
 // Rows held in 4-bit blocks already, out in bf16: 4096 x 4096 x 11008 119 us (3.1 PFLOP/s, the last of 2.7
-// rounds of tiles 69% full), 4096 x 16384 x 8192 261 us (4.2). The matrix cores are busy 34 to 38% of the
+// rounds of tiles 69% full), 4096 x 16384 x 8192 261 us (4.2). The matrix cores are busy 33 to 37% of the
 // time. The products alone, without loads and LDS reads, keep them busy 64% (6.3 PFLOP/s), and the loads
 // and LDS reads alone take 0.7 of the whole time: neither hides the other, and every stage waits for all
 // its loads and for all waves. Power is a part of it: on zeros the same kernel takes 6 to 19% less. Rings

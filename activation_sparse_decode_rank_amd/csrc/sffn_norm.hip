@@ -76,10 +76,9 @@ __global__ __launch_bounds__(TPB) void k_dequantize_mx4(Mx4DequantArgs a, int L)
 
 // lanes a row, and the grid: rows down x, pieces of long rows down y, 2^20 workgroups (2^28 threads)
 // at most: the kernels go on from there. A workgroup takes several sets of rows from LEAST workgroups of
-// one set on, so that every compute unit still has some. bf16 from blocks: 2000 x 2000 4.1 us so and 4.5
-// with one set, 2866 x 1703 5.3 and 5.6, 4096 x 4096 8.7 and 10.8, but 777 x 1999 3.6 and 3.2. Into blocks
-// it decides little: 4096 x 4096 10.0 and 10.3, 2048 x 12288 13.7 both ways, 2866 x 1703 6.0 and 5.6, 777 x
-// 1999 4.1 and 3.2.
+// one set on, so that every compute unit still has some. bf16 from blocks: 2866 x 1703 5.3 us so and
+// 5.6 with one set, 4096 x 4096 8.7 and 10.8, but 1500 x 1703 4.2 and 3.9. Into blocks it decides little:
+// 4096 x 4096 10.0 and 10.3, 2048 x 12288 13.7 both ways, 2866 x 1703 6.0 and 5.6, 1500 x 1703 4.5 and 3.9.
 constexpr int64_t LEAST = 2048;
 struct RowGrid {
   int L;
